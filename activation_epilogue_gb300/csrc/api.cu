@@ -694,6 +694,7 @@ gemm_epi_status launch_gemm(gemm_epi_plan_s* p, const gemm_epi_operands& ops, in
     prm.ln_bias = ops.ln_bias;
     prm.scale_a = ops.scale_a;
     prm.scale_b = ops.scale_b;
+    prm.scale_a_rows = p->scale_a_rows;
     prm.status = p->d_status;
     prm.wait_limit_ns = p->wait_limit_ns;
     prm.m = static_cast<int>(p->m);
@@ -969,6 +970,10 @@ gemm_epi_status gemm_epi_plan_set_option(gemm_epi_plan_t p, gemm_epi_option opt,
     case GEMM_EPI_OPT_B_READY:
         if (value != 0 && value != 1) return GEMM_EPI_ERR_INVALID_ARG;
         p->b_ready = static_cast<int>(value);
+        return GEMM_EPI_OK;
+    case GEMM_EPI_OPT_SCALE_A_ROWS:
+        if (value != 0 && (value != 1 || p->dtype != GEMM_EPI_E4M3)) return GEMM_EPI_ERR_INVALID_ARG;
+        p->scale_a_rows = static_cast<int>(value);
         return GEMM_EPI_OK;
     case GEMM_EPI_OPT_DEBUG_STALL:
         if (value != 0 && value != 1) return GEMM_EPI_ERR_INVALID_ARG;

@@ -1274,8 +1274,9 @@ __device__ __forceinline__ void run_epilogue(const GemmParams& p, uint8_t* smem,
     }
     // Bias, residual and the outputs may belong to a programmatic predecessor grid.
     grid_dependency_wait();
-    // E4M3 inputs: the per-tensor dequantisation scales
-    const float fp8_scale = F8 ? __ldg(p.scale_a) * __ldg(p.scale_b) : 1.0f;
+    // E4M3 inputs: the dequantisation scale, one for the tensor or (scale_a_rows) one per row
+    // of A, which is one per lane of the accumulator and is read with each tile's row below
+    const float fp8_tensor_scale = F8 && !p.scale_a_rows ? __ldg(p.scale_a) * __ldg(p.scale_b) : 1.0f;
 
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -1319,6 +1320,9 @@ __device__ __forceinline__ void run_epilogue(const GemmParams& p, uint8_t* smem,
                               : m64 ? tm * 64 + quarter * 16
                                     : tm * kBM + quarter * 32;
         const int lane_idx = m64 && lane >= 16 ? lane_limit : lane_base + lane;
+        float fp8_scale = fp8_tensor_scale;
+        if (F8 && p.scale_a_rows)
+            fp8_scale = lane_idx < lane_limit ? __ldg(p.scale_a + lane_idx) * __ldg(p.scale_b) : 0.0f;
         if (*abort_flag) break;
         if (EW == 8 && col_bias) {
             __syncwarp();  // every lane is done reading the previous tile's values

@@ -66,9 +66,11 @@ struct GemmParams {
     const float* ln_bias;    // LN_GELU_BIAS: b'_j = beta . W + b (fp32)
     // FP8 (E4M3) inputs (CTA-pair kernel instantiated for them): tm_B maps B transposed
     // (n x k, K-major boxes {128 k, 128 n}); K blocks are 128 deep; the accumulator is
-    // multiplied by *scale_a * *scale_b before the bias.
+    // multiplied by *scale_a * *scale_b before the bias, or by scale_a[row] * *scale_b where
+    // scale_a_rows is set.
     const float* scale_a;
     const float* scale_b;
+    int scale_a_rows;
     int* status;
     unsigned long long wait_limit_ns;
     int m, n, k;
@@ -264,5 +266,69 @@ cudaError_t layernorm_launch(const void* X, const void* residual, const void* ga
 cudaError_t layernorm_fold_launch(const void* gamma, const void* beta, const void* W,
                                   const void* b, void* Wf, float* colsum, float* bias_f, int d,
                                   int f, int bf16, int sm_count, cudaStream_t stream);
+
+// RMS norm (csrc/rmsnorm.cu); d a multiple of 8.  residual and H are both given or both null
+// (then the norm is of X); Y holds 16-bit values (kRms16) or E4M3 codes.
+enum RmsnormMode : int { kRms16 = -1, kRmsRow = 0, kRmsTensor = 1, kRmsGiven = 2 };
+struct RmsnormArgs {
+    const void* X;
+    const void* residual;
+    const void* gamma;
+    void* H;
+    void* Y;
+    float* scale;      // kRmsRow: t, kRmsTensor: 1 (written); kRmsGiven: 1 (read)
+    float* rstd;       // t, or null
+    uint32_t* ws_max;  // kRmsTensor workspace: kRmsMaxParts maxima ...
+    float* ws_rstd;    // ... and t values of rstd
+    float eps;
+    int mode;
+    int t, d;
+};
+struct RmsnormBackwardArgs {
+    const void* dY;
+    const void* H;
+    const void* gamma;
+    const float* rstd;
+    const void* dH;
+    void* dX;
+    float* dgamma;
+    float* ws_dgamma;  // rmsnorm_backward_parts(t) rows of d partial sums
+    int t, d;
+};
+constexpr int kRmsMaxParts = 1024;
+constexpr int kRmsBackwardParts = 304;
+int rmsnorm_backward_parts(long long t);
+cudaError_t rmsnorm_launch(const RmsnormArgs& a, bool bf16, cudaStream_t stream);
+cudaError_t rmsnorm_backward_launch(const RmsnormBackwardArgs& a, bool bf16, cudaStream_t stream);
+
+// Products with 4-bit weights (csrc/w4.cu): W n rows of k / 2 bytes, scales and zeros k / group
+// rows of n.  w4_dequantize_launch writes B (k x n) to D.
+struct W4Args {
+    const void* A;
+    const void* W;
+    const void* scales;
+    const uint8_t* zeros;  // null: 8
+    const void* bias;
+    const void* residual;
+    void* D;
+    int m, n, k, group, epilog;
+};
+constexpr int kW4MaxM = 64;
+cudaError_t w4_matmul_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
+cudaError_t w4_dequantize_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
+
+// Dropout (csrc/dropout.cu): an element is kept when its 16 random bits are >= drop.
+struct DropoutArgs {
+    const void* X;
+    const void* residual;
+    void* Y;
+    const unsigned long long* offset_device;
+    unsigned long long offset;
+    long long count;
+    uint32_t key0, key1;
+    uint32_t drop;
+    float scale;
+};
+cudaError_t dropout_launch(const DropoutArgs& a, bool bf16, int sm_count, cudaStream_t stream);
 
 }  // namespace gemm_epi

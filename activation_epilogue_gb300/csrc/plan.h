@@ -52,6 +52,7 @@ struct gemm_epi_plan_s {
     int prefetch;  // L2 prefetch distance in K blocks (GEMM_EPI_OPT_PREFETCH)
     int no_pdl;    // 1: launch without programmatic dependent launch (GEMM_EPI_OPT_PDL = 0)
     int b_ready;   // 1: no earlier work on the stream writes B (GEMM_EPI_OPT_B_READY)
+    int scale_a_rows;  // E4M3: scale_a holds one scale per row of A (GEMM_EPI_OPT_SCALE_A_ROWS)
     unsigned long long wait_limit_ns;
     int debug_stall;
     int* d_status;

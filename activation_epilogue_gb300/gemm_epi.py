@@ -23,7 +23,7 @@ BACKWARD = ("DRELU_BGRAD", "DGELU_BGRAD")
 BIAS_LAYOUT = {"M1": 0, "1N": 1}
 OPTION = {"VARIANT": 0, "TILE_N": 1, "SPLIT_K": 2, "GRID": 3, "GROUP_M": 4,
           "WAIT_LIMIT_US": 5, "DEBUG_STALL": 6, "PREFETCH": 7, "PDL": 8, "SPLIT_MODE": 9,
-          "TILE_M": 10, "TILE_ORDER": 11, "B_READY": 12}
+          "TILE_M": 10, "TILE_ORDER": 11, "B_READY": 12, "SCALE_A_ROWS": 13}
 STATUS = {0: "OK", 1: "ERR_INVALID_ARG", 2: "ERR_UNSUPPORTED_SHAPE", 3: "ERR_MISALIGNED",
           4: "ERR_NO_DEVICE", 5: "ERR_ARCH", 6: "ERR_ALLOC", 7: "ERR_LAUNCH",
           8: "ERR_DEVICE_TIMEOUT", 9: "ERR_SCRATCH_LIMIT"}
@@ -38,8 +38,15 @@ EXPORTS = ["gemm_epi_plan", "gemm_epi_plan_set_option", "gemm_epi_execute",
            "gemm_epi_execute_operands_unfused", "gemm_epi_ffn_set_option",
            "gemm_epi_ffn_plan_describe", "gemm_epi_layernorm", "gemm_epi_layernorm_stats",
            "gemm_epi_layernorm_fold", "gemm_epi_ffn_plan_layernorm",
-           "gemm_epi_ffn_execute_layernorm", "gemm_epi_execute_host"]
+           "gemm_epi_ffn_execute_layernorm", "gemm_epi_execute_host", "gemm_epi_rmsnorm",
+           "gemm_epi_rmsnorm_e4m3", "gemm_epi_rmsnorm_backward", "gemm_epi_rmsnorm_workspace",
+           "gemm_epi_w4_matmul", "gemm_epi_w4_dequantize", "gemm_epi_dropout"]
 FFN_OPTION = {"LAUNCHES": 0, "SPLIT2": 1, "TILE_ORDER": 2, "B_READY": 3}
+
+SCALE_MODE = {"ROW": 0, "TENSOR": 1, "GIVEN": 2}
+
+# Most rows of A in one gemm_epi_w4_matmul call.
+W4_MAX_ROWS = 64
 
 # Largest t * f the allocation-free FFN call accepts (its static scratch holds H).
 FFN_NOALLOC_MAX_HIDDEN = 16 * 1024 * 1024
@@ -128,6 +135,24 @@ def load_library(path: str | None = None):
         lib.gemm_epi_execute_operands.argtypes = [vp, ctypes.POINTER(Operands), vp]
         lib.gemm_epi_execute_operands_unfused.restype = i32
         lib.gemm_epi_execute_operands_unfused.argtypes = [vp, ctypes.POINTER(Operands), vp, vp]
+        u64 = ctypes.c_uint64
+        lib.gemm_epi_rmsnorm.restype = i32
+        lib.gemm_epi_rmsnorm.argtypes = [i64, i64, i32, vp, vp, vp, f32, vp, vp, vp, vp]
+        lib.gemm_epi_rmsnorm_e4m3.restype = i32
+        lib.gemm_epi_rmsnorm_e4m3.argtypes = [i64, i64, i32, vp, vp, vp, f32, vp, vp, i32, vp, vp,
+                                              vp, vp]
+        lib.gemm_epi_rmsnorm_backward.restype = i32
+        lib.gemm_epi_rmsnorm_backward.argtypes = [i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                  vp]
+        lib.gemm_epi_rmsnorm_workspace.restype = i64
+        lib.gemm_epi_rmsnorm_workspace.argtypes = [i64, i64]
+        lib.gemm_epi_w4_matmul.restype = i32
+        lib.gemm_epi_w4_matmul.argtypes = [i64, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp,
+                                           vp, vp]
+        lib.gemm_epi_w4_dequantize.restype = i32
+        lib.gemm_epi_w4_dequantize.argtypes = [i64, i64, i64, i32, vp, vp, vp, vp, vp]
+        lib.gemm_epi_dropout.restype = i32
+        lib.gemm_epi_dropout.argtypes = [i64, i32, vp, vp, f32, u64, u64, vp, vp, vp]
         if path is None:
             _lib = lib
         return lib
@@ -148,6 +173,17 @@ def _ptr(t):
         return None
     if isinstance(t, int):
         return t
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous (row-major)")
+    return t.data_ptr()
+
+
+def _dev(t):
+    """As _ptr, for calls that run without a plan: a tensor of another device is refused."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous (row-major)")
     return t.data_ptr()
@@ -263,6 +299,60 @@ def gemm_epi_ffn_execute_layernorm(plan, X, eps: float, W1_folded, colsum, b1_fo
                                                          _ptr(b1_folded), _ptr(W2), _ptr(b2),
                                                          _ptr(R), _ptr(Y), _stream(stream)),
            "gemm_epi_ffn_execute_layernorm")
+
+
+def gemm_epi_rmsnorm(t: int, d: int, dtype: str, X, residual, gamma, eps: float, H, Y, rstd=None,
+                     stream=None):
+    _check(load_library().gemm_epi_rmsnorm(t, d, DTYPE[dtype], _dev(X), _dev(residual),
+                                           _dev(gamma), eps, _dev(H), _dev(Y), _dev(rstd),
+                                           _stream(stream)), "gemm_epi_rmsnorm")
+
+
+def gemm_epi_rmsnorm_e4m3(t: int, d: int, dtype: str, X, residual, gamma, eps: float, H, Q,
+                          mode: str, scale, rstd=None, workspace=None, stream=None):
+    """mode: "ROW" (t scales written), "TENSOR" (one, needs workspace) or "GIVEN" (one, read)."""
+    _check(load_library().gemm_epi_rmsnorm_e4m3(t, d, DTYPE[dtype], _dev(X), _dev(residual),
+                                                _dev(gamma), eps, _dev(H), _dev(Q),
+                                                SCALE_MODE[mode], _dev(scale), _dev(rstd),
+                                                _dev(workspace), _stream(stream)),
+           "gemm_epi_rmsnorm_e4m3")
+
+
+def gemm_epi_rmsnorm_backward(t: int, d: int, dtype: str, dY, H, gamma, rstd, dH, dX, dgamma,
+                              workspace, stream=None):
+    _check(load_library().gemm_epi_rmsnorm_backward(t, d, DTYPE[dtype], _dev(dY), _dev(H),
+                                                    _dev(gamma), _dev(rstd), _dev(dH), _dev(dX),
+                                                    _dev(dgamma), _dev(workspace),
+                                                    _stream(stream)),
+           "gemm_epi_rmsnorm_backward")
+
+
+def gemm_epi_rmsnorm_workspace(t: int, d: int) -> int:
+    """Bytes of workspace for the RMS norm calls of a t x d problem (0: a refused shape)."""
+    return int(load_library().gemm_epi_rmsnorm_workspace(t, d))
+
+
+def gemm_epi_w4_matmul(m: int, n: int, k: int, group: int, dtype: str, epilog: str, A, W, scales,
+                       zeros, bias, residual, D, stream=None):
+    _check(load_library().gemm_epi_w4_matmul(m, n, k, group, DTYPE[dtype], EPILOG[epilog],
+                                             _dev(A), _dev(W), _dev(scales), _dev(zeros),
+                                             _dev(bias), _dev(residual), _dev(D),
+                                             _stream(stream)), "gemm_epi_w4_matmul")
+
+
+def gemm_epi_w4_dequantize(n: int, k: int, group: int, dtype: str, W, scales, zeros, B,
+                           stream=None):
+    _check(load_library().gemm_epi_w4_dequantize(n, k, group, DTYPE[dtype], _dev(W),
+                                                 _dev(scales), _dev(zeros), _dev(B),
+                                                 _stream(stream)), "gemm_epi_w4_dequantize")
+
+
+def gemm_epi_dropout(count: int, dtype: str, X, residual, p: float, seed: int, offset: int, Y,
+                     offset_device=None, stream=None):
+    """seed and offset are taken mod 2^64; offset_device: an int64 CUDA tensor of one value."""
+    _check(load_library().gemm_epi_dropout(count, DTYPE[dtype], _dev(X), _dev(residual), p, seed,
+                                           offset, _dev(offset_device), _dev(Y),
+                                           _stream(stream)), "gemm_epi_dropout")
 
 
 def gemm_epi_free(plan):

@@ -78,7 +78,8 @@ typedef enum {
     GEMM_EPI_F16 = 0,  /* IEEE binary16 inputs and output */
     GEMM_EPI_BF16 = 1, /* bfloat16 inputs and output */
     GEMM_EPI_E4M3 = 2  /* 8-bit floating-point inputs (E4M3: 4 exponent bits, 3 fraction bits,
-                          bias 7, no infinities, max 448) with per-tensor fp32 scales; bias,
+                          bias 7, no infinities, max 448) with per-tensor fp32 scales (or, with
+                          GEMM_EPI_OPT_SCALE_A_ROWS, one for each row of A); bias,
                           residual and D in bfloat16.  A is m x k row-major; B is given
                           TRANSPOSED, n x k row-major (both operands contiguous along k), and
                           k must be a multiple of 16.  D = epi(scale_a * scale_b * (A.B) +
@@ -191,7 +192,7 @@ typedef enum {
                                        below that); the other kernels ignore it.  With 2 the
                                        plan's launches must not overlap on the GPU (they
                                        share the counter) */
-    GEMM_EPI_OPT_B_READY = 12       /* 1: no earlier work on the stream writes B (a weight
+    GEMM_EPI_OPT_B_READY = 12,      /* 1: no earlier work on the stream writes B (a weight
                                        that stays in place between calls), so under the
                                        programmatic dependent launch (PDL = 1) the small-m,
                                        swapped and single-CTA row-tile kernels copy B's
@@ -203,6 +204,11 @@ typedef enum {
                                        read waits; the small-m kernel then only brings its
                                        slab of B into L2 ahead of the wait, which needs no
                                        promise.  The host-buffer call ignores it */
+    GEMM_EPI_OPT_SCALE_A_ROWS = 13  /* E4M3 plans: 1 = scale_a holds m fp32 scales, one for each
+                                       row of A (gemm_epi_rmsnorm_e4m3 with
+                                       GEMM_EPI_SCALE_ROW), D = epi(scale_a[i] * scale_b *
+                                       (A.B) + bias); 0 (default) = one scale.  Other plans:
+                                       ERR_INVALID_ARG for 1 */
 } gemm_epi_option;
 
 /*
@@ -339,6 +345,106 @@ gemm_epi_status gemm_epi_layernorm_fold(int64_t d, int64_t f, gemm_epi_dtype dty
                                         const void* gamma, const void* beta, const void* W,
                                         const void* b, void* W_folded, float* colsum,
                                         float* bias_folded, cudaStream_t stream);
+
+/* ---- RMS norm ----------------------------------------------------------------------------
+ * The norm of "Root Mean Square Layer Normalization" (Zhang and Sennrich, 2019) with the
+ * residual's addition in front of it:
+ *     H = X + residual, rounded to the 16-bit type (without a residual the norm is of X),
+ *     rstd_i = 1 / sqrt(mean_j H_ij^2 + eps),      Y_ij = H_ij rstd_i gamma_j.
+ * The norm is of the rounded H, the values that the next sub-layer and the backward pass
+ * read; sums and rstd are fp32, Y is rounded once.  X, residual, H, Y: t x d; gamma: d
+ * elements; all of `dtype` (F16 or BF16), d a multiple of 8 and >= 8, 16-byte aligned.  H is
+ * given exactly when the residual is.  H and Y may each be X or the residual itself, but not
+ * the same buffer; no other overlap.  rstd: t fp32, 4-byte aligned, or NULL (the backward
+ * pass reads it).  eps >= 0.  A NaN or an infinity in a row of H makes that row of Y NaN (or,
+ * finite / infinite, 0) as the formula does.  t == 0 launches nothing.  Asynchronous on
+ * `stream`, launched as programmatic dependents of its previous work (which they wait for
+ * before they touch memory); the caller owns every buffer, the calls keep nothing, and calls
+ * on different streams are independent as long as their buffers are. */
+gemm_epi_status gemm_epi_rmsnorm(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* X,
+                                 const void* residual, const void* gamma, float eps, void* H,
+                                 void* Y, float* rstd, cudaStream_t stream);
+
+typedef enum {
+    GEMM_EPI_SCALE_ROW = 0,    /* scale[i] = max_j |Y_ij| / 448, t values written */
+    GEMM_EPI_SCALE_TENSOR = 1, /* scale[0] = max_ij |Y_ij| / 448, one value written */
+    GEMM_EPI_SCALE_GIVEN = 2   /* scale[0] is read: a calibrated scale, > 0 */
+} gemm_epi_scale_mode;
+
+/* The same norm with Y in E4M3 for an E4M3 plan: Q_ij = Y_ij / scale rounded once from fp32 to
+ * the nearest E4M3 value, ties to even, saturated at +-448 (Q: t x d bytes, 16-byte aligned,
+ * overlapping nothing else).  The scale is what the plan takes as scale_a: one value (TENSOR,
+ * GIVEN), or one per row (ROW, with GEMM_EPI_OPT_SCALE_A_ROWS); fp32, 4-byte aligned.  A row
+ * (tensor) whose largest |Y| is below 2^-100 gets scale 0 and zeros; a NaN gives the row (the
+ * tensor) a NaN scale and NaN codes; under GIVEN a NaN stays NaN and an infinity saturates.
+ * workspace: for TENSOR, gemm_epi_rmsnorm_workspace(t, d) bytes of device memory, 16-byte
+ * aligned, that no other call uses until this one has run; ignored otherwise. */
+gemm_epi_status gemm_epi_rmsnorm_e4m3(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* X,
+                                      const void* residual, const void* gamma, float eps,
+                                      void* H, void* Q, gemm_epi_scale_mode mode, float* scale,
+                                      float* rstd, void* workspace, cudaStream_t stream);
+
+/* Gradients of Y (and of H, which the residual stream also carries on): from dY, the norm's
+ * input H (X where there was no residual), gamma and the forward call's rstd,
+ *     g_ij = dY_ij gamma_j,   xh_ij = H_ij rstd_i,
+ *     dX_ij = rstd_i (g_ij - xh_ij mean_j(g_ij xh_ij)) + dH_ij,   dgamma_j = sum_i dY_ij xh_ij.
+ * dX is the gradient of X and of the residual alike.  dH, the gradient that reaches H past the
+ * norm, may be NULL (zero).  dY, H, dH, dX: t x d of `dtype`, dX may be dY or dH; dgamma: d
+ * fp32, summed in an order that depends on (t, d) alone (the same inputs give the same bits);
+ * t == 0 writes zeros to it.  workspace as above, always needed (t > 0). */
+gemm_epi_status gemm_epi_rmsnorm_backward(int64_t t, int64_t d, gemm_epi_dtype dtype,
+                                          const void* dY, const void* H, const void* gamma,
+                                          const float* rstd, const void* dH, void* dX,
+                                          float* dgamma, void* workspace, cudaStream_t stream);
+
+/* Bytes of workspace that the RMS norm calls of this shape need (0 for a shape they refuse). */
+int64_t gemm_epi_rmsnorm_workspace(int64_t t, int64_t d);
+
+/* ---- products with 4-bit weights --------------------------------------------------------
+ *     D[m,n] = epi(A[m,k] . B[k,n] + bias),   B[i][j] = (q[j][i] - z) * s,
+ * with the weight held in 4 bits: W is n rows of k/2 bytes (column j of B is row j of W,
+ * contiguous along k, two values per byte, the lower half first; q in 0..15), scales is
+ * k/group rows of n values of `dtype`, and zeros k/group rows of n bytes (0..15), or NULL for
+ * z = 8 everywhere; s and z are those of row i / group and column j.  group is 32, 64 or 128;
+ * k a multiple of group, n a multiple of 8.  For decoding: m is 1 to 64 rows of A (0 launches
+ * nothing); for more, gemm_epi_w4_dequantize and a plan.  A: m x k, bias: n elements (the
+ * (1,n) layout), residual and D: m x n, of `dtype` (F16 or BF16); epilogs BIAS, RELU_BIAS,
+ * GELU_BIAS, TANH_BIAS, BIAS_RESIDUAL and NONE as for plans; bias is NULL exactly for NONE,
+ * the residual given exactly for BIAS_RESIDUAL, and D may be the residual itself.  The
+ * differences q - z are exact in 16 bits and their products with A are summed in fp32, group
+ * by group, with the scales applied in fp32.  A, W, residual and D 16-byte aligned, the rest
+ * 2-byte (zeros: any).  No workspace, no plan; asynchronous on `stream` as above. */
+gemm_epi_status gemm_epi_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group,
+                                   gemm_epi_dtype dtype, gemm_epi_epilog epilog, const void* A,
+                                   const void* W, const void* scales, const uint8_t* zeros,
+                                   const void* bias, const void* residual, void* D,
+                                   cudaStream_t stream);
+
+/* The same weight as the row-major B (k x n of `dtype`, 16-byte aligned) of a plan:
+ * B[i][j] = (q - z) * s, the product formed in fp32 and rounded once. */
+gemm_epi_status gemm_epi_w4_dequantize(int64_t n, int64_t k, int64_t group,
+                                       gemm_epi_dtype dtype, const void* W, const void* scales,
+                                       const uint8_t* zeros, void* B, cudaStream_t stream);
+
+/* ---- dropout -----------------------------------------------------------------------------
+ * Y = residual + keep * X / (1 - p) (residual may be NULL: without it), over `count` elements
+ * in order, the mask never stored: its bits come from the generator Philox4x32-10 ("Parallel
+ * random numbers: as easy as 1, 2, 3", Salmon et al., 2011) with the key `seed` and the 128-bit
+ * counter (offset + *offset_device + e / 8, 0) for element e (64-bit sum, wrapping), of whose
+ * four words it takes half e % 2 (0 = the lower) of word (e % 8) / 2.  The element is kept when
+ * those 16 bits are >= P = round(65536 p); the scale is 65536 / (65536 - P), so the expectation
+ * is exact for the p that is used, a multiple of 2^-16.  p is 0 to 1 (1 drops all: Y = residual
+ * or 0).  A dropped element does not read into Y, NaN or infinite as it may be.
+ * The backward pass is the same call on dY with the same p, seed and offset and no residual
+ * (the residual's gradient is dY itself).  A call uses ceil(count / 8) counter values: the next
+ * one with the same seed starts that much further on.  offset_device: device uint64 that is
+ * added to offset when the kernel runs (NULL: 0), for captured graphs, whose replays would
+ * otherwise repeat the mask; 8-byte aligned.  X, residual, Y: `dtype` (F16 or BF16), 16-byte
+ * aligned; Y may be X or the residual; count == 0 launches nothing.  Sums in fp32, one rounding;
+ * asynchronous on `stream` as above. */
+gemm_epi_status gemm_epi_dropout(int64_t count, gemm_epi_dtype dtype, const void* X,
+                                 const void* residual, float p, uint64_t seed, uint64_t offset,
+                                 const uint64_t* offset_device, void* Y, cudaStream_t stream);
 
 /* Release the plan (the page's .free()).  NULL is accepted and ignored. */
 gemm_epi_status gemm_epi_free(gemm_epi_plan_t p);

@@ -1,0 +1,187 @@
+"""Products with 4-bit weights and group scales, and the weights written out, against 64 bits."""
+import pytest
+import torch
+
+import sublayer_reference as ref
+from activation_epilogue_gb300 import gemm_epi
+from sublayer_reference import TD
+
+pytestmark = pytest.mark.gpu
+
+EPILOGS = ["NONE", "BIAS", "RELU_BIAS", "GELU_BIAS", "TANH_BIAS", "BIAS_RESIDUAL"]
+# (m, n, k): one to 64 rows around every multiple of 8, n and k that end inside a tile
+SHAPES = [(1, 8, 32), (1, 264, 96), (2, 520, 1024), (3, 40, 2080), (7, 72, 4096), (8, 136, 160),
+          (9, 1000, 512), (15, 24, 8192), (16, 256, 256), (17, 48, 1056), (31, 88, 640),
+          (32, 64, 2048), (33, 200, 384), (48, 1024, 1152), (63, 16, 4160), (64, 328, 1024)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from activation_epilogue_gb300 import build
+    build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _run(p, group, dtype, epilog, stream=None, D=None):
+    m, k = p["A"].shape
+    n = p["W"].shape[0]
+    g = {key: None if v is None else v.cuda() for key, v in p.items() if key != "q"}
+    if D is None:
+        D = torch.full((m, n), float("nan"), dtype=TD[dtype], device="cuda")
+    gemm_epi.gemm_epi_w4_matmul(m, n, k, group, dtype, epilog, g["A"], g["W"], g["scales"], g["zeros"],
+                                None if epilog == "NONE" else g["bias"],
+                                g["R"] if epilog == "BIAS_RESIDUAL" else None, D, stream)
+    return D
+
+
+def _check(p, group, dtype, epilog, what=""):
+    D = _run(p, group, dtype, epilog)
+    want, error = ref.w4_matmul(p, group, epilog)
+    ref.check_16(D, want, dtype, error, f"D {what}")
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_w4_matmul(m, n, k, group, dtype):
+    k = -(-k // group) * group
+    epilog = EPILOGS[(m + n // 8 + group // 32) % len(EPILOGS)]
+    _check(ref.w4_problem(m, n, k, group, dtype, (m + group // 32) % 2 == 0, m + n + k), group, dtype, epilog)
+
+
+@pytest.mark.parametrize("epilog", EPILOGS)
+@pytest.mark.parametrize("m", [1, 5, 12, 40])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_w4_epilogs(epilog, m, zeros):
+    for dtype in ("bf16", "f16"):
+        _check(ref.w4_problem(m, 104, 768, 64, dtype, zeros, m), 64, dtype, epilog, epilog)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [1, 11])
+def test_w4_integers_are_exact(group, dtype, m):
+    # integer activations and unit scales: every sum is an integer that fp32 holds, and small
+    # enough for the output type (a wrong or missing term shows as a whole number)
+    g = torch.Generator().manual_seed(group + m)
+    n, k = 72, 896
+    q = torch.full((n, k), 8)
+    z = torch.full((k // group, n), 8, dtype=torch.uint8)
+    at = torch.randint(0, k, (n, 6), generator=g)
+    q.scatter_(1, at, torch.randint(0, 16, (n, 6), generator=g))
+    A = torch.randint(-2, 3, (m, k), generator=g).to(TD[dtype])
+    p = dict(q=q, W=ref.w4_pack(q), scales=torch.ones(k // group, n, dtype=TD[dtype]), zeros=z, A=A,
+             bias=None, R=None)
+    want = A.double() @ ref.w4_weight(q, p["scales"], z, group)
+    for zeros in (z, None):
+        D = _run({**p, "zeros": zeros}, group, dtype, "NONE")
+        assert torch.equal(D.double().cpu(), want)
+
+
+def test_w4_every_position_and_value():
+    # A picks out single rows of B: every nibble position, value, group and zero point
+    n, group = 16, 32
+    for dtype in ("bf16", "f16"):
+        for k in (32, 128, 288, 512):
+            q = (torch.arange(n * k).view(n, k) * 7 + torch.arange(n).view(n, 1)) % 16
+            z = (torch.arange(k // group * n).view(-1, n) % 16).to(torch.uint8)
+            scales = torch.pow(2.0, (torch.arange(k // group * n).view(-1, n) % 5 - 2).float()).to(TD[dtype])
+            B = ref.w4_weight(q, scales, z, group)
+            for k0 in range(0, k, 64):
+                rows = min(64, k - k0)
+                A = torch.zeros(rows, k, dtype=TD[dtype])
+                A[torch.arange(rows), k0 + torch.arange(rows)] = 1
+                p = dict(q=q, W=ref.w4_pack(q), scales=scales, zeros=z, A=A, bias=None, R=None)
+                assert torch.equal(_run(p, group, dtype, "NONE").double().cpu(), B[k0:k0 + rows])
+
+
+def test_w4_rows_do_not_mix():
+    # a NaN or an infinity in one row of A reaches that row of D only; behind the last row
+    # nothing is written
+    p = ref.w4_problem(5, 64, 512, 64, "bf16", False, 3)
+    clean = _run(p, 64, "bf16", "BIAS").cpu()
+    p["A"][2, 100] = float("nan")
+    p["A"][3, 7] = float("inf")
+    D = torch.full((8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    _run(p, 64, "bf16", "BIAS", D=D[:5])
+    D = D.cpu()
+    assert D[2].isnan().all() and not D[3].isfinite().any()
+    assert torch.equal(D[[0, 1, 4]], clean[[0, 1, 4]]) and (D[5:] == 7.0).all()
+
+
+def test_w4_in_place_residual_and_repeatable():
+    p = ref.w4_problem(3, 520, 2048, 128, "bf16", True, 5)
+    first = _run(p, 128, "bf16", "BIAS_RESIDUAL")
+    R = p["R"].cuda()
+    g = {key: None if v is None else v.cuda() for key, v in p.items() if key != "q"}
+    gemm_epi.gemm_epi_w4_matmul(3, 520, 2048, 128, "bf16", "BIAS_RESIDUAL", g["A"], g["W"], g["scales"],
+                                g["zeros"], g["bias"], R, R)
+    assert torch.equal(R, first) and torch.equal(_run(p, 128, "bf16", "BIAS_RESIDUAL"), first)
+
+
+def test_w4_k_zero_is_the_epilogue_alone():
+    bias = torch.randn(64, generator=torch.Generator().manual_seed(1)).to(torch.float16)
+    D = torch.full((3, 64), float("nan"), dtype=torch.float16, device="cuda")
+    gemm_epi.gemm_epi_w4_matmul(3, 64, 0, 64, "f16", "RELU_BIAS", None, None, None, None, bias.cuda(), None, D)
+    assert torch.equal(D.cpu(), bias.clamp(min=0).expand(3, -1))
+
+
+def test_w4_in_a_graph_and_on_a_stream():
+    p = ref.w4_problem(2, 264, 1024, 32, "f16", True, 6)
+    want = _run(p, 32, "f16", "GELU_BIAS").cpu()
+    g = {key: None if v is None else v.cuda() for key, v in p.items() if key != "q"}
+    D = torch.zeros(2, 264, dtype=torch.float16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+
+    def call(stream=None):
+        gemm_epi.gemm_epi_w4_matmul(2, 264, 1024, 32, "f16", "GELU_BIAS", g["A"], g["W"], g["scales"],
+                                    g["zeros"], g["bias"], None, D, stream)
+    with torch.cuda.graph(graph):
+        call()
+    g["A"].mul_(-1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(D.cpu(), _run({**p, "A": -p["A"]}, 32, "f16", "GELU_BIAS").cpu())
+    g["A"].mul_(-1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call(side)
+    side.synchronize()
+    assert torch.equal(D.cpu(), want)
+
+
+@pytest.mark.parametrize("n,k", [(8, 32), (40, 96), (64, 64), (72, 1056), (264, 384), (1000, 2048)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype,zeros", [("bf16", True), ("f16", False)])
+def test_w4_dequantize(n, k, group, dtype, zeros):
+    k = -(-k // group) * group
+    p = ref.w4_problem(1, n, k, group, dtype, zeros, n + k)
+    B = torch.full((k + 1, n), 7.0, dtype=TD[dtype], device="cuda")
+    gemm_epi.gemm_epi_w4_dequantize(n, k, group, dtype, p["W"].cuda(), p["scales"].cuda(),
+                                    p["zeros"].cuda() if zeros else None, B)
+    # (q - z) s is exact in fp32 (4 bits times 11 at most): one rounding, the same bits
+    want = ref.w4_weight(p["q"], p["scales"], p["zeros"], group).to(TD[dtype])
+    assert torch.equal(B[:k].cpu(), want) and (B[k:] == 7.0).all()
+
+
+@pytest.mark.slow
+def test_w4_offsets_past_32_bits():
+    n, k, group, m = 65544, 65536 + 128, 128, 2       # 4.3e9 weights, B of 8.6 GB
+    g = torch.Generator(device="cuda").manual_seed(4)
+    W = torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = (torch.rand(k // group, n, generator=g, device="cuda") / 256).to(torch.bfloat16)
+    A = torch.randn(m, k, generator=g, device="cuda").to(torch.bfloat16)
+    D = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    gemm_epi.gemm_epi_w4_matmul(m, n, k, group, "bf16", "NONE", A, W, scales, None, None, None, D)
+    cols = torch.tensor([0, 7, 32768, n - 9, n - 1])
+    w = W[cols.cuda()].cpu()
+    q = torch.stack((w & 15, w >> 4), 2).view(len(cols), k)
+    p = dict(q=q, scales=scales[:, cols.cuda()].cpu(), zeros=None, A=A.cpu())
+    want, error = ref.w4_matmul(p, group, "NONE")
+    ref.check_16(D[:, cols.cuda()], want, "bf16", error, "D")
+    B = torch.empty(k, n, dtype=torch.bfloat16, device="cuda")
+    gemm_epi.gemm_epi_w4_dequantize(n, k, group, "bf16", W, scales, None, B)
+    want = ref.w4_weight(q, p["scales"], None, group).to(torch.bfloat16)
+    assert torch.equal(B[:, cols.cuda()].cpu(), want)

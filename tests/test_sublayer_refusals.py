@@ -1,0 +1,141 @@
+"""The RMS norm, 4-bit-weight and dropout calls: what they refuse, and the empty problems they
+accept, before any device is touched (no GPU)."""
+import pytest
+import torch
+
+from activation_epilogue_gb300 import build as libbuild
+from activation_epilogue_gb300 import gemm_epi
+
+P = 1 << 20          # an aligned address that no call may read
+INVALID, SHAPE, MISALIGNED = 1, 2, 3
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    libbuild.build()
+    gemm_epi.load_library()
+
+
+def _status(call, **kw):
+    with pytest.raises(gemm_epi.GemmEpiError) as e:
+        call(**kw, stream=0)
+    return e.value.status
+
+
+NORM = dict(t=4, d=64, dtype="bf16", X=P, residual=P, gamma=P, eps=1e-6, H=P, Y=2 * P)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype="e4m3"), INVALID), (dict(t=-1), SHAPE), (dict(d=12), SHAPE), (dict(d=0), SHAPE),
+    (dict(t=2 ** 31), SHAPE), (dict(t=2 ** 30, d=8192), SHAPE), (dict(eps=-1.0), INVALID),
+    (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID), (dict(X=None), INVALID),
+    (dict(gamma=None), INVALID), (dict(Y=None), INVALID), (dict(H=None), INVALID),
+    (dict(residual=None), INVALID), (dict(Y=P, H=P), INVALID), (dict(X=P + 8), MISALIGNED),
+    (dict(gamma=P + 2), MISALIGNED), (dict(H=P + 8), MISALIGNED), (dict(Y=P + 8), MISALIGNED),
+    (dict(residual=P + 8), MISALIGNED), (dict(rstd=P + 2), MISALIGNED),
+])
+def test_rmsnorm_refusals(change, status):
+    assert _status(gemm_epi.gemm_epi_rmsnorm, **{**NORM, **change}) == status
+
+
+NORM8 = dict(t=4, d=64, dtype="f16", X=P, residual=None, gamma=P, eps=1e-6, H=None, Q=2 * P,
+             mode="TENSOR", scale=P, workspace=P)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(scale=None), INVALID), (dict(workspace=None), INVALID), (dict(Q=P), INVALID),
+    (dict(scale=P + 2), MISALIGNED), (dict(workspace=P + 8), MISALIGNED), (dict(Q=P + 8), MISALIGNED),
+    (dict(d=4), SHAPE), (dict(dtype="e4m3"), INVALID), (dict(mode="ROW", scale=None), INVALID),
+    (dict(residual=2 * P, H=3 * P), INVALID),
+])
+def test_rmsnorm_e4m3_refusals(change, status):
+    assert _status(gemm_epi.gemm_epi_rmsnorm_e4m3, **{**NORM8, **change}) == status
+
+
+def test_rmsnorm_e4m3_bad_mode():
+    lib = gemm_epi.load_library()
+    for mode in (-1, 3):
+        assert lib.gemm_epi_rmsnorm_e4m3(4, 64, 1, P, None, P, 1e-6, None, 2 * P, mode, P, None, P,
+                                         None) == INVALID
+
+
+BWD = dict(t=4, d=64, dtype="bf16", dY=P, H=2 * P, gamma=P, rstd=P, dH=None, dX=3 * P, dgamma=P,
+           workspace=P)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype="e4m3"), INVALID), (dict(d=20), SHAPE), (dict(dY=None), INVALID),
+    (dict(H=None), INVALID), (dict(gamma=None), INVALID), (dict(rstd=None), INVALID),
+    (dict(dX=None), INVALID), (dict(dgamma=None), INVALID), (dict(workspace=None), INVALID),
+    (dict(dX=2 * P), INVALID), (dict(dY=P + 8), MISALIGNED), (dict(rstd=P + 2), MISALIGNED),
+    (dict(dH=P + 8), MISALIGNED), (dict(dgamma=P + 2), MISALIGNED),
+    (dict(workspace=P + 8), MISALIGNED),
+])
+def test_rmsnorm_backward_refusals(change, status):
+    assert _status(gemm_epi.gemm_epi_rmsnorm_backward, **{**BWD, **change}) == status
+
+
+def test_rmsnorm_workspace_sizes():
+    ws = gemm_epi.gemm_epi_rmsnorm_workspace
+    assert ws(4, 12) == 0 and ws(-1, 8) == 0 and ws(4, 0) == 0
+    assert ws(0, 8) >= 0 and ws(1, 8) > 0
+    for t, d in ((1, 8), (100000, 8), (7, 65536)):
+        assert ws(t, d) % 16 == 0
+
+
+W4 = dict(m=2, n=64, k=128, group=32, dtype="bf16", epilog="BIAS", A=P, W=P, scales=P, zeros=None,
+          bias=P, residual=None, D=P)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(group=16), SHAPE), (dict(group=0), SHAPE), (dict(k=48), SHAPE), (dict(n=12), SHAPE),
+    (dict(m=65), SHAPE), (dict(m=-1), SHAPE), (dict(n=-8), SHAPE), (dict(k=-32), SHAPE),
+    (dict(n=2 ** 31), SHAPE), (dict(dtype="e4m3"), INVALID), (dict(epilog="RELU_AUX_BIAS"), INVALID),
+    (dict(epilog="GELU_AUX_BIAS"), INVALID), (dict(epilog="LN_GELU_BIAS"), INVALID),
+    (dict(epilog="DRELU_BGRAD"), INVALID), (dict(A=None), INVALID), (dict(W=None), INVALID),
+    (dict(scales=None), INVALID), (dict(D=None), INVALID), (dict(bias=None), INVALID),
+    (dict(residual=P), INVALID), (dict(epilog="BIAS_RESIDUAL"), INVALID),
+    (dict(epilog="NONE"), INVALID), (dict(A=P + 8), MISALIGNED), (dict(W=P + 4), MISALIGNED),
+    (dict(D=P + 8), MISALIGNED), (dict(scales=P + 1), MISALIGNED), (dict(bias=P + 1), MISALIGNED),
+])
+def test_w4_refusals(change, status):
+    assert _status(gemm_epi.gemm_epi_w4_matmul, **{**W4, **change}) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(group=48), SHAPE), (dict(k=96, group=64), SHAPE), (dict(n=4), SHAPE), (dict(W=None), INVALID),
+    (dict(scales=None), INVALID), (dict(B=None), INVALID), (dict(B=P + 2), MISALIGNED),
+    (dict(W=P + 8), MISALIGNED), (dict(dtype="e4m3"), INVALID),
+])
+def test_w4_dequantize_refusals(change, status):
+    base = dict(n=64, k=128, group=32, dtype="f16", W=P, scales=P, zeros=None, B=P)
+    assert _status(gemm_epi.gemm_epi_w4_dequantize, **{**base, **change}) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(count=-1), SHAPE), (dict(dtype="e4m3"), INVALID), (dict(p=-0.1), INVALID),
+    (dict(p=1.5), INVALID), (dict(p=float("nan")), INVALID), (dict(X=None), INVALID),
+    (dict(Y=None), INVALID), (dict(X=P + 2), MISALIGNED), (dict(Y=P + 8), MISALIGNED),
+    (dict(residual=P + 2), MISALIGNED), (dict(offset_device=P + 4), MISALIGNED),
+])
+def test_dropout_refusals(change, status):
+    base = dict(count=100, dtype="bf16", X=P, residual=None, p=0.1, seed=1, offset=0, Y=P)
+    assert _status(gemm_epi.gemm_epi_dropout, **{**base, **change}) == status
+
+
+def test_empty_problems_launch_nothing():
+    none = dict(stream=0)
+    gemm_epi.gemm_epi_rmsnorm(0, 64, "bf16", None, None, None, 1e-6, None, None, **none)
+    gemm_epi.gemm_epi_rmsnorm_e4m3(0, 64, "bf16", None, None, None, 1e-6, None, None, "TENSOR", None, **none)
+    gemm_epi.gemm_epi_w4_matmul(0, 64, 128, 32, "bf16", "BIAS", None, None, None, None, None, None, None, **none)
+    gemm_epi.gemm_epi_w4_matmul(2, 0, 128, 32, "bf16", "BIAS", None, None, None, None, None, None, None, **none)
+    gemm_epi.gemm_epi_w4_dequantize(64, 0, 32, "bf16", None, None, None, None, **none)
+    gemm_epi.gemm_epi_dropout(0, "f16", None, None, 0.5, 1, 2, None, **none)
+
+
+def test_binding_refuses_tensors_it_cannot_pass():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        gemm_epi.gemm_epi_rmsnorm(4, 64, "bf16", x, None, x, 1e-6, None, x, stream=0)
+    with pytest.raises(ValueError, match="CUDA"):
+        gemm_epi.gemm_epi_dropout(256, "bf16", x, None, 0.5, 1, 2, x, stream=0)
