@@ -3,6 +3,7 @@
 // thread before it touches memory.
 #pragma once
 
+#include <atomic>
 #include <cuda_runtime.h>
 
 namespace gemm_epi {
@@ -22,6 +23,21 @@ cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, i
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
+// Let a kernel use up to `bytes` of dynamic shared memory on the current device; `done` (one
+// bit per device, static beside the kernel's launch) makes it a single call per device.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel* kernel, int bytes, std::atomic<unsigned long long>& done)
+{
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (s == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return s;
 }
 
 }  // namespace gemm_epi

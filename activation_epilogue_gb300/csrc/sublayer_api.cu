@@ -168,8 +168,8 @@ gemm_epi_status gemm_epi_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t grou
         (residual != nullptr) != (epilog == GEMM_EPI_BIAS_RESIDUAL))
         return GEMM_EPI_ERR_INVALID_ARG;
     if (k > 0 && (!A || !W || !scales)) return GEMM_EPI_ERR_INVALID_ARG;
-    if (!aligned(A, 16) || !aligned(W, 16) || !aligned(scales, 2) || !aligned(bias, 2) ||
-        !aligned(residual, 16) || !aligned(D, 16))
+    if (!aligned(A, 16) || !aligned(W, 16) || !aligned(scales, 16) || !aligned(zeros, 8) ||
+        !aligned(bias, 2) || !aligned(residual, 16) || !aligned(D, 16))
         return GEMM_EPI_ERR_MISALIGNED;
     int sms = 0;
     st = device_sms(&sms);
@@ -198,7 +198,8 @@ gemm_epi_status gemm_epi_w4_dequantize(int64_t n, int64_t k, int64_t group,
     if (st != GEMM_EPI_OK) return st;
     if (n == 0 || k == 0) return GEMM_EPI_OK;
     if (!W || !scales || !B) return GEMM_EPI_ERR_INVALID_ARG;
-    if (!aligned(W, 16) || !aligned(scales, 2) || !aligned(B, 16)) return GEMM_EPI_ERR_MISALIGNED;
+    if (!aligned(W, 16) || !aligned(scales, 16) || !aligned(zeros, 8) || !aligned(B, 16))
+        return GEMM_EPI_ERR_MISALIGNED;
     int sms = 0;
     st = device_sms(&sms);
     if (st != GEMM_EPI_OK) return st;

@@ -412,8 +412,8 @@ int64_t gemm_epi_rmsnorm_workspace(int64_t t, int64_t d);
  * GELU_BIAS, TANH_BIAS, BIAS_RESIDUAL and NONE as for plans; bias is NULL exactly for NONE,
  * the residual given exactly for BIAS_RESIDUAL, and D may be the residual itself.  The
  * differences q - z are exact in 16 bits and their products with A are summed in fp32, group
- * by group, with the scales applied in fp32.  A, W, residual and D 16-byte aligned, the rest
- * 2-byte (zeros: any).  No workspace, no plan; asynchronous on `stream` as above. */
+ * by group, with the scales applied in fp32.  A, W, scales, residual and D 16-byte aligned,
+ * zeros 8-byte, bias 2-byte.  No workspace, no plan; asynchronous on `stream` as above. */
 gemm_epi_status gemm_epi_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group,
                                    gemm_epi_dtype dtype, gemm_epi_epilog epilog, const void* A,
                                    const void* W, const void* scales, const uint8_t* zeros,

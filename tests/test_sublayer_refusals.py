@@ -96,7 +96,8 @@ W4 = dict(m=2, n=64, k=128, group=32, dtype="bf16", epilog="BIAS", A=P, W=P, sca
     (dict(scales=None), INVALID), (dict(D=None), INVALID), (dict(bias=None), INVALID),
     (dict(residual=P), INVALID), (dict(epilog="BIAS_RESIDUAL"), INVALID),
     (dict(epilog="NONE"), INVALID), (dict(A=P + 8), MISALIGNED), (dict(W=P + 4), MISALIGNED),
-    (dict(D=P + 8), MISALIGNED), (dict(scales=P + 1), MISALIGNED), (dict(bias=P + 1), MISALIGNED),
+    (dict(D=P + 8), MISALIGNED), (dict(scales=P + 2), MISALIGNED), (dict(bias=P + 1), MISALIGNED),
+    (dict(zeros=P + 4), MISALIGNED),
 ])
 def test_w4_refusals(change, status):
     assert _status(gemm_epi.gemm_epi_w4_matmul, **{**W4, **change}) == status
