@@ -78,8 +78,8 @@ cudaError_t dropout_launch(const DropoutArgs& a, bool bf16, int sm_count, cudaSt
     const long long blocks = (a.count + 8 * 256 - 1) / (8 * 256);
     const long long cap = static_cast<long long>(sm_count) * 8;
     const int grid = static_cast<int>(blocks < cap ? blocks : cap);
-    return bf16 ? launch_dependent(dropout_kernel<true>, grid, 256, 0, stream, a)
-                : launch_dependent(dropout_kernel<false>, grid, 256, 0, stream, a);
+    return bf16 ? launch_dependent(dropout_kernel<true>, grid, 256, 0, stream, 1, a)
+                : launch_dependent(dropout_kernel<false>, grid, 256, 0, stream, 1, a);
 }
 
 }  // namespace gemm_epi

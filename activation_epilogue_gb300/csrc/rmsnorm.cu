@@ -240,21 +240,21 @@ int rmsnorm_backward_parts(long long t)
 cudaError_t rmsnorm_launch(const RmsnormArgs& a, bool bf16, cudaStream_t stream)
 {
     const int grid = a.mode == kRmsTensor ? rmsnorm_max_parts(a.t) : a.t;
-    cudaError_t e = bf16 ? launch_dependent(rmsnorm_kernel<true>, grid, kThreadsPerRow, 0, stream, a)
-                         : launch_dependent(rmsnorm_kernel<false>, grid, kThreadsPerRow, 0, stream, a);
+    cudaError_t e = bf16 ? launch_dependent(rmsnorm_kernel<true>, grid, kThreadsPerRow, 0, stream, 1, a)
+                         : launch_dependent(rmsnorm_kernel<false>, grid, kThreadsPerRow, 0, stream, 1, a);
     if (e != cudaSuccess || a.mode != kRmsTensor) return e;
-    return bf16 ? launch_dependent(rmsnorm_quantise_kernel<true>, grid, kThreadsPerRow, 0, stream, a, grid)
-                : launch_dependent(rmsnorm_quantise_kernel<false>, grid, kThreadsPerRow, 0, stream, a, grid);
+    return bf16 ? launch_dependent(rmsnorm_quantise_kernel<true>, grid, kThreadsPerRow, 0, stream, 1, a, grid)
+                : launch_dependent(rmsnorm_quantise_kernel<false>, grid, kThreadsPerRow, 0, stream, 1, a, grid);
 }
 
 cudaError_t rmsnorm_backward_launch(const RmsnormBackwardArgs& a, bool bf16, cudaStream_t stream)
 {
     const int parts = rmsnorm_backward_parts(a.t);
     const cudaError_t e =
-        bf16 ? launch_dependent(rmsnorm_backward_kernel<true>, parts, kThreadsPerRow, 0, stream, a)
-             : launch_dependent(rmsnorm_backward_kernel<false>, parts, kThreadsPerRow, 0, stream, a);
+        bf16 ? launch_dependent(rmsnorm_backward_kernel<true>, parts, kThreadsPerRow, 0, stream, 1, a)
+             : launch_dependent(rmsnorm_backward_kernel<false>, parts, kThreadsPerRow, 0, stream, 1, a);
     if (e != cudaSuccess) return e;
-    return launch_dependent(rmsnorm_dgamma_kernel, (a.d + 255) / 256, 256, 0, stream,
+    return launch_dependent(rmsnorm_dgamma_kernel, (a.d + 255) / 256, 256, 0, stream, 1,
                             static_cast<const float*>(a.ws_dgamma), parts, a.d, a.dgamma);
 }
 

@@ -19,7 +19,6 @@
 //   * A group's sum is complete in the accumulator (groups are whole MMAs, all of whose lanes
 //     are in one group), so the scale multiplies an fp32 sum, and no weight is ever rounded.
 //   * The KW warps' sums meet in shared memory, in order; then the epilogue.
-#include "gelu.cuh"
 #include "kernel_params.h"
 #include "launch.h"
 #include "ptx.cuh"
@@ -30,6 +29,8 @@ namespace gemm_epi {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kThreadsW4 = kWarps * 32;
+constexpr int kMaxSmem = 227 * 1024;
 constexpr int kBlockK = 128;  // values of k per warp and stage: 64 bytes of each row of W
 
 // The epilogue of one element, from the exact functions (a few elements per thread).
@@ -44,17 +45,9 @@ __device__ __forceinline__ float w4_epilogue(float v, int epilog, float residual
     }
 }
 
-// 16 bytes to shared memory, or zeros where `live` is false (src must be readable either way).
-__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool live)
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
-                 : "memory");
-}
-
-__device__ __forceinline__ void cp_async_8_or_zero(uint32_t dst, const void* src, bool live)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0)
-                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -63,6 +56,13 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait_group()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr)
@@ -78,57 +78,90 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
                                           uint32_t a3, uint32_t b0, uint32_t b1)
 {
     if constexpr (BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
                      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
                      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The 16-bit type's bits of 128 (bf16) or 1024 (f16), in both halves.
+// (a & b) | c in one instruction (left to itself the compiler takes two where b and c are both
+// constants).
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
 template <bool BF16>
-__device__ constexpr uint32_t w4_magic()
+__device__ __forceinline__ uint32_t sub16x2(uint32_t a, uint32_t b)
 {
-    return BF16 ? 0x43004300u : 0x64006400u;
+    uint32_t d;
+    if constexpr (BF16)
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
-// q - z of nibbles (j, j + 4) of a word as a register pair; zoff = magic + z in both halves.
-template <bool BF16, int J>
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t zoff)
-{
-    const uint32_t v = ((w >> (4 * J)) & 0x000F000Fu) | w4_magic<BF16>();
-    if constexpr (BF16) {
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&zoff));
-        return *reinterpret_cast<const uint32_t*>(&d);
+// What turns a word of W into values: the bits that a pair's nibbles are set in, and with the
+// zero points z of the column, what to subtract.
+//   bf16 (7 bits of mantissa): nibble in bits 0-3 under 128's bits is 128 + q.
+//   f16 (10 bits): nibble in bits 0-3 under 1024's bits is 1024 + q, in bits 4-7 under 64's
+//   bits 64 + q, so two pairs come of each shift.
+template <bool BF16>
+struct W4Unpack {
+    uint32_t sub_even, sub_odd;  // of pairs 0, 2 and 1, 3
+    __device__ __forceinline__ void set(uint32_t z)
+    {
+        if constexpr (BF16) {
+            sub_even = sub_odd = z * 0x10001u + 0x43004300u;
+        } else {
+            sub_even = z * 0x10001u + 0x64006400u;
+            sub_odd = z * 0x100010u + 0x54005400u;
+        }
     }
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&zoff));
-    return *reinterpret_cast<const uint32_t*>(&d);
-}
+    // v[j]: q - z of nibbles j (lower half) and j + 4, exactly
+    __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&v)[4]) const
+    {
+        if constexpr (BF16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = sub16x2<true>(and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u), sub_even);
+        } else {
+            const uint32_t h = w >> 8;
+            v[0] = sub16x2<false>(and_or(w, 0x000F000Fu, 0x64006400u), sub_even);
+            v[1] = sub16x2<false>(and_or(w, 0x00F000F0u, 0x54005400u), sub_odd);
+            v[2] = sub16x2<false>(and_or(h, 0x000F000Fu, 0x64006400u), sub_even);
+            v[3] = sub16x2<false>(and_or(h, 0x00F000F0u, 0x54005400u), sub_odd);
+        }
+    }
+};
 
-// Shared-memory layout of one stage, in bytes, for m rows of A.
+// One stage in shared memory for m rows of A, in bytes.  Rows are padded so that eight rows'
+// 16-byte pieces (ldmatrix), or two rows' 64 bytes (rows of A), fall in different banks.
 template <int MT, int CW, int G>
 struct W4Stage {
     static constexpr int kKW = kWarps / CW;
     static constexpr int kCols = 16 * MT * CW;
     static constexpr int kStageK = kBlockK * kKW;
     static constexpr int kGroups = kStageK / G;
-    static constexpr int kW = kCols * kKW * 64;           // [kw][column][64 bytes], chunks swizzled
-    static constexpr int kScales = kGroups * kCols * 2;   // [group][column]
-    static constexpr int kZeros = kGroups * kCols;        // [group][column]
-    static constexpr int kARow = kStageK * 2 + 64;        // a row of A, padded by half a bank cycle
-    static constexpr int kA = kW + kScales + kZeros;
-    static __host__ __device__ int bytes(int m) { return kA + m * kARow; }
+    static constexpr int kWRow = kKW * 64 + 16;
+    static constexpr int kARow = kStageK * 2 + 64;
+    static constexpr int kScales = kCols * kWRow;                  // [group][column] 16 bits
+    static constexpr int kZeros = kScales + kGroups * kCols * 2;   // [group][column] bytes
+    static constexpr int kA = kZeros + kGroups * kCols;
+    static __host__ __device__ constexpr int bytes(int m) { return kA + m * kARow; }
 };
 
-constexpr int kMaxStages = 6;
-
-template <bool BF16, int NT, int MT, int CW, int G>
-__global__ void __launch_bounds__(kWarps * 32) w4_matmul_kernel(const W4Args a, int stages)
+// cluster: CTAs of a cluster that split k (their sums meet over distributed shared memory).
+template <bool BF16, int NT, int MT, int CW, int G, int STAGES>
+__global__ void __launch_bounds__(kThreadsW4) w4_matmul_kernel(const W4Args a, int cluster)
 {
     using S = W4Stage<MT, CW, G>;
     constexpr int KW = S::kKW;
@@ -136,46 +169,68 @@ __global__ void __launch_bounds__(kWarps * 32) w4_matmul_kernel(const W4Args a, 
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cw = warp % CW, kw = warp / CW;
-    const int n0 = blockIdx.x * S::kCols;
+    const int rank = static_cast<int>(blockIdx.x) % cluster;
+    const int n0 = static_cast<int>(blockIdx.x) / cluster * S::kCols;
+    const int cols = min(S::kCols, a.n - n0);
     const int stage_bytes = S::bytes(a.m);
-    const int steps = (a.k + S::kStageK - 1) / S::kStageK;
+    const int all_steps = (a.k + S::kStageK - 1) / S::kStageK;
+    const int first = static_cast<int>(static_cast<long long>(all_steps) * rank / cluster);
+    const int steps = static_cast<int>(static_cast<long long>(all_steps) * (rank + 1) / cluster) - first;
 
-    grid_dependency_wait();
-    grid_launch_dependents();
+    // What this thread copies in every stage.  W: kWCopies 16-byte chunks (32 values of k) of
+    // column wcol, kWLanes chunks apart; columns past n copy the last one's (nobody reads what
+    // comes of them).  A: chunk ac (8 values) of rows arow, arow + kARows, ...  Scales and zero
+    // points: 8 columns of one group, the first half of the block and the second.
+    constexpr int kWLanes = kThreadsW4 / S::kCols;
+    constexpr int kWCopies = KW * 4 / kWLanes;
+    constexpr int kAChunks = S::kStageK / 8;
+    constexpr int kARows = kThreadsW4 / kAChunks;
+    constexpr int kSChunks = S::kGroups * (S::kCols / 8);
+    static_assert(kThreadsW4 % S::kCols == 0 && KW * 4 % kWLanes == 0 && kThreadsW4 % kAChunks == 0 &&
+                      2 * kSChunks <= kThreadsW4, "every thread has a fixed part in the copies");
+    const int wcol = tid / kWLanes, wc = tid % kWLanes;
+    const int ac = tid % kAChunks, arow = tid / kAChunks;
+    const int sc = tid % (kThreadsW4 / 2);
+    const int sgroup = sc / (S::kCols / 8), scol = sc % (S::kCols / 8) * 8;
+    const bool copies_scales = tid < kSChunks;
+    const bool copies_zeros = a.zeros != nullptr && tid >= kThreadsW4 / 2 && sc < kSChunks;
+    const uint8_t* wsrc = static_cast<const uint8_t*>(a.W) +
+                          (static_cast<long long>(min(n0 + wcol, a.n - 1)) * a.k + first * S::kStageK) / 2 + wc * 16;
+    const uint16_t* asrc = static_cast<const uint16_t*>(a.A) + static_cast<long long>(arow) * a.k + first * S::kStageK + ac * 8;
+    const long long a_step = static_cast<long long>(kARows) * a.k;
+    const long long s_step = static_cast<long long>(S::kGroups) * a.n;
+    const long long sat = static_cast<long long>(first * S::kGroups + sgroup) * a.n + min(n0 + scol, a.n - 8);
+    const uint16_t* ssrc = static_cast<const uint16_t*>(a.scales) + sat;
+    const uint8_t* zsrc = a.zeros + sat;
+    const uint32_t wdst = wcol * S::kWRow + wc * 16;
+    const uint32_t adst = S::kA + arow * S::kARow + ac * 16;
+    int load_left = a.k - first * S::kStageK;  // values of k from the next stage to load on
 
-    const uint8_t* W = static_cast<const uint8_t*>(a.W);
-    const uint16_t* A = static_cast<const uint16_t*>(a.A);
-    const uint16_t* scales = static_cast<const uint16_t*>(a.scales);
-    auto load = [&](int step) {
-        const uint32_t st = sbase + (step % stages) * stage_bytes;
-        const int k0 = step * S::kStageK;
-        // weights: chunk = 16 bytes = 32 values of k
-        constexpr int kRowChunks = KW * 4;
-        for (int i = tid; i < S::kCols * kRowChunks; i += kWarps * 32) {
-            const int col = i / kRowChunks, c = i % kRowChunks;
-            const int k = k0 + c * 32;
-            const bool live = n0 + col < a.n && k < a.k;
-            const uint8_t* src = live ? W + (static_cast<long long>(n0 + col) * a.k + k) / 2 : W;
-            const uint32_t dst = st + ((c / 4) * S::kCols + col) * 64 + (((c & 3) ^ ((col >> 1) & 3)) << 4);
-            cp_async_16_or_zero(dst, src, live);
+    auto load = [&](uint32_t st) {
+        // (past the end of k nothing is copied, and nothing of it is read)
+        const bool whole = load_left >= S::kStageK;
+#pragma unroll
+        for (int i = 0; i < kWCopies; ++i)
+            if (whole || (wc + i * kWLanes) * 32 < load_left)
+                cp_async_16(st + wdst + i * kWLanes * 16, wsrc + i * kWLanes * 16);
+        wsrc += S::kStageK / 2;
+        if (whole || ac * 8 < load_left) {
+            const uint16_t* ap = asrc;
+            uint32_t dst = st + adst;
+            for (int row = arow; row < a.m; row += kARows) {
+                cp_async_16(dst, ap);
+                ap += a_step;
+                dst += kARows * S::kARow;
+            }
         }
-        // rows of A: chunk = 8 values
-        constexpr int kAChunks = S::kStageK / 8;
-        for (int i = tid; i < a.m * kAChunks; i += kWarps * 32) {
-            const int row = i / kAChunks, c = i % kAChunks;
-            const int k = k0 + c * 8;
-            const bool live = k < a.k;
-            const uint16_t* src = live ? A + static_cast<long long>(row) * a.k + k : A;
-            cp_async_16_or_zero(st + S::kA + row * S::kARow + c * 16, src, live);
+        asrc += S::kStageK;
+        if (whole || sgroup * G < load_left) {
+            if (copies_scales) cp_async_16(st + S::kScales + (sgroup * S::kCols + scol) * 2, ssrc);
+            if (copies_zeros) cp_async_8(st + S::kZeros + sgroup * S::kCols + scol, zsrc);
         }
-        // scales and zero points: 8 columns each
-        for (int i = tid; i < S::kGroups * (S::kCols / 8); i += kWarps * 32) {
-            const int g = i / (S::kCols / 8), c = i % (S::kCols / 8) * 8;
-            const bool live = n0 + c < a.n && k0 + g * G < a.k;
-            const long long at = live ? static_cast<long long>(k0 / G + g) * a.n + n0 + c : 0;
-            cp_async_16_or_zero(st + S::kW + (g * S::kCols + c) * 2, scales + at, live);
-            if (a.zeros) cp_async_8_or_zero(st + S::kW + S::kScales + g * S::kCols + c, a.zeros + at, live);
-        }
+        ssrc += s_step;
+        zsrc += s_step;
+        load_left -= S::kStageK;
     };
 
     float total[MT][NT][4];
@@ -186,96 +241,100 @@ __global__ void __launch_bounds__(kWarps * 32) w4_matmul_kernel(const W4Args a, 
 #pragma unroll
             for (int c = 0; c < 4; ++c) total[i][j][c] = 0.0f;
 
-    for (int s = 0; s < stages - 1; ++s) {
-        if (s < steps) load(s);
+    grid_dependency_wait();
+    grid_launch_dependents();
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+        if (s < steps) load(sbase + s * stage_bytes);
         cp_async_commit();
     }
     const int r = lane >> 2, t = lane & 3;
-    for (int step = 0; step < steps; ++step) {
+    // byte offsets in a stage of what this lane reads
+    const uint32_t woff = (cw * MT * 16 + (lane & 7)) * S::kWRow + kw * 64 + ((lane >> 3) << 4);
+    int aoff[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)  // (rows past m: columns of the product that nobody reads)
+        aoff[j] = S::kA + min(j * 8 + r, a.m - 1) * S::kARow + kw * 256 + t * 16;
+    const int soff = S::kScales + (kw * (kBlockK / G) * S::kCols + cw * MT * 16 + r) * 2;
+    const int zat = S::kZeros + kw * (kBlockK / G) * S::kCols + cw * MT * 16 + r;
+    int k_left = a.k - first * S::kStageK - kw * kBlockK;  // from this warp's part of the stage on
+    int slot = 0, fill = (STAGES - 1) * stage_bytes;       // byte offsets of stages
+    for (int step = 0; step < steps; ++step, k_left -= S::kStageK) {
         // this step's copies (of this thread, then of all) have landed, and every warp is done
         // with the stage that the next load overwrites
-        switch (stages) {
-        case 2: cp_async_wait_group<0>(); break;
-        case 3: cp_async_wait_group<1>(); break;
-        case 4: cp_async_wait_group<2>(); break;
-        case 5: cp_async_wait_group<3>(); break;
-        default: cp_async_wait_group<4>(); break;
-        }
+        cp_async_wait_group<STAGES - 2>();
         __syncthreads();
-        if (step + stages - 1 < steps) load(step + stages - 1);
+        if (step + STAGES - 1 < steps) load(sbase + fill);
         cp_async_commit();
-        const uint32_t st = sbase + (step % stages) * stage_bytes;
-        const uint8_t* stp = smem + (step % stages) * stage_bytes;
-        // this warp's weights: chunk i of row (lane & 7) [+ 8] for ldmatrix
-        uint32_t w[MT][2][4];
+        fill = fill == (STAGES - 1) * stage_bytes ? 0 : fill + stage_bytes;
+        const uint8_t* stp = smem + slot;
+        const uint32_t st = sbase + slot;
+        slot = slot == (STAGES - 1) * stage_bytes ? 0 : slot + stage_bytes;
+        auto block = [&](int chunks) {
+            uint32_t w[MT][2][4];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int col = (cw * MT + i) * 16 + h * 8 + (lane & 7);
-                ldmatrix_x4(w[i][h], st + (kw * S::kCols + col) * 64 + (((lane >> 3) ^ ((col >> 1) & 3)) << 4));
-            }
-        float part[MT][NT][4];
+                for (int h = 0; h < 2; ++h) ldmatrix_x4(w[i][h], st + woff + (i * 16 + h * 8) * S::kWRow);
+            float part[MT][NT][4];
+            W4Unpack<BF16> unpack[MT][2];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int g = kw * (kBlockK / G) + c * 32 / G;  // group within the stage
-            if (c * 32 % G == 0) {
+            for (int c = 0; c < 4; ++c) {
+                if (c >= chunks) break;
+                const int g = c * 32 / G;  // this warp's group
+                if (c * 32 % G == 0) {
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
+                    for (int i = 0; i < MT; ++i) {
+                        unpack[i][0].set(a.zeros ? stp[zat + g * S::kCols + i * 16] : 8);
+                        unpack[i][1].set(a.zeros ? stp[zat + g * S::kCols + i * 16 + 8] : 8);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                        for (int j = 0; j < NT; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) part[i][j][e] = 0.0f;
-            }
-            // rows of A: 8 values of k per lane, paired (k, k + 4)
-            uint32_t b[NT][4];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int row = min(j * 8 + r, a.m - 1);  // (rows past m: columns nobody reads)
-                const uint4 v = *reinterpret_cast<const uint4*>(stp + S::kA + row * S::kARow + kw * 256 + c * 64 + t * 16);
-                b[j][0] = __byte_perm(v.x, v.z, 0x5410);
-                b[j][1] = __byte_perm(v.x, v.z, 0x7632);
-                b[j][2] = __byte_perm(v.y, v.w, 0x5410);
-                b[j][3] = __byte_perm(v.y, v.w, 0x7632);
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int col = (cw * MT + i) * 16 + r;
-                uint32_t z0 = 8, z1 = 8;
-                if (a.zeros) {
-                    const uint8_t* zp = stp + S::kW + S::kScales + g * S::kCols + col;
-                    z0 = zp[0];
-                    z1 = zp[8];
+                            for (int e = 0; e < 4; ++e) part[i][j][e] = 0.0f;
+                    }
                 }
-                z0 = z0 * 0x10001u + w4_magic<BF16>();
-                z1 = z1 * 0x10001u + w4_magic<BF16>();
-                const uint32_t lo = w[i][0][c], hi = w[i][1][c];
-                const uint32_t p0 = w4_pair<BF16, 0>(lo, z0), p1 = w4_pair<BF16, 1>(lo, z0);
-                const uint32_t p2 = w4_pair<BF16, 2>(lo, z0), p3 = w4_pair<BF16, 3>(lo, z0);
-                const uint32_t q0 = w4_pair<BF16, 0>(hi, z1), q1 = w4_pair<BF16, 1>(hi, z1);
-                const uint32_t q2 = w4_pair<BF16, 2>(hi, z1), q3 = w4_pair<BF16, 3>(hi, z1);
+                // rows of A: 8 values of k per lane, paired (k, k + 4)
+                uint32_t b[NT][4];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    mma_16816<BF16>(part[i][j], p0, q0, p1, q1, b[j][0], b[j][1]);
-                    mma_16816<BF16>(part[i][j], p2, q2, p3, q3, b[j][2], b[j][3]);
+                    const uint4 v = *reinterpret_cast<const uint4*>(stp + aoff[j] + c * 64);
+                    b[j][0] = __byte_perm(v.x, v.z, 0x5410);
+                    b[j][1] = __byte_perm(v.x, v.z, 0x7632);
+                    b[j][2] = __byte_perm(v.y, v.w, 0x5410);
+                    b[j][3] = __byte_perm(v.y, v.w, 0x7632);
                 }
-                if ((c + 1) * 32 % G == 0) {
-                    const uint16_t* sp = reinterpret_cast<const uint16_t*>(stp + S::kW) + g * S::kCols + col;
-                    const float s0 = decode16<BF16>(sp[0]), s1 = decode16<BF16>(sp[8]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t p[4], q[4];
+                    unpack[i][0](w[i][0][c], p);
+                    unpack[i][1](w[i][1][c], q);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        total[i][j][0] = fmaf(part[i][j][0], s0, total[i][j][0]);
-                        total[i][j][1] = fmaf(part[i][j][1], s0, total[i][j][1]);
-                        total[i][j][2] = fmaf(part[i][j][2], s1, total[i][j][2]);
-                        total[i][j][3] = fmaf(part[i][j][3], s1, total[i][j][3]);
+                        mma_16816<BF16>(part[i][j], p[0], q[0], p[1], q[1], b[j][0], b[j][1]);
+                        mma_16816<BF16>(part[i][j], p[2], q[2], p[3], q[3], b[j][2], b[j][3]);
+                    }
+                    if ((c + 1) * 32 % G == 0) {
+                        const uint16_t* s16 = reinterpret_cast<const uint16_t*>(stp + soff) + g * S::kCols + i * 16;
+                        const float s0 = decode16<BF16>(s16[0]), s1 = decode16<BF16>(s16[8]);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            total[i][j][0] = fmaf(part[i][j][0], s0, total[i][j][0]);
+                            total[i][j][1] = fmaf(part[i][j][1], s0, total[i][j][1]);
+                            total[i][j][2] = fmaf(part[i][j][2], s1, total[i][j][2]);
+                            total[i][j][3] = fmaf(part[i][j][3], s1, total[i][j][3]);
+                        }
                     }
                 }
             }
-        }
+        };
+        if (k_left >= kBlockK)
+            block(4);
+        else if (k_left > 0)
+            block(k_left / 32);  // (k ends on a group's border)
     }
+    cp_async_wait_group<0>();
 
     // The k-warps' sums: [kw][row of A][column], then one thread per element adds them in order.
-    cp_async_wait_group<0>();
     __syncthreads();
     float* red = reinterpret_cast<float*>(smem);
     constexpr int kRedRow = S::kCols + 1;  // (odd: a warp's stores to 8 rows fall in 8 banks)
@@ -290,55 +349,73 @@ __global__ void __launch_bounds__(kWarps * 32) w4_matmul_kernel(const W4Args a, 
                 red[(kw * NT * 8 + row) * kRedRow + col] = total[i][j][e];
             }
     __syncthreads();
-    for (int i = tid; i < a.m * S::kCols; i += kWarps * 32) {
-        const int row = i / S::kCols, col = i % S::kCols;
-        if (n0 + col >= a.n) continue;
-        float v = 0.0f;
+    const int elements = a.m * S::kCols;
+    if (cluster > 1) {
+        for (int i = tid; i < elements; i += kThreadsW4) {
+            const int at = i / S::kCols * kRedRow + i % S::kCols;
+            float v = red[at];
 #pragma unroll
-        for (int q = 0; q < KW; ++q) v += red[(q * NT * 8 + row) * kRedRow + col];
+            for (int q = 1; q < KW; ++q) v += red[q * NT * 8 * kRedRow + at];
+            red[at] = v;
+        }
+        cluster_sync_all();
+    }
+    for (int i = rank * kThreadsW4 + tid; i < elements; i += kThreadsW4 * cluster) {
+        const int row = i / S::kCols, col = i % S::kCols;
+        if (col >= cols) continue;
+        const int ra = row * kRedRow + col;
+        float v = 0.0f;
+        if (cluster > 1) {
+            for (int q = 0; q < cluster; ++q) v += ld_shared_cluster_f32(map_shared_rank(sbase + ra * 4, q));
+        } else {
+#pragma unroll
+            for (int q = 0; q < KW; ++q) v += red[q * NT * 8 * kRedRow + ra];
+        }
         const long long at = static_cast<long long>(row) * a.n + n0 + col;
         if (a.bias) v += decode16<BF16>(static_cast<const uint16_t*>(a.bias)[n0 + col]);
         const float res = a.residual ? decode16<BF16>(static_cast<const uint16_t*>(a.residual)[at]) : 0.0f;
         static_cast<uint16_t*>(a.D)[at] = encode16<BF16>(w4_epilogue(v, a.epilog, res));
     }
+    if (cluster > 1) cluster_sync_all();  // the peers' shared memory stays until it is read
 }
 
-template <bool BF16, int NT, int MT, int CW, int G>
-cudaError_t w4_launch_one(const W4Args& a, cudaStream_t stream)
+template <bool BF16, int NT, int MT, int CW, int G, int STAGES>
+cudaError_t w4_launch_one(const W4Args& a, int sms, cudaStream_t stream)
 {
     using S = W4Stage<MT, CW, G>;
-    constexpr int kMaxSmem = 227 * 1024;
-    auto kernel = w4_matmul_kernel<BF16, NT, MT, CW, G>;
+    auto kernel = w4_matmul_kernel<BF16, NT, MT, CW, G, STAGES>;
     static std::atomic<unsigned long long> prepared;
     const cudaError_t e = allow_smem(kernel, kMaxSmem, prepared);
     if (e != cudaSuccess) return e;
     const int steps = (a.k + S::kStageK - 1) / S::kStageK;
-    int stages = steps + 1 < kMaxStages ? steps + 1 : kMaxStages;
-    if (stages < 2) stages = 2;
-    while (stages > 2 && stages * S::bytes(a.m) > 100 * 1024) --stages;
-    int smem = stages * S::bytes(a.m);
+    const int tiles = (a.n + S::kCols - 1) / S::kCols;
+    int smem = STAGES * S::bytes(a.m);
     const int red = S::kKW * NT * 8 * (S::kCols + 1) * 4;
     if (smem < red) smem = red;
-    return launch_dependent(kernel, (a.n + S::kCols - 1) / S::kCols, kWarps * 32, smem, stream, a, stages);
+    // k split over a cluster while that leaves an SM for every block (1024x4096, one row:
+    // 3.4 us whole, 3.2 in 4, 4.3 in 8; 4096x4096, 48 rows: 36.8 whole, 13.7 in 4, 26.4 in 8)
+    int cluster = 1;
+    while (cluster < 8 && tiles * cluster * 2 <= sms && steps >= 2 * cluster) cluster *= 2;
+    return launch_dependent(kernel, tiles * cluster, kThreadsW4, smem, stream, cluster, a, cluster);
 }
 
-template <bool BF16, int NT, int MT, int CW>
-cudaError_t w4_launch_group(const W4Args& a, cudaStream_t stream)
+template <bool BF16, int NT, int MT, int CW, int STAGES>
+cudaError_t w4_launch_group(const W4Args& a, int sms, cudaStream_t stream)
 {
-    if (a.group == 32) return w4_launch_one<BF16, NT, MT, CW, 32>(a, stream);
-    if (a.group == 64) return w4_launch_one<BF16, NT, MT, CW, 64>(a, stream);
-    return w4_launch_one<BF16, NT, MT, CW, 128>(a, stream);
+    if (a.group == 32) return w4_launch_one<BF16, NT, MT, CW, 32, STAGES>(a, sms, stream);
+    if (a.group == 64) return w4_launch_one<BF16, NT, MT, CW, 64, STAGES>(a, sms, stream);
+    return w4_launch_one<BF16, NT, MT, CW, 128, STAGES>(a, sms, stream);
 }
 
 template <bool BF16>
-cudaError_t w4_launch_type(const W4Args& a, cudaStream_t stream)
+cudaError_t w4_launch_type(const W4Args& a, int sms, cudaStream_t stream)
 {
-    if (a.m <= 2) return w4_launch_group<BF16, 1, 1, 1>(a, stream);
-    if (a.m <= 8) return w4_launch_group<BF16, 1, 1, 2>(a, stream);
-    if (a.m <= 16) return w4_launch_group<BF16, 2, 1, 4>(a, stream);
-    if (a.m <= 32) return w4_launch_group<BF16, 4, 2, 4>(a, stream);
-    if (a.m <= 48) return w4_launch_group<BF16, 6, 2, 4>(a, stream);
-    return w4_launch_group<BF16, 8, 2, 4>(a, stream);
+    if (a.m <= 4) return w4_launch_group<BF16, 1, 2, 1, 4>(a, sms, stream);
+    if (a.m <= 8) return w4_launch_group<BF16, 1, 2, 1, 3>(a, sms, stream);
+    if (a.m <= 16) return w4_launch_group<BF16, 2, 1, 4, 4>(a, sms, stream);
+    if (a.m <= 32) return w4_launch_group<BF16, 4, 2, 4, 4>(a, sms, stream);
+    if (a.m <= 48) return w4_launch_group<BF16, 6, 2, 4, 3>(a, sms, stream);
+    return w4_launch_group<BF16, 8, 2, 4, 3>(a, sms, stream);
 }
 
 // A block writes 64 (k) x 64 (n) of B through shared memory.
@@ -376,16 +453,15 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const W4Args a)
 
 cudaError_t w4_matmul_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream)
 {
-    (void)sm_count;
-    return bf16 ? w4_launch_type<true>(a, stream) : w4_launch_type<false>(a, stream);
+    return bf16 ? w4_launch_type<true>(a, sm_count, stream) : w4_launch_type<false>(a, sm_count, stream);
 }
 
 cudaError_t w4_dequantize_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream)
 {
     (void)sm_count;
     const int grid = static_cast<int>(((a.n + 63) / 64) * static_cast<long long>((a.k + 63) / 64));
-    return bf16 ? launch_dependent(w4_dequantize_kernel<true>, grid, 256, 0, stream, a)
-                : launch_dependent(w4_dequantize_kernel<false>, grid, 256, 0, stream, a);
+    return bf16 ? launch_dependent(w4_dequantize_kernel<true>, grid, 256, 0, stream, 1, a)
+                : launch_dependent(w4_dequantize_kernel<false>, grid, 256, 0, stream, 1, a);
 }
 
 }  // namespace gemm_epi
