@@ -31,8 +31,23 @@ __device__ __forceinline__ uint4 philox(unsigned long long counter, uint32_t k0,
     return make_uint4(x0, x1, x2, x3);
 }
 
+constexpr int kThreads = 256;
+constexpr int kPerThread = 2;  // generator blocks (of 8 elements) per thread
+
+// A thread's 8 elements of generator block b, loaded; beyond the end zeros.
 template <bool BF16>
-__global__ void __launch_bounds__(256) dropout_kernel(const DropoutArgs a)
+__device__ __forceinline__ uint4 load_block(const uint16_t* p, long long b, long long count)
+{
+    if (b * 8 + 8 <= count) return *reinterpret_cast<const uint4*>(p + b * 8);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (b * 8 + j < count) w[j / 2] |= static_cast<uint32_t>(p[b * 8 + j]) << (j & 1 ? 16 : 0);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool BF16, bool RES>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs a)
 {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -40,46 +55,58 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutArgs a)
     const uint16_t* X = static_cast<const uint16_t*>(a.X);
     const uint16_t* R = static_cast<const uint16_t*>(a.residual);
     uint16_t* Y = static_cast<uint16_t*>(a.Y);
-    const long long blocks = (a.count + 7) / 8;
-    const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-    for (long long b = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; b < blocks; b += stride) {
-        const uint4 w = philox(offset + static_cast<unsigned long long>(b), a.key0, a.key1);
+    const long long first = static_cast<long long>(blockIdx.x) * (kThreads * kPerThread) + threadIdx.x;
+    uint4 x4[kPerThread], r4[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        x4[i] = load_block<BF16>(X, first + i * kThreads, a.count);
+        if (RES) r4[i] = load_block<BF16>(R, first + i * kThreads, a.count);
+    }
+    // a word's upper 16 bits are >= drop when the word is >= drop << 16, its lower 16 bits when
+    // the word shifted up is; drop = 65536 (keep nothing) is a threshold that zero words miss
+    const bool none = a.drop >= 65536u;
+    const uint32_t least = none ? 0xFFFFFFFFu : a.drop << 16;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const long long b = first + i * kThreads;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (!none) w = philox(offset + static_cast<unsigned long long>(b), a.key0, a.key1);
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-        const int left = static_cast<int>(min(8ll, a.count - b * 8));
-        float x[8], r[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (left == 8) {
-            decode8<BF16>(*reinterpret_cast<const uint4*>(X + b * 8), x);
-            if (R) decode8<BF16>(*reinterpret_cast<const uint4*>(R + b * 8), r);
-        } else {
-            for (int j = 0; j < 8; ++j) {
-                x[j] = j < left ? decode16<BF16>(X[b * 8 + j]) : 0.0f;
-                if (R && j < left) r[j] = decode16<BF16>(R[b * 8 + j]);
-            }
-        }
+        float x[8], r[8];
+        decode8<BF16>(x4[i], x);
+        if (RES) decode8<BF16>(r4[i], r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t u = j & 1 ? ww[j / 2] >> 16 : ww[j / 2] & 0xFFFFu;
-            const float y = u >= a.drop ? x[j] * a.scale : 0.0f;
-            x[j] = R ? y + r[j] : y;
+            const bool keep = (j & 1 ? ww[j / 2] : ww[j / 2] << 16) >= least;
+            const float y = keep ? x[j] * a.scale : 0.0f;
+            x[j] = RES ? y + r[j] : y;
         }
-        if (left == 8) {
-            *reinterpret_cast<uint4*>(Y + b * 8) = encode8<BF16>(x);
+        const uint4 y4 = encode8<BF16>(x);
+        if (b * 8 + 8 <= a.count) {
+            *reinterpret_cast<uint4*>(Y + b * 8) = y4;
         } else {
+            const uint32_t yy[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (j < left) Y[b * 8 + j] = encode16<BF16>(x[j]);
+                if (b * 8 + j < a.count) Y[b * 8 + j] = static_cast<uint16_t>(yy[j / 2] >> (j & 1 ? 16 : 0));
         }
     }
 }
 
+template <bool BF16, bool RES>
+cudaError_t dropout_launch_one(const DropoutArgs& a, cudaStream_t stream)
+{
+    const long long per_block = 8ll * kThreads * kPerThread;
+    return launch_dependent(dropout_kernel<BF16, RES>, static_cast<int>((a.count + per_block - 1) / per_block),
+                            kThreads, 0, stream, 1, a);  // (count <= 2^40: the grid fits)
+}
+
 }  // namespace
 
-cudaError_t dropout_launch(const DropoutArgs& a, bool bf16, int sm_count, cudaStream_t stream)
+cudaError_t dropout_launch(const DropoutArgs& a, bool bf16, cudaStream_t stream)
 {
-    const long long blocks = (a.count + 8 * 256 - 1) / (8 * 256);
-    const long long cap = static_cast<long long>(sm_count) * 8;
-    const int grid = static_cast<int>(blocks < cap ? blocks : cap);
-    return bf16 ? launch_dependent(dropout_kernel<true>, grid, 256, 0, stream, 1, a)
-                : launch_dependent(dropout_kernel<false>, grid, 256, 0, stream, 1, a);
+    if (a.residual) return bf16 ? dropout_launch_one<true, true>(a, stream) : dropout_launch_one<false, true>(a, stream);
+    return bf16 ? dropout_launch_one<true, false>(a, stream) : dropout_launch_one<false, false>(a, stream);
 }
 
 }  // namespace gemm_epi

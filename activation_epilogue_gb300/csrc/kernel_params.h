@@ -292,12 +292,12 @@ struct RmsnormBackwardArgs {
     const void* dH;
     void* dX;
     float* dgamma;
-    float* ws_dgamma;  // rmsnorm_backward_parts(t) rows of d partial sums
+    float* ws_mean;    // workspace: t means (rows too long for registers) ...
+    float* ws_dgamma;  // ... and rmsnorm_backward_parts(t, d) rows of d partial sums
     int t, d;
 };
 constexpr int kRmsMaxParts = 1024;
-constexpr int kRmsBackwardParts = 304;
-int rmsnorm_backward_parts(long long t);
+int rmsnorm_backward_parts(long long t, long long d);
 cudaError_t rmsnorm_launch(const RmsnormArgs& a, bool bf16, cudaStream_t stream);
 cudaError_t rmsnorm_backward_launch(const RmsnormBackwardArgs& a, bool bf16, cudaStream_t stream);
 
@@ -315,7 +315,7 @@ struct W4Args {
 };
 constexpr int kW4MaxM = 64;
 cudaError_t w4_matmul_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
-cudaError_t w4_dequantize_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
+cudaError_t w4_dequantize_launch(const W4Args& a, bool bf16, cudaStream_t stream);
 
 // Dropout (csrc/dropout.cu): an element is kept when its 16 random bits are >= drop.
 struct DropoutArgs {
@@ -329,6 +329,6 @@ struct DropoutArgs {
     uint32_t drop;
     float scale;
 };
-cudaError_t dropout_launch(const DropoutArgs& a, bool bf16, int sm_count, cudaStream_t stream);
+cudaError_t dropout_launch(const DropoutArgs& a, bool bf16, cudaStream_t stream);
 
 }  // namespace gemm_epi

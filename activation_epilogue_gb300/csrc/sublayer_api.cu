@@ -137,7 +137,8 @@ gemm_epi_status gemm_epi_rmsnorm_backward(int64_t t, int64_t d, gemm_epi_dtype d
     a.dH = dH;
     a.dX = dX;
     a.dgamma = dgamma;
-    a.ws_dgamma = static_cast<float*>(workspace);
+    a.ws_mean = static_cast<float*>(workspace);
+    a.ws_dgamma = a.ws_mean + round16(sizeof(float) * t) / sizeof(float);
     a.t = static_cast<int>(t);
     a.d = static_cast<int>(d);
     return launched(rmsnorm_backward_launch(a, dtype == GEMM_EPI_BF16, stream));
@@ -147,7 +148,7 @@ int64_t gemm_epi_rmsnorm_workspace(int64_t t, int64_t d)
 {
     if (!norm_shape_ok(t, d)) return 0;
     const int64_t forward = round16(sizeof(uint32_t) * kRmsMaxParts) + round16(sizeof(float) * t);
-    const int64_t backward = round16(sizeof(float) * rmsnorm_backward_parts(t) * d);
+    const int64_t backward = round16(sizeof(float) * t) + round16(sizeof(float) * rmsnorm_backward_parts(t, d) * d);
     return forward > backward ? forward : backward;
 }
 
@@ -211,7 +212,7 @@ gemm_epi_status gemm_epi_w4_dequantize(int64_t n, int64_t k, int64_t group,
     a.n = static_cast<int>(n);
     a.k = static_cast<int>(k);
     a.group = static_cast<int>(group);
-    return launched(w4_dequantize_launch(a, dtype == GEMM_EPI_BF16, sms, stream));
+    return launched(w4_dequantize_launch(a, dtype == GEMM_EPI_BF16, stream));
 }
 
 gemm_epi_status gemm_epi_dropout(int64_t count, gemm_epi_dtype dtype, const void* X,
@@ -239,7 +240,7 @@ gemm_epi_status gemm_epi_dropout(int64_t count, gemm_epi_dtype dtype, const void
     a.key1 = static_cast<uint32_t>(seed >> 32);
     a.drop = static_cast<uint32_t>(std::nearbyint(static_cast<double>(p) * 65536.0));
     a.scale = a.drop == 65536 ? 0.0f : static_cast<float>(65536.0 / (65536.0 - a.drop));
-    return launched(dropout_launch(a, dtype == GEMM_EPI_BF16, sms, stream));
+    return launched(dropout_launch(a, dtype == GEMM_EPI_BF16, stream));
 }
 
 }  // extern "C"

@@ -50,14 +50,6 @@ __device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void cp_async_wait_group()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr)
 {
     float v;
@@ -418,34 +410,72 @@ cudaError_t w4_launch_type(const W4Args& a, int sms, cudaStream_t stream)
     return w4_launch_group<BF16, 8, 2, 4, 3>(a, sms, stream);
 }
 
-// A block writes 64 (k) x 64 (n) of B through shared memory.
+// The weight written out: a block turns 128 (k) x 128 (n) of W, column by column in memory,
+// into rows of B.  A thread unpacks 32 values of k of two neighbouring columns, so that a
+// (k, two columns) word is one 4-byte store to shared memory; the words of a row are permuted
+// by 8 times the number of its 32 rows, which puts the four rows a warp stores to at a time in
+// different banks.  (q - z) is exact in 16 bits, and the 16-bit product with the scale is the
+// exact product rounded once.  Bound by B's bytes.
+constexpr int kDequantTile = 128;
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t mul16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    if constexpr (BF16)
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(256) w4_dequantize_kernel(const W4Args a)
 {
-    __shared__ uint16_t tile[64][66];
+    __shared__ uint32_t tile[kDequantTile][kDequantTile / 2];
+    const int n_tiles = (a.n + kDequantTile - 1) / kDequantTile;
+    const int n0 = blockIdx.x % n_tiles * kDequantTile, k0 = blockIdx.x / n_tiles * kDequantTile;
     grid_dependency_wait();
     grid_launch_dependents();
-    const uint16_t* S = static_cast<const uint16_t*>(a.scales);
-    const int k_tiles = (a.k + 63) / 64;
-    const int n0 = blockIdx.x / k_tiles * 64, k0 = blockIdx.x % k_tiles * 64;
-    for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-        const int col = n0 + i / 8, k = k0 + i % 8 * 8;
-        if (col >= a.n || k >= a.k) continue;
-        const uint32_t q = *reinterpret_cast<const uint32_t*>(
-            static_cast<const uint8_t*>(a.W) + (static_cast<long long>(col) * a.k + k) / 2);
-        const long long gi = static_cast<long long>(k / a.group) * a.n + col;
-        const float s = decode16<BF16>(S[gi]);
-        const int z = a.zeros ? a.zeros[gi] : 8;
+    const int t = threadIdx.x & 3, pair = threadIdx.x >> 2;
+    const int col = n0 + 2 * pair, k = k0 + 32 * t;
+    if (col < a.n && k < a.k) {  // (n is even, k a multiple of 32)
+        const uint8_t* src = static_cast<const uint8_t*>(a.W) + (static_cast<long long>(col) * a.k + k) / 2;
+        const uint4 w0 = __ldcs(reinterpret_cast<const uint4*>(src));
+        const uint4 w1 = __ldcs(reinterpret_cast<const uint4*>(src + a.k / 2));
+        const long long at = static_cast<long long>(k / a.group) * a.n + col;
+        const uint32_t s = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.scales) + at);
+        const uint32_t z = a.zeros ? *reinterpret_cast<const uint16_t*>(a.zeros + at) : 0x0808u;
+        const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
+        W4Unpack<BF16> u0, u1;
+        u0.set(z & 0xFFu);
+        u1.set(z >> 8);
+        const uint32_t ww0[4] = {w0.x, w0.y, w0.z, w0.w}, ww1[4] = {w1.x, w1.y, w1.z, w1.w};
+        const int at_word = pair ^ (8 * t);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            tile[k - k0 + j][col - n0] =
-                encode16<BF16>(static_cast<float>(static_cast<int>((q >> (4 * j)) & 15u) - z) * s);
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v0[4], v1[4];
+            u0(ww0[i], v0);
+            u1(ww1[i], v1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = mul16x2<BF16>(v0[j], s0), y = mul16x2<BF16>(v1[j], s1);
+                tile[32 * t + 8 * i + j][at_word] = __byte_perm(x, y, 0x5410);
+                tile[32 * t + 8 * i + j + 4][at_word] = __byte_perm(x, y, 0x7632);
+            }
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-        const int k = k0 + i / 64, col = n0 + i % 64;
-        if (k < a.k && col < a.n)
-            static_cast<uint16_t*>(a.D)[static_cast<long long>(k) * a.n + col] = tile[i / 64][i % 64];
+    const int c = threadIdx.x % 16 * 8;
+    if (n0 + c >= a.n) return;  // (n is a multiple of 8)
+    const int rows = min(kDequantTile, a.k - k0);
+    uint16_t* out = static_cast<uint16_t*>(a.D) + static_cast<long long>(k0) * a.n + n0 + c;
+#pragma unroll
+    for (int i = 0; i < kDequantTile / 16; ++i) {
+        const int row = i * 16 + threadIdx.x / 16;
+        if (row < rows)
+            *reinterpret_cast<uint4*>(out + static_cast<long long>(row) * a.n) =
+                *reinterpret_cast<const uint4*>(&tile[row][(c / 2) ^ (8 * (row / 32))]);
     }
 }
 
@@ -456,10 +486,10 @@ cudaError_t w4_matmul_launch(const W4Args& a, bool bf16, int sm_count, cudaStrea
     return bf16 ? w4_launch_type<true>(a, sm_count, stream) : w4_launch_type<false>(a, sm_count, stream);
 }
 
-cudaError_t w4_dequantize_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream)
+cudaError_t w4_dequantize_launch(const W4Args& a, bool bf16, cudaStream_t stream)
 {
-    (void)sm_count;
-    const int grid = static_cast<int>(((a.n + 63) / 64) * static_cast<long long>((a.k + 63) / 64));
+    const long long n_tiles = (a.n + kDequantTile - 1) / kDequantTile, k_tiles = (a.k + kDequantTile - 1) / kDequantTile;
+    const int grid = static_cast<int>(n_tiles * k_tiles);  // (n k <= 2^40: at most 2^26 and the edges)
     return bf16 ? launch_dependent(w4_dequantize_kernel<true>, grid, 256, 0, stream, 1, a)
                 : launch_dependent(w4_dequantize_kernel<false>, grid, 256, 0, stream, 1, a);
 }
