@@ -23,6 +23,7 @@
 #include "launch.h"
 #include "ptx.cuh"
 #include "vec16.cuh"
+#include "w4_unpack.cuh"
 
 namespace gemm_epi {
 
@@ -32,30 +33,6 @@ constexpr int kWarps = 8;
 constexpr int kThreadsW4 = kWarps * 32;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kBlockK = 128;  // values of k per warp and stage: 64 bytes of each row of W
-
-// The epilogue of one element, from the exact functions (a few elements per thread).
-__device__ __forceinline__ float w4_epilogue(float v, int epilog, float residual)
-{
-    switch (epilog) {
-    case EPI_RELU_BIAS: return v > 0.0f || v != v ? v : 0.0f;
-    case EPI_GELU_BIAS: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    case EPI_TANH_BIAS: return tanhf(v);
-    case EPI_BIAS_RESIDUAL: return v + residual;
-    default: return v;
-    }
-}
-
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr)
 {
@@ -80,60 +57,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-// (a & b) | c in one instruction (left to itself the compiler takes two where b and c are both
-// constants).
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c)
-{
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t sub16x2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    if constexpr (BF16)
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    else
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// What turns a word of W into values: the bits that a pair's nibbles are set in, and with the
-// zero points z of the column, what to subtract.
-//   bf16 (7 bits of mantissa): nibble in bits 0-3 under 128's bits is 128 + q.
-//   f16 (10 bits): nibble in bits 0-3 under 1024's bits is 1024 + q, in bits 4-7 under 64's
-//   bits 64 + q, so two pairs come of each shift.
-template <bool BF16>
-struct W4Unpack {
-    uint32_t sub_even, sub_odd;  // of pairs 0, 2 and 1, 3
-    __device__ __forceinline__ void set(uint32_t z)
-    {
-        if constexpr (BF16) {
-            sub_even = sub_odd = z * 0x10001u + 0x43004300u;
-        } else {
-            sub_even = z * 0x10001u + 0x64006400u;
-            sub_odd = z * 0x100010u + 0x54005400u;
-        }
-    }
-    // v[j]: q - z of nibbles j (lower half) and j + 4, exactly
-    __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&v)[4]) const
-    {
-        if constexpr (BF16) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = sub16x2<true>(and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u), sub_even);
-        } else {
-            const uint32_t h = w >> 8;
-            v[0] = sub16x2<false>(and_or(w, 0x000F000Fu, 0x64006400u), sub_even);
-            v[1] = sub16x2<false>(and_or(w, 0x00F000F0u, 0x54005400u), sub_odd);
-            v[2] = sub16x2<false>(and_or(h, 0x000F000Fu, 0x64006400u), sub_even);
-            v[3] = sub16x2<false>(and_or(h, 0x00F000F0u, 0x54005400u), sub_odd);
-        }
-    }
-};
 
 // One stage in shared memory for m rows of A, in bytes.  Rows are padded so that eight rows'
 // 16-byte pieces (ldmatrix), or two rows' 64 bytes (rows of A), fall in different banks.
@@ -404,10 +327,11 @@ cudaError_t w4_launch_type(const W4Args& a, int sms, cudaStream_t stream)
 {
     if (a.m <= 4) return w4_launch_group<BF16, 1, 2, 1, 4>(a, sms, stream);
     if (a.m <= 8) return w4_launch_group<BF16, 1, 2, 1, 3>(a, sms, stream);
-    if (a.m <= 16) return w4_launch_group<BF16, 2, 1, 4, 4>(a, sms, stream);
-    if (a.m <= 32) return w4_launch_group<BF16, 4, 2, 4, 4>(a, sms, stream);
-    if (a.m <= 48) return w4_launch_group<BF16, 6, 2, 4, 3>(a, sms, stream);
-    return w4_launch_group<BF16, 8, 2, 4, 3>(a, sms, stream);
+    // 9 to 16 rows: this kernel's second tile of rows costs a small weight less than tcgen05's
+    // longer start (4096x1024: 4.4 us here, 6.0 there), a large one more (8192x8192: 26.8, 18.4)
+    if (a.m <= 16 && static_cast<long long>(a.n) * a.k <= 12ll << 20)
+        return w4_launch_group<BF16, 2, 1, 4, 4>(a, sms, stream);
+    return w4_tensor_launch(a, BF16, sms, stream);
 }
 
 // The weight written out: a block turns 128 (k) x 128 (n) of W, column by column in memory,

@@ -1,0 +1,481 @@
+// Products with 4-bit weights for 9 to 64 rows of A, on tcgen05: D^T = W A^T with 128 columns of
+// D as the MMA's rows and the rows of A as its columns.
+//
+// mma.sync takes 16 cycles for 16 x 8 x 16 on this part, an eighth of tcgen05's rate, so that
+// from two 8-row tiles of A on it, and not the weight's bytes, bounds a product (16384x8192,
+// 48 rows: 72 us; this kernel's figures stand at its launch).  tcgen05 reads its first operand from
+// tensor memory, where a thread's lane is the MMA's row: the thread that unpacks a row of W
+// writes it there with tcgen05.st, and the unpacked weight never passes through shared memory
+// (whose bandwidth it would exhaust: 128 x 128 values written and read again are 512 cycles of
+// it, the block's share of the weight's bytes 370).
+//
+//   * The producer (one thread) copies blocks of 128 k of A by TMA (128-byte swizzle, rows past
+//     m and k past the end read as zeros).
+//   * Two chains take every second block each, with two of four blocks of tensor memory, two of
+//     four accumulators and an issuing thread of their own.  (One issuer's own instructions
+//     took 1300 cycles a block, nearly all of a call: 48 us for 16384x8192 with 48 rows.)
+//   * A chain's four unpacking warps have a quarter of the 128 rows each: a block's 2 KB of a
+//     quarter come through a ring of the warp's own in shared memory (cp.async, no barrier but
+//     the warp's), each thread unpacks its row's 64 bytes to q - z, exactly, two neighbouring k
+//     per 32-bit word, and stores them to tensor memory.
+//   * The chain's issuer runs the MMAs of one group of the scales after another.
+//   * Four warps read the groups' sums, of both chains in turn, multiply them by the group's
+//     scales (one per lane: the lane is the column of D) and add them up in fp32, two rows of A
+//     per instruction; at the end all threads apply the epilogue and store D.
+// A chain's waits are for its own earlier blocks alone, in order, so that no wait can take an
+// older phase of a barrier for the one it needs.
+#include "kernel_params.h"
+#include "launch.h"
+#include "plan.h"
+#include "ptx.cuh"
+#include "w4_unpack.cuh"
+
+namespace gemm_epi {
+
+namespace {
+
+constexpr int kCols = 128;                  // columns of D per block: MMA rows
+constexpr int kBlockK = 128;                // k per block of the pipeline
+constexpr int kSumWarps = 4;                // warps 0-3
+constexpr int kChains = 2;
+constexpr int kUnpackWarps = 4 * kChains;   // warps 4-11
+constexpr int kProducerWarp = kSumWarps + kUnpackWarps;
+constexpr int kIssuerWarp = kProducerWarp + 1;  // and the next
+constexpr int kThreads = 32 * (kIssuerWarp + kChains);
+constexpr int kWDepth = 6;                  // blocks in flight per unpacking warp
+constexpr int kASlots = 2 * kChains;        // blocks of unpacked weight in tensor memory
+constexpr int kAcc = 2 * kChains;           // accumulators
+constexpr int kMaxBSlots = 8;               // blocks of A in shared memory (most)
+constexpr int kScaleDepth = 8;              // pairs of blocks' scales in flight per summing warp
+constexpr int kTmemA = 0, kTmemAcc = 256;   // columns of tensor memory; 512 allocated
+
+// barriers (8 bytes each), then the tensor memory address and the failure flag
+enum : int {
+    kAFull = 0,
+    kAEmpty = kAFull + kASlots,
+    kBFull = kAEmpty + kASlots,
+    kBEmpty = kBFull + kMaxBSlots,
+    kAccFull = kBEmpty + kMaxBSlots,
+    kAccEmpty = kAccFull + kAcc,
+    kDrain = kAccEmpty + kAcc,
+    kBars = kDrain + kChains
+};
+constexpr int kHeader = 512;
+static_assert(kBars * 8 + 8 <= kHeader, "header");
+
+// Shared memory: blocks of A, a ring of each unpacking warp (32 rows' 64 bytes of W, and the
+// groups' zero points), a ring of each summing warp (the groups' scales of its 32 columns).
+template <int NP, int G>
+struct Layout {
+    static constexpr int kGroups = kBlockK / G;
+    static constexpr int kB = NP * kBlockK * 2;
+    static constexpr int kBSlots = NP == 64 ? 6 : kMaxBSlots;
+    static constexpr int kWSlot = 32 * 64 + kGroups * 32;
+    static constexpr int kSSlot = kChains * kGroups * 64;
+    static constexpr int kOffW = kBSlots * kB;
+    static constexpr int kOffS = kOffW + kUnpackWarps * kWDepth * kWSlot;
+    static constexpr int kOffBar = kOffS + kSumWarps * kScaleDepth * kSSlot;
+    static constexpr int kBytes = 1024 + kOffBar + kHeader;  // (1024: alignment)
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+    static_assert(kOffBar >= NP * kCols * 4, "the sums fit the rings");
+};
+
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Store 16 words of this thread's lane (no wait).
+__device__ __forceinline__ void tmem_store_16cols_async(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        :
+        : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+          "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+          "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// (x, y) += (a, b) * s
+__device__ __forceinline__ void fma2(float& x, float& y, uint32_t a, uint32_t b, float s)
+{
+    unsigned long long acc, v, ss;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(ss));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(acc));
+}
+
+
+template <bool BF16, int NP, int G>
+__global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_constant__ W4Args a,
+                                                                const __grid_constant__ CUtensorMap tm_A,
+                                                                int cluster)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const uint32_t sbase = smem_u32(smem);
+    using L = Layout<NP, G>;
+    constexpr int kB = L::kB, kBSlots = L::kBSlots;
+    constexpr int kGroups = L::kGroups;  // per block
+    const uint32_t bar0 = sbase + L::kOffBar;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(smem + L::kOffBar + kBars * 8);
+    volatile int* failed = reinterpret_cast<volatile int*>(holder + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(blockIdx.x) % cluster;
+    const int n0 = static_cast<int>(blockIdx.x) / cluster * kCols;
+    const int all_blocks = (a.k + kBlockK - 1) / kBlockK;
+    const int first = static_cast<int>(static_cast<long long>(all_blocks) * rank / cluster);
+    const int blocks = static_cast<int>(static_cast<long long>(all_blocks) * (rank + 1) / cluster) - first;
+    const int groups = min(blocks * kGroups, a.k / G - first * kGroups);  // of this block's part of k
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kASlots; ++i) {
+            mbar_init(bar0 + 8 * (kAFull + i), 4);
+            mbar_init(bar0 + 8 * (kAEmpty + i), 1);
+        }
+        for (int i = 0; i < kBSlots; ++i) {
+            mbar_init(bar0 + 8 * (kBFull + i), 1);
+            mbar_init(bar0 + 8 * (kBEmpty + i), 1);
+        }
+        for (int i = 0; i < kAcc; ++i) {
+            mbar_init(bar0 + 8 * (kAccFull + i), 1);
+            mbar_init(bar0 + 8 * (kAccEmpty + i), kSumWarps);
+        }
+        for (int i = 0; i < kChains; ++i) mbar_init(bar0 + 8 * (kDrain + i), 1);
+        *failed = 0;
+        fence_mbar_init();
+    }
+    if (warp == kIssuerWarp) {
+        tmem_alloc(smem_u32(holder), 512);
+        tmem_relinquish_alloc_permit();
+    }
+    if (warp == kProducerWarp && lane == 0 && blocks > 0) prefetch_tensormap(&tm_A);
+    tcgen05_fence_before_sync();
+    __syncthreads();
+    tcgen05_fence_after_sync();
+    const uint32_t tmem = *holder;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    float total[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) total[j] = 0.0f;
+
+    if (warp == kProducerWarp) {
+        if (lane == 0) {
+            int issued = 0;
+            for (int i = 0; i < blocks; ++i) {
+                const int slot = i % kBSlots;
+                if (!w4_wait(bar0 + 8 * (kBEmpty + slot), (i / kBSlots & 1) ^ 1, failed)) break;
+                const uint32_t full = bar0 + 8 * (kBFull + slot);
+                mbar_arrive_expect_tx(full, kB);
+                tma_load_2d(sbase + slot * kB, &tm_A, full, (first + i) * kBlockK, 0);
+                tma_load_2d(sbase + slot * kB + kB / 2, &tm_A, full, (first + i) * kBlockK + 64, 0);
+                ++issued;
+            }
+            if (*failed) {
+                // the copies on their way land before the block's shared memory is given back
+                for (int i = max(0, issued - kBSlots); i < issued; ++i)
+                    w4_drain(bar0 + 8 * (kBFull + i % kBSlots), i / kBSlots & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kIssuerWarp) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = make_idesc_f16(BF16 ? 1u : 0u, 0u, 0u, kCols, NP);
+            bool issued = false;
+            const uint64_t desc0 = make_sdesc_sw128(sbase, 0, 1024);
+            const int chain = warp - kIssuerWarp;
+            int last = -1, n = 0;  // n: groups of this chain so far
+            int bs = chain, a_phase = 0, b_phase = 0;
+            uint32_t half = 0;  // which of the chain's two blocks of tensor memory
+            for (int i = chain; i < blocks; i += kChains) {
+                const uint32_t as = chain + kChains * half;
+                if (!w4_wait(bar0 + 8 * (kAFull + as), a_phase, failed) ||
+                    !w4_wait(bar0 + 8 * (kBFull + bs), b_phase, failed))
+                    break;
+                const uint64_t desc = desc0 + static_cast<uint32_t>(bs * kB >> 4);
+                const uint32_t a_tmem = tmem + kTmemA + as * 64;
+                bool ok = true;
+#pragma unroll
+                for (int q = 0; q < kGroups; ++q) {
+                    if (i * kGroups + q >= groups) break;
+                    const int acc = chain + kChains * (n & 1);
+                    if (!w4_wait(bar0 + 8 * (kAccEmpty + acc), (n >> 1 & 1) ^ 1, failed)) {
+                        ok = false;
+                        break;
+                    }
+                    tcgen05_fence_after_sync();
+                    const uint32_t d_tmem = tmem + kTmemAcc + acc * 64;
+#pragma unroll
+                    for (int s = 0; s < G / 16; ++s) {
+                        const int k16 = q * (G / 16) + s;  // 16 k within the block
+                        mma_f16_ts(d_tmem, a_tmem + k16 * 8, desc + ((k16 / 4 * (kB / 2) + k16 % 4 * 32) >> 4),
+                                   idesc, s > 0);
+                    }
+                    issued = true;
+                    mma_commit(bar0 + 8 * (kAccFull + acc));
+                    ++n;
+                }
+                if (!ok) break;
+                mma_commit(bar0 + 8 * (kAEmpty + as));
+                mma_commit(bar0 + 8 * (kBEmpty + bs));
+                last = i;
+                half ^= 1;
+                if (half == 0) a_phase ^= 1;
+                bs += kChains;
+                if (bs >= kBSlots) {
+                    bs -= kBSlots;
+                    b_phase ^= 1;
+                }
+            }
+            // (the last commits arrive before the block leaves)
+            if (last >= 0 && !*failed) w4_wait(bar0 + 8 * (kBEmpty + last % kBSlots), last / kBSlots & 1, failed);
+            if (*failed && issued) {
+                // every MMA issued completes before tensor memory is released
+                mma_commit(bar0 + 8 * (kDrain + chain));
+                w4_drain(bar0 + 8 * (kDrain + chain), 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kSumWarps) {
+        // ---- unpacking: this warp's quarter (its tensor memory lanes) of its chain's blocks ----
+        const int quarter = warp & 3, part = (warp - kSumWarps) >> 2;
+        const int ring = L::kOffW + (warp - kSumWarps) * (kWDepth * L::kWSlot);
+        // copies: 16-byte chunk lane % 4 of rows lane / 4 + 8 j; 8 zero points of one group
+        const int crow = lane >> 2, chunk = lane & 3;
+        const uint8_t* src[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            src[j] = static_cast<const uint8_t*>(a.W) +
+                     (static_cast<long long>(min(n0 + quarter * 32 + crow + 8 * j, a.n - 1)) * a.k +
+                      static_cast<long long>(first + part) * kBlockK) / 2 + chunk * 16;
+        const uint32_t dst = crow * 64 + ((chunk ^ ((crow >> 1) & 3)) << 4);  // (+ 8 rows: + 512)
+        const int k_first = (first + part) * kBlockK;
+        int k_left = a.k - k_first;
+        const int zgroup = lane >> 2, zcol = (lane & 3) * 8;
+        const bool copies_zeros = a.zeros != nullptr && zgroup < kGroups && n0 + quarter * 32 + zcol < a.n;
+        const uint8_t* zsrc = a.zeros + static_cast<long long>(k_first / G + zgroup) * a.n + n0 + quarter * 32 + zcol;
+        const long long z_step = static_cast<long long>(kChains * kGroups) * a.n;
+        const int mine = blocks > part ? (blocks - part + kChains - 1) / kChains : 0;
+        auto fetch = [&](int slot) {
+            const uint32_t to = sbase + ring + slot * L::kWSlot;
+            if (chunk * 32 < k_left) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cp_async_16(to + dst + j * 512, src[j]);
+            }
+            if (copies_zeros && zgroup * G < k_left) cp_async_8(to + 2048 + zgroup * 32 + zcol, zsrc);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) src[j] += kChains * kBlockK / 2;
+            zsrc += z_step;
+            k_left -= kChains * kBlockK;
+        };
+#pragma unroll
+        for (int j = 0; j < kWDepth - 1; ++j) {
+            if (j < mine) fetch(j);
+            cp_async_commit();
+        }
+        const uint32_t t_lane = tmem + kTmemA + (static_cast<uint32_t>(quarter * 32) << 16);
+        for (int b = 0; b < mine; ++b) {
+            if (b + kWDepth - 1 < mine) fetch((b + kWDepth - 1) % kWDepth);
+            cp_async_commit();
+            cp_async_wait_group<kWDepth - 1>();
+            __syncwarp();
+            const uint8_t* slot = smem + ring + (b % kWDepth) * L::kWSlot;
+            const uint8_t* mem = slot + lane * 64;
+            const int as = part + kChains * (b & 1);
+            if (!w4_wait(bar0 + 8 * (kAEmpty + as), (b >> 1 & 1) ^ 1, failed)) break;
+            tcgen05_fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint4 w4 = *reinterpret_cast<const uint4*>(mem + ((c ^ ((lane >> 1) & 3)) << 4));
+                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                W4UnpackInOrder<BF16> unpack;
+                unpack.set(a.zeros ? slot[2048 + c * 32 / G * 32 + lane] : 8u);
+                uint32_t v[16];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) unpack(w[j], v + 4 * j);
+                tmem_store_16cols_async(t_lane + as * 64 + c * 16, v);
+            }
+            tmem_wait_st();
+            tcgen05_fence_before_sync();
+            __syncwarp();  // (also: the slot is read before its next copy is issued)
+            if (lane == 0) mbar_arrive(bar0 + 8 * (kAFull + as));
+        }
+        cp_async_wait_group<0>();
+    } else {
+        // ---- the groups' sums, scaled and added ----
+        const int ring = L::kOffS + warp * (kScaleDepth * L::kSSlot);
+        const int sgroup = lane >> 2, scol = (lane & 3) * 8;
+        const bool copies = sgroup < kChains * kGroups && n0 + warp * 32 + scol < a.n;
+        const uint16_t* src = static_cast<const uint16_t*>(a.scales) +
+                              static_cast<long long>(first * kGroups + sgroup) * a.n + n0 + warp * 32 + scol;
+        const long long s_step = static_cast<long long>(kChains * kGroups) * a.n;
+        const int pairs = (blocks + kChains - 1) / kChains;
+        int left = groups;  // from the next pair of blocks to copy on
+        auto fetch = [&](int slot) {
+            if (copies && sgroup < left)
+                cp_async_16(sbase + ring + slot * L::kSSlot + sgroup * 64 + scol * 2, src);
+            src += s_step;
+            left -= kChains * kGroups;
+        };
+#pragma unroll
+        for (int j = 0; j < kScaleDepth - 1; ++j) {
+            if (j < pairs) fetch(j);
+            cp_async_commit();
+        }
+        const uint32_t t_lane = tmem + kTmemAcc + (static_cast<uint32_t>(warp * 32) << 16);
+        for (int i = 0; i < pairs; ++i) {
+            if (i + kScaleDepth - 1 < pairs) fetch((i + kScaleDepth - 1) % kScaleDepth);
+            cp_async_commit();
+            cp_async_wait_group<kScaleDepth - 1>();
+            __syncwarp();
+            const uint16_t* scales = reinterpret_cast<const uint16_t*>(smem + ring + (i % kScaleDepth) * L::kSSlot) + lane;
+            bool ok = true;
+#pragma unroll
+            for (int p = 0; p < kChains * kGroups; ++p) {
+                const int chain = p % kChains;              // the chains in turn
+                const int in_pair = chain * kGroups + p / kChains;  // group within the pair of blocks
+                if (i * kChains * kGroups + in_pair >= groups) continue;
+                const int n = i * kGroups + p / kChains;    // of the chain
+                const int q = chain + kChains * (n & 1);
+                const float sc = decode16<BF16>(scales[in_pair * 32]);
+                if (!w4_wait(bar0 + 8 * (kAccFull + q), n >> 1 & 1, failed)) {
+                    ok = false;
+                    break;
+                }
+                tcgen05_fence_after_sync();
+                uint32_t r[2][16];
+                tmem_load_16cols_async(t_lane + q * 64, r[0]);
+#pragma unroll
+                for (int j = 0; j < NP / 16; ++j) {
+                    tmem_wait_ld(r[j & 1]);
+                    if (j + 1 < NP / 16) {
+                        tmem_load_16cols_async(t_lane + q * 64 + (j + 1) * 16, r[(j + 1) & 1]);
+                    } else {
+                        tcgen05_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar0 + 8 * (kAccEmpty + q));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2)
+                        fma2(total[j * 16 + e], total[j * 16 + e + 1], r[j & 1][e], r[j & 1][e + 1], sc);
+                }
+            }
+            if (!ok) break;
+            __syncwarp();  // the slot is read before its next copy is issued
+        }
+        cp_async_wait_group<0>();
+    }
+
+    tcgen05_fence_before_sync();
+    __syncthreads();
+    if (warp == kIssuerWarp) {
+        tcgen05_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+    // The sums as [row][column] in shared memory, then the epilogue in a loop over all threads (one
+    // copy of its code: unrolled over the rows it took 8 us a call to fetch).  With k split over a
+    // cluster, block r of it takes every cluster-th element and adds the blocks' sums in order.
+    float* red = reinterpret_cast<float*>(smem);
+    if (warp < kSumWarps) {
+        const bool gave_up = *failed != 0;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) red[j * kCols + threadIdx.x] = gave_up ? __int_as_float(0x7FC00000) : total[j];
+    }
+    if (cluster > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    // a thread has two neighbouring columns of rows first_row, first_row + step, ...
+    constexpr int kRowsAtOnce = kThreads / (kCols / 2);
+    const int c2 = threadIdx.x % (kCols / 2) * 2, col = n0 + c2;
+    const int first_row = static_cast<int>(threadIdx.x) / (kCols / 2) + rank * kRowsAtOnce;
+    if (threadIdx.x < kRowsAtOnce * (kCols / 2) && col < a.n) {  // (n is even)
+        float2 bias = make_float2(0.0f, 0.0f);
+        if (a.bias) {
+            const uint16_t* p = static_cast<const uint16_t*>(a.bias) + col;
+            bias = make_float2(decode16<BF16>(p[0]), decode16<BF16>(p[1]));
+        }
+#pragma unroll 2
+        for (int row = first_row; row < a.m; row += cluster * kRowsAtOnce) {
+            float2 v = make_float2(0.0f, 0.0f);
+            const int at_red = row * kCols + c2;
+            if (cluster == 1) {
+                v = *reinterpret_cast<const float2*>(red + at_red);
+            } else {
+                for (int q = 0; q < cluster; ++q) {
+                    const float2 w = ld_shared_cluster_f32x2(map_shared_rank(sbase + at_red * 4, q));
+                    v.x += w.x;
+                    v.y += w.y;
+                }
+            }
+            const long long at = static_cast<long long>(row) * a.n + col;
+            float2 res = make_float2(0.0f, 0.0f);
+            if (a.residual) res = decode16x2<BF16>(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.residual) + at));
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.D) + at) =
+                encode16x2<BF16>(w4_epilogue(v.x + bias.x, a.epilog, res.x), w4_epilogue(v.y + bias.y, a.epilog, res.y));
+        }
+    }
+    if (cluster > 1) cluster_sync_all();  // the peers' shared memory stays until it is read
+}
+
+template <bool BF16, int NP, int G>
+cudaError_t launch_one(const W4Args& a, const CUtensorMap& map, int sms, cudaStream_t stream)
+{
+    auto kernel = w4_tensor_kernel<BF16, NP, G>;
+    static std::atomic<unsigned long long> prepared;
+    const cudaError_t e = allow_smem(kernel, Layout<NP, G>::kBytes, prepared);
+    if (e != cudaSuccess) return e;
+    const int tiles = (a.n + kCols - 1) / kCols, blocks = (a.k + kBlockK - 1) / kBlockK;
+    int cluster = sms / tiles;
+    if (cluster > 8) cluster = 8;
+    if (cluster > blocks / 4) cluster = blocks / 4;
+    if (cluster < 1) cluster = 1;
+    return launch_dependent(kernel, tiles * cluster, kThreads, Layout<NP, G>::kBytes, stream, cluster, a, map, cluster);
+}
+
+template <bool BF16, int NP>
+cudaError_t launch_group(const W4Args& a, const CUtensorMap& map, int sms, cudaStream_t stream)
+{
+    if (a.group == 32) return launch_one<BF16, NP, 32>(a, map, sms, stream);
+    if (a.group == 64) return launch_one<BF16, NP, 64>(a, map, sms, stream);
+    return launch_one<BF16, NP, 128>(a, map, sms, stream);
+}
+
+template <bool BF16>
+cudaError_t launch_type(const W4Args& a, const CUtensorMap& map, int sms, cudaStream_t stream)
+{
+    if (a.m <= 16) return launch_group<BF16, 16>(a, map, sms, stream);
+    if (a.m <= 32) return launch_group<BF16, 32>(a, map, sms, stream);
+    if (a.m <= 48) return launch_group<BF16, 48>(a, map, sms, stream);
+    return launch_group<BF16, 64>(a, map, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t w4_tensor_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream)
+{
+    CUtensorMap map = {};
+    const uint32_t rows = static_cast<uint32_t>((a.m + 15) / 16 * 16);
+    if (a.k > 0 &&
+        !gemm_epi_impl::encode_2d(&map, a.A, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                  static_cast<uint64_t>(a.k), static_cast<uint64_t>(a.m), 64, rows,
+                                  CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    return bf16 ? launch_type<true>(a, map, sm_count, stream) : launch_type<false>(a, map, sm_count, stream);
+}
+
+}  // namespace gemm_epi
