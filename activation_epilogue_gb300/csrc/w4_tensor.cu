@@ -11,19 +11,25 @@
 //
 //   * The producer (one thread) copies blocks of 128 k of A by TMA (128-byte swizzle, rows past
 //     m and k past the end read as zeros).
-//   * Two chains take every second block each, with two of four blocks of tensor memory, two of
-//     four accumulators and an issuing thread of their own.  (One issuer's own instructions
-//     took 1300 cycles a block, nearly all of a call: 48 us for 16384x8192 with 48 rows.)
+//   * Four chains take every fourth block each, with a block of tensor memory (two halves), one
+//     or two accumulators and an issuing thread of their own.  (One issuer's own instructions
+//     took 1300 cycles a block, nearly all of a call: 48 us for 16384x8192 with 48 rows; two
+//     chains 31 us, four 26.6.)
 //   * A chain's four unpacking warps have a quarter of the 128 rows each: a block's 2 KB of a
 //     quarter come through a ring of the warp's own in shared memory (cp.async, no barrier but
 //     the warp's), each thread unpacks its row's 64 bytes to q - z, exactly, two neighbouring k
-//     per 32-bit word, and stores them to tensor memory.
+//     per 32-bit word, and stores them to tensor memory, half a block at a time.
 //   * The chain's issuer runs the MMAs of one group of the scales after another.
-//   * Four warps read the groups' sums, of both chains in turn, multiply them by the group's
-//     scales (one per lane: the lane is the column of D) and add them up in fp32, two rows of A
-//     per instruction; at the end all threads apply the epilogue and store D.
+//   * Eight warps (a quarter of the lanes, half of the rows of A each) read the groups' sums, of
+//     the chains in turn, multiply them by the group's scales (one per lane: the lane is the
+//     column of D) and add them up in fp32, two rows of A per instruction; at the end all
+//     threads apply the epilogue and store D.
 // A chain's waits are for its own earlier blocks alone, in order, so that no wait can take an
 // older phase of a barrier for the one it needs.
+// Measured (16384x8192, bf16, 48 rows): 26.6 us with groups of 128, 32 with 64, 46 with 32
+// (a group's hand-over from the issuer to the summing warps costs more than its MMAs); about
+// 6 us of each is start and end (4096x1024: 6.4 us), the rest 630 cycles a block of 128 x 128
+// against some 370 for the unpacking instructions alone and for the weight's bytes.
 #include "kernel_params.h"
 #include "launch.h"
 #include "plan.h"
@@ -36,28 +42,28 @@ namespace {
 
 constexpr int kCols = 128;                  // columns of D per block: MMA rows
 constexpr int kBlockK = 128;                // k per block of the pipeline
-constexpr int kSumWarps = 4;                // warps 0-3
-constexpr int kChains = 2;
-constexpr int kUnpackWarps = 4 * kChains;   // warps 4-11
+constexpr int kChains = 4;
+constexpr int kSumWarps = 8;                // warps 0-7: a quarter of the lanes, half of the rows of A
+constexpr int kUnpackWarps = 4 * kChains;   // warps 8-23: a quarter of the lanes of one chain
 constexpr int kProducerWarp = kSumWarps + kUnpackWarps;
-constexpr int kIssuerWarp = kProducerWarp + 1;  // and the next
+constexpr int kIssuerWarp = kProducerWarp + 1;  // warps 25-28, one thread each
 constexpr int kThreads = 32 * (kIssuerWarp + kChains);
-constexpr int kWDepth = 6;                  // blocks in flight per unpacking warp
-constexpr int kASlots = 2 * kChains;        // blocks of unpacked weight in tensor memory
-constexpr int kAcc = 2 * kChains;           // accumulators
+constexpr int kWDepth = 3;                  // blocks in flight per unpacking warp
+constexpr int kHalves = 2 * kChains;        // half blocks (64 k) of unpacked weight in tensor memory
+constexpr int kMaxAcc = 2 * kChains;        // accumulators
 constexpr int kMaxBSlots = 8;               // blocks of A in shared memory (most)
-constexpr int kScaleDepth = 8;              // pairs of blocks' scales in flight per summing warp
+constexpr int kScaleDepth = 3;              // rounds of the chains' scales in flight per summing warp
 constexpr int kTmemA = 0, kTmemAcc = 256;   // columns of tensor memory; 512 allocated
 
 // barriers (8 bytes each), then the tensor memory address and the failure flag
 enum : int {
     kAFull = 0,
-    kAEmpty = kAFull + kASlots,
-    kBFull = kAEmpty + kASlots,
+    kAEmpty = kAFull + kHalves,
+    kBFull = kAEmpty + kHalves,
     kBEmpty = kBFull + kMaxBSlots,
     kAccFull = kBEmpty + kMaxBSlots,
-    kAccEmpty = kAccFull + kAcc,
-    kDrain = kAccEmpty + kAcc,
+    kAccEmpty = kAccFull + kMaxAcc,
+    kDrain = kAccEmpty + kMaxAcc,
     kBars = kDrain + kChains
 };
 constexpr int kHeader = 512;
@@ -69,7 +75,9 @@ template <int NP, int G>
 struct Layout {
     static constexpr int kGroups = kBlockK / G;
     static constexpr int kB = NP * kBlockK * 2;
-    static constexpr int kBSlots = NP == 64 ? 6 : kMaxBSlots;
+    static constexpr int kBSlots = NP == 64 ? 4 : kMaxBSlots;  // (a multiple of the chains)
+    static constexpr int kAccPer = NP <= 32 ? 2 : 1;           // accumulators of a chain
+    static constexpr int kAccCols = 64 / kAccPer;
     static constexpr int kWSlot = 32 * 64 + kGroups * 32;
     static constexpr int kSSlot = kChains * kGroups * 64;
     static constexpr int kOffW = kBSlots * kB;
@@ -106,6 +114,23 @@ __device__ __forceinline__ void tmem_store_16cols_async(uint32_t taddr, const ui
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Start loading 8 columns of this thread's lane; valid after tmem_wait_ld8 on them.
+__device__ __forceinline__ void tmem_load_8cols_async(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld8(uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+
 // (x, y) += (a, b) * s
 __device__ __forceinline__ void fma2(float& x, float& y, uint32_t a, uint32_t b, float s)
 {
@@ -141,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
     const int groups = min(blocks * kGroups, a.k / G - first * kGroups);  // of this block's part of k
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kASlots; ++i) {
+        for (int i = 0; i < kHalves; ++i) {
             mbar_init(bar0 + 8 * (kAFull + i), 4);
             mbar_init(bar0 + 8 * (kAEmpty + i), 1);
         }
@@ -149,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
             mbar_init(bar0 + 8 * (kBFull + i), 1);
             mbar_init(bar0 + 8 * (kBEmpty + i), 1);
         }
-        for (int i = 0; i < kAcc; ++i) {
+        for (int i = 0; i < kMaxAcc; ++i) {
             mbar_init(bar0 + 8 * (kAccFull + i), 1);
             mbar_init(bar0 + 8 * (kAccEmpty + i), kSumWarps);
         }
@@ -169,9 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
     grid_dependency_wait();
     grid_launch_dependents();
 
-    float total[NP];
+    float total[NP / 2];
 #pragma unroll
-    for (int j = 0; j < NP; ++j) total[j] = 0.0f;
+    for (int j = 0; j < NP / 2; ++j) total[j] = 0.0f;
 
     if (warp == kProducerWarp) {
         if (lane == 0) {
@@ -199,42 +224,44 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
             const uint64_t desc0 = make_sdesc_sw128(sbase, 0, 1024);
             const int chain = warp - kIssuerWarp;
             int last = -1, n = 0;  // n: groups of this chain so far
-            int bs = chain, a_phase = 0, b_phase = 0;
-            uint32_t half = 0;  // which of the chain's two blocks of tensor memory
-            for (int i = chain; i < blocks; i += kChains) {
-                const uint32_t as = chain + kChains * half;
-                if (!w4_wait(bar0 + 8 * (kAFull + as), a_phase, failed) ||
-                    !w4_wait(bar0 + 8 * (kBFull + bs), b_phase, failed))
-                    break;
+            int bs = chain;
+            uint32_t phase = 0, b_phase = 0;
+            bool ok = true;
+            for (int i = chain; i < blocks && ok; i += kChains, phase ^= 1) {
                 const uint64_t desc = desc0 + static_cast<uint32_t>(bs * kB >> 4);
-                const uint32_t a_tmem = tmem + kTmemA + as * 64;
-                bool ok = true;
+                uint32_t d_tmem = 0;
 #pragma unroll
-                for (int q = 0; q < kGroups; ++q) {
-                    if (i * kGroups + q >= groups) break;
-                    const int acc = chain + kChains * (n & 1);
-                    if (!w4_wait(bar0 + 8 * (kAccEmpty + acc), (n >> 1 & 1) ^ 1, failed)) {
-                        ok = false;
-                        break;
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    ok = ok && w4_wait(bar0 + 8 * (kAFull + 2 * chain + h), phase, failed);
+                    if (h == 0) ok = ok && w4_wait(bar0 + 8 * (kBFull + bs), b_phase, failed);
+                    if (!ok) break;
                     tcgen05_fence_after_sync();
-                    const uint32_t d_tmem = tmem + kTmemAcc + acc * 64;
 #pragma unroll
-                    for (int s = 0; s < G / 16; ++s) {
-                        const int k16 = q * (G / 16) + s;  // 16 k within the block
-                        mma_f16_ts(d_tmem, a_tmem + k16 * 8, desc + ((k16 / 4 * (kB / 2) + k16 % 4 * 32) >> 4),
-                                   idesc, s > 0);
+                    for (int s = 0; s < 4; ++s) {
+                        const int k16 = 4 * h + s;        // 16 k within the block
+                        constexpr int kSteps = G / 16;    // of a group
+                        if (i * kGroups + k16 / kSteps >= groups) break;
+                        if (k16 % kSteps == 0) {
+                            const int acc = chain * L::kAccPer + n % L::kAccPer;
+                            ok = w4_wait(bar0 + 8 * (kAccEmpty + acc), (n / L::kAccPer & 1) ^ 1, failed);
+                            if (!ok) break;
+                            tcgen05_fence_after_sync();
+                            d_tmem = tmem + kTmemAcc + acc * L::kAccCols;
+                        }
+                        mma_f16_ts(d_tmem, tmem + kTmemA + chain * 64 + k16 * 8,
+                                   desc + ((h * (kB / 2) + s * 32) >> 4), idesc, k16 % kSteps > 0);
+                        issued = true;
+                        if ((k16 + 1) % kSteps == 0) {
+                            mma_commit(bar0 + 8 * (kAccFull + chain * L::kAccPer + n % L::kAccPer));
+                            ++n;
+                        }
                     }
-                    issued = true;
-                    mma_commit(bar0 + 8 * (kAccFull + acc));
-                    ++n;
+                    if (!ok) break;
+                    mma_commit(bar0 + 8 * (kAEmpty + 2 * chain + h));
                 }
                 if (!ok) break;
-                mma_commit(bar0 + 8 * (kAEmpty + as));
                 mma_commit(bar0 + 8 * (kBEmpty + bs));
                 last = i;
-                half ^= 1;
-                if (half == 0) a_phase ^= 1;
                 bs += kChains;
                 if (bs >= kBSlots) {
                     bs -= kBSlots;
@@ -252,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
         __syncwarp();
     } else if (warp >= kSumWarps) {
         // ---- unpacking: this warp's quarter (its tensor memory lanes) of its chain's blocks ----
-        const int quarter = warp & 3, part = (warp - kSumWarps) >> 2;
+        const int quarter = warp & 3, chain = (warp - kSumWarps) >> 2;
         const int ring = L::kOffW + (warp - kSumWarps) * (kWDepth * L::kWSlot);
         // copies: 16-byte chunk lane % 4 of rows lane / 4 + 8 j; 8 zero points of one group
         const int crow = lane >> 2, chunk = lane & 3;
@@ -261,15 +288,15 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
         for (int j = 0; j < 4; ++j)
             src[j] = static_cast<const uint8_t*>(a.W) +
                      (static_cast<long long>(min(n0 + quarter * 32 + crow + 8 * j, a.n - 1)) * a.k +
-                      static_cast<long long>(first + part) * kBlockK) / 2 + chunk * 16;
+                      static_cast<long long>(first + chain) * kBlockK) / 2 + chunk * 16;
         const uint32_t dst = crow * 64 + ((chunk ^ ((crow >> 1) & 3)) << 4);  // (+ 8 rows: + 512)
-        const int k_first = (first + part) * kBlockK;
+        const int k_first = (first + chain) * kBlockK;
         int k_left = a.k - k_first;
         const int zgroup = lane >> 2, zcol = (lane & 3) * 8;
         const bool copies_zeros = a.zeros != nullptr && zgroup < kGroups && n0 + quarter * 32 + zcol < a.n;
         const uint8_t* zsrc = a.zeros + static_cast<long long>(k_first / G + zgroup) * a.n + n0 + quarter * 32 + zcol;
         const long long z_step = static_cast<long long>(kChains * kGroups) * a.n;
-        const int mine = blocks > part ? (blocks - part + kChains - 1) / kChains : 0;
+        const int mine = blocks > chain ? (blocks - chain + kChains - 1) / kChains : 0;
         auto fetch = [&](int slot) {
             const uint32_t to = sbase + ring + slot * L::kWSlot;
             if (chunk * 32 < k_left) {
@@ -287,58 +314,74 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
             if (j < mine) fetch(j);
             cp_async_commit();
         }
-        const uint32_t t_lane = tmem + kTmemA + (static_cast<uint32_t>(quarter * 32) << 16);
-        for (int b = 0; b < mine; ++b) {
-            if (b + kWDepth - 1 < mine) fetch((b + kWDepth - 1) % kWDepth);
+        const uint32_t t_lane = tmem + kTmemA + chain * 64 + (static_cast<uint32_t>(quarter * 32) << 16);
+        int slot = 0, fill = kWDepth - 1;
+        uint32_t phase = 1;
+        bool ok = true;
+        for (int b = 0; b < mine && ok; ++b, phase ^= 1) {
+            if (b + kWDepth - 1 < mine) fetch(fill);
             cp_async_commit();
+            if (++fill == kWDepth) fill = 0;
             cp_async_wait_group<kWDepth - 1>();
             __syncwarp();
-            const uint8_t* slot = smem + ring + (b % kWDepth) * L::kWSlot;
-            const uint8_t* mem = slot + lane * 64;
-            const int as = part + kChains * (b & 1);
-            if (!w4_wait(bar0 + 8 * (kAEmpty + as), (b >> 1 & 1) ^ 1, failed)) break;
-            tcgen05_fence_after_sync();
+            const uint8_t* mem = smem + ring + slot * L::kWSlot;
+            if (++slot == kWDepth) slot = 0;
+            W4UnpackInOrder<BF16> unpack[kGroups];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 w4 = *reinterpret_cast<const uint4*>(mem + ((c ^ ((lane >> 1) & 3)) << 4));
-                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-                W4UnpackInOrder<BF16> unpack;
-                unpack.set(a.zeros ? slot[2048 + c * 32 / G * 32 + lane] : 8u);
-                uint32_t v[16];
+            for (int q = 0; q < kGroups; ++q) unpack[q].set(a.zeros ? mem[2048 + q * 32 + lane] : 8u);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) unpack(w[j], v + 4 * j);
-                tmem_store_16cols_async(t_lane + as * 64 + c * 16, v);
+            for (int h = 0; h < 2; ++h) {
+                uint4 w4[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    w4[c] = *reinterpret_cast<const uint4*>(mem + lane * 64 + (((2 * h + c) ^ ((lane >> 1) & 3)) << 4));
+                ok = w4_wait(bar0 + 8 * (kAEmpty + 2 * chain + h), phase, failed);
+                if (!ok) break;
+                tcgen05_fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t w[4] = {w4[c].x, w4[c].y, w4[c].z, w4[c].w};
+                    uint32_t v[16];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) unpack[(2 * h + c) * 32 / G](w[j], v + 4 * j);
+                    tmem_store_16cols_async(t_lane + (2 * h + c) * 16, v);
+                }
+                tmem_wait_st();
+                tcgen05_fence_before_sync();
+                __syncwarp();  // (also: the slot is read before its next copy is issued)
+                if (lane == 0) mbar_arrive(bar0 + 8 * (kAFull + 2 * chain + h));
             }
-            tmem_wait_st();
-            tcgen05_fence_before_sync();
-            __syncwarp();  // (also: the slot is read before its next copy is issued)
-            if (lane == 0) mbar_arrive(bar0 + 8 * (kAFull + as));
         }
         cp_async_wait_group<0>();
     } else {
         // ---- the groups' sums, scaled and added ----
+        const int quarter = warp & 3;
         const int ring = L::kOffS + warp * (kScaleDepth * L::kSSlot);
         const int sgroup = lane >> 2, scol = (lane & 3) * 8;
-        const bool copies = sgroup < kChains * kGroups && n0 + warp * 32 + scol < a.n;
+        const bool copies = sgroup < kChains * kGroups && n0 + quarter * 32 + scol < a.n;
+        constexpr int kPasses = kChains * kGroups > 8 ? kChains * kGroups / 8 : 1;
         const uint16_t* src = static_cast<const uint16_t*>(a.scales) +
-                              static_cast<long long>(first * kGroups + sgroup) * a.n + n0 + warp * 32 + scol;
+                              static_cast<long long>(first * kGroups + sgroup) * a.n + n0 + quarter * 32 + scol;
         const long long s_step = static_cast<long long>(kChains * kGroups) * a.n;
-        const int pairs = (blocks + kChains - 1) / kChains;
+        const int rounds = (blocks + kChains - 1) / kChains;
         int left = groups;  // from the next pair of blocks to copy on
         auto fetch = [&](int slot) {
-            if (copies && sgroup < left)
-                cp_async_16(sbase + ring + slot * L::kSSlot + sgroup * 64 + scol * 2, src);
+#pragma unroll
+            for (int j = 0; j < kPasses; ++j)
+                if (copies && sgroup + 8 * j < left)
+                    cp_async_16(sbase + ring + slot * L::kSSlot + (sgroup + 8 * j) * 64 + scol * 2,
+                                src + static_cast<long long>(8 * j) * a.n);
             src += s_step;
             left -= kChains * kGroups;
         };
 #pragma unroll
         for (int j = 0; j < kScaleDepth - 1; ++j) {
-            if (j < pairs) fetch(j);
+            if (j < rounds) fetch(j);
             cp_async_commit();
         }
-        const uint32_t t_lane = tmem + kTmemAcc + (static_cast<uint32_t>(warp * 32) << 16);
-        for (int i = 0; i < pairs; ++i) {
-            if (i + kScaleDepth - 1 < pairs) fetch((i + kScaleDepth - 1) % kScaleDepth);
+        const uint32_t t_lane = tmem + kTmemAcc + (static_cast<uint32_t>(quarter * 32) << 16) + (warp >> 2) * (NP / 2);
+        for (int i = 0; i < rounds; ++i) {
+            if (i + kScaleDepth - 1 < rounds) fetch((i + kScaleDepth - 1) % kScaleDepth);
             cp_async_commit();
             cp_async_wait_group<kScaleDepth - 1>();
             __syncwarp();
@@ -347,31 +390,32 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
 #pragma unroll
             for (int p = 0; p < kChains * kGroups; ++p) {
                 const int chain = p % kChains;              // the chains in turn
-                const int in_pair = chain * kGroups + p / kChains;  // group within the pair of blocks
-                if (i * kChains * kGroups + in_pair >= groups) continue;
+                const int in_round = chain * kGroups + p / kChains;  // group within the round of blocks
+                if (i * kChains * kGroups + in_round >= groups) continue;
                 const int n = i * kGroups + p / kChains;    // of the chain
-                const int q = chain + kChains * (n & 1);
-                const float sc = decode16<BF16>(scales[in_pair * 32]);
-                if (!w4_wait(bar0 + 8 * (kAccFull + q), n >> 1 & 1, failed)) {
+                const int acc = chain * L::kAccPer + n % L::kAccPer;
+                const float sc = decode16<BF16>(scales[in_round * 32]);
+                if (!w4_wait(bar0 + 8 * (kAccFull + acc), n / L::kAccPer & 1, failed)) {
                     ok = false;
                     break;
                 }
                 tcgen05_fence_after_sync();
-                uint32_t r[2][16];
-                tmem_load_16cols_async(t_lane + q * 64, r[0]);
+                const uint32_t t_acc = t_lane + acc * L::kAccCols;
+                uint32_t r[2][8];
+                tmem_load_8cols_async(t_acc, r[0]);
 #pragma unroll
                 for (int j = 0; j < NP / 16; ++j) {
-                    tmem_wait_ld(r[j & 1]);
+                    tmem_wait_ld8(r[j & 1]);
                     if (j + 1 < NP / 16) {
-                        tmem_load_16cols_async(t_lane + q * 64 + (j + 1) * 16, r[(j + 1) & 1]);
+                        tmem_load_8cols_async(t_acc + (j + 1) * 8, r[(j + 1) & 1]);
                     } else {
                         tcgen05_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar0 + 8 * (kAccEmpty + q));
+                        if (lane == 0) mbar_arrive(bar0 + 8 * (kAccEmpty + acc));
                     }
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2)
-                        fma2(total[j * 16 + e], total[j * 16 + e + 1], r[j & 1][e], r[j & 1][e + 1], sc);
+                    for (int e = 0; e < 8; e += 2)
+                        fma2(total[j * 8 + e], total[j * 8 + e + 1], r[j & 1][e], r[j & 1][e + 1], sc);
                 }
             }
             if (!ok) break;
@@ -393,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
     if (warp < kSumWarps) {
         const bool gave_up = *failed != 0;
 #pragma unroll
-        for (int j = 0; j < NP; ++j) red[j * kCols + threadIdx.x] = gave_up ? __int_as_float(0x7FC00000) : total[j];
+        for (int j = 0; j < NP / 2; ++j)
+            red[((warp >> 2) * (NP / 2) + j) * kCols + (warp & 3) * 32 + lane] = gave_up ? __int_as_float(0x7FC00000) : total[j];
     }
     if (cluster > 1)
         cluster_sync_all();
