@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,6 +29,9 @@ SOURCES = ["api.cu", "host_exec.cu", "ffn_api.cu", "layernorm_api.cu", "gemm_pai
            "gemm_smallm.cu", "ffn_onchip.cu", "elementwise.cu", "layernorm.cu",
            "sublayer_api.cu", "rmsnorm.cu", "w4.cu", "w4_tensor.cu",
            "dropout.cu"]
+# The binding's marshalling in C (needs Python's headers; without them the binding uses ctypes).
+FASTCALL = os.path.join(PKG, "_fastcall.so")
+FASTCALL_SRC = os.path.join(CSRC, "fastcall.c")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,10 +49,28 @@ def _deps() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or (_python_include() and not os.path.exists(FASTCALL)):
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(f) > t for f in _deps() + [__file__])
+
+
+def _python_include() -> str | None:
+    path = sysconfig.get_path("include")
+    return path if path and os.path.exists(os.path.join(path, "Python.h")) else None
+
+
+def _compile_fastcall() -> None:
+    include = _python_include()
+    if include is None:
+        return
+    tmp = FASTCALL + f".tmp{os.getpid()}"
+    cmd = ["gcc", "-O2", "-std=gnu11", "-Wall", "-shared", "-fPIC", "-I", include, "-I", INCLUDE,
+           FASTCALL_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on fastcall.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FASTCALL)
 
 
 def _compile(nvcc: str, src: str) -> tuple[str, str]:
@@ -66,6 +88,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
+    _compile_fastcall()
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(lambda s: _compile(nvcc, s), SOURCES))
     with open(os.path.join(BUILD, "ptxas.log"), "w") as fh:

@@ -322,30 +322,85 @@ def gemm_epi_ffn_execute_layernorm(plan, X, eps: float, W1_folded, colsum, b1_fo
            "gemm_epi_ffn_execute_layernorm")
 
 
+class _CtypesCalls:
+    """The calls below through ctypes, with the arguments of the C ABI in order."""
+
+    def __init__(self, lib):
+        self._lib = lib
+
+    def rmsnorm(self, t, d, dtype, X, residual, gamma, eps, H, Y, rstd, stream):
+        return self._lib.gemm_epi_rmsnorm(t, d, dtype, _dev(X), _dev(residual), _dev(gamma), eps,
+                                          _dev(H), _dev(Y), _dev(rstd), stream)
+
+    def rmsnorm_e4m3(self, t, d, dtype, X, residual, gamma, eps, H, Q, mode, scale, rstd,
+                     workspace, stream):
+        return self._lib.gemm_epi_rmsnorm_e4m3(t, d, dtype, _dev(X), _dev(residual), _dev(gamma),
+                                               eps, _dev(H), _dev(Q), mode, _dev(scale),
+                                               _dev(rstd), _dev(workspace), stream)
+
+    def rmsnorm_backward(self, t, d, dtype, dY, H, gamma, rstd, dH, dX, dgamma, workspace, stream):
+        return self._lib.gemm_epi_rmsnorm_backward(t, d, dtype, _dev(dY), _dev(H), _dev(gamma),
+                                                   _dev(rstd), _dev(dH), _dev(dX), _dev(dgamma),
+                                                   _dev(workspace), stream)
+
+    def w4_matmul(self, m, n, k, group, dtype, epilog, A, W, scales, zeros, bias, residual, D,
+                  stream):
+        return self._lib.gemm_epi_w4_matmul(m, n, k, group, dtype, epilog, _dev(A), _dev(W),
+                                            _dev(scales), _dev(zeros), _dev(bias), _dev(residual),
+                                            _dev(D), stream)
+
+    def w4_dequantize(self, n, k, group, dtype, W, scales, zeros, B, stream):
+        return self._lib.gemm_epi_w4_dequantize(n, k, group, dtype, _dev(W), _dev(scales),
+                                                _dev(zeros), _dev(B), stream)
+
+    def dropout(self, count, dtype, X, residual, p, seed, offset, offset_device, Y, stream):
+        return self._lib.gemm_epi_dropout(count, dtype, _dev(X), _dev(residual), p, seed, offset,
+                                          _dev(offset_device), _dev(Y), stream)
+
+
+_calls = None
+
+
+def _bind_calls():
+    """The per-token calls, through the C marshalling where it was built, else ctypes."""
+    global _calls
+    lib = load_library()
+    try:
+        from activation_epilogue_gb300 import _fastcall
+    except ImportError:
+        _calls = _CtypesCalls(lib)
+        return _calls
+    _fastcall.bind(*(ctypes.cast(getattr(lib, "gemm_epi_" + name), ctypes.c_void_p).value
+                     for name in ("rmsnorm", "rmsnorm_e4m3", "rmsnorm_backward", "w4_matmul",
+                                  "w4_dequantize", "dropout")))
+    _calls = _fastcall
+    return _calls
+
+
 def gemm_epi_rmsnorm(t: int, d: int, dtype: str, X, residual, gamma, eps: float, H, Y, rstd=None,
                      stream=None):
-    _check(load_library().gemm_epi_rmsnorm(t, d, DTYPE[dtype], _dev(X), _dev(residual),
-                                           _dev(gamma), eps, _dev(H), _dev(Y), _dev(rstd),
-                                           _stream(stream)), "gemm_epi_rmsnorm")
+    status = (_calls or _bind_calls()).rmsnorm(t, d, DTYPE[dtype], X, residual, gamma, eps, H, Y,
+                                               rstd, _stream(stream))
+    if status:
+        _check(status, "gemm_epi_rmsnorm")
 
 
 def gemm_epi_rmsnorm_e4m3(t: int, d: int, dtype: str, X, residual, gamma, eps: float, H, Q,
                           mode: str, scale, rstd=None, workspace=None, stream=None):
     """mode: "ROW" (t scales written), "TENSOR" (one, needs workspace) or "GIVEN" (one, read)."""
-    _check(load_library().gemm_epi_rmsnorm_e4m3(t, d, DTYPE[dtype], _dev(X), _dev(residual),
-                                                _dev(gamma), eps, _dev(H), _dev(Q),
-                                                SCALE_MODE[mode], _dev(scale), _dev(rstd),
-                                                _dev(workspace), _stream(stream)),
-           "gemm_epi_rmsnorm_e4m3")
+    status = (_calls or _bind_calls()).rmsnorm_e4m3(t, d, DTYPE[dtype], X, residual, gamma, eps, H,
+                                                    Q, SCALE_MODE[mode], scale, rstd, workspace,
+                                                    _stream(stream))
+    if status:
+        _check(status, "gemm_epi_rmsnorm_e4m3")
 
 
 def gemm_epi_rmsnorm_backward(t: int, d: int, dtype: str, dY, H, gamma, rstd, dH, dX, dgamma,
                               workspace, stream=None):
-    _check(load_library().gemm_epi_rmsnorm_backward(t, d, DTYPE[dtype], _dev(dY), _dev(H),
-                                                    _dev(gamma), _dev(rstd), _dev(dH), _dev(dX),
-                                                    _dev(dgamma), _dev(workspace),
-                                                    _stream(stream)),
-           "gemm_epi_rmsnorm_backward")
+    status = (_calls or _bind_calls()).rmsnorm_backward(t, d, DTYPE[dtype], dY, H, gamma, rstd, dH,
+                                                        dX, dgamma, workspace, _stream(stream))
+    if status:
+        _check(status, "gemm_epi_rmsnorm_backward")
 
 
 def gemm_epi_rmsnorm_workspace(t: int, d: int) -> int:
@@ -355,25 +410,28 @@ def gemm_epi_rmsnorm_workspace(t: int, d: int) -> int:
 
 def gemm_epi_w4_matmul(m: int, n: int, k: int, group: int, dtype: str, epilog: str, A, W, scales,
                        zeros, bias, residual, D, stream=None):
-    _check(load_library().gemm_epi_w4_matmul(m, n, k, group, DTYPE[dtype], EPILOG[epilog],
-                                             _dev(A), _dev(W), _dev(scales), _dev(zeros),
-                                             _dev(bias), _dev(residual), _dev(D),
-                                             _stream(stream)), "gemm_epi_w4_matmul")
+    status = (_calls or _bind_calls()).w4_matmul(m, n, k, group, DTYPE[dtype], EPILOG[epilog], A,
+                                                 W, scales, zeros, bias, residual, D,
+                                                 _stream(stream))
+    if status:
+        _check(status, "gemm_epi_w4_matmul")
 
 
 def gemm_epi_w4_dequantize(n: int, k: int, group: int, dtype: str, W, scales, zeros, B,
                            stream=None):
-    _check(load_library().gemm_epi_w4_dequantize(n, k, group, DTYPE[dtype], _dev(W),
-                                                 _dev(scales), _dev(zeros), _dev(B),
-                                                 _stream(stream)), "gemm_epi_w4_dequantize")
+    status = (_calls or _bind_calls()).w4_dequantize(n, k, group, DTYPE[dtype], W, scales, zeros,
+                                                     B, _stream(stream))
+    if status:
+        _check(status, "gemm_epi_w4_dequantize")
 
 
 def gemm_epi_dropout(count: int, dtype: str, X, residual, p: float, seed: int, offset: int, Y,
                      offset_device=None, stream=None):
     """seed and offset are taken mod 2^64; offset_device: an int64 CUDA tensor of one value."""
-    _check(load_library().gemm_epi_dropout(count, DTYPE[dtype], _dev(X), _dev(residual), p, seed,
-                                           offset, _dev(offset_device), _dev(Y),
-                                           _stream(stream)), "gemm_epi_dropout")
+    status = (_calls or _bind_calls()).dropout(count, DTYPE[dtype], X, residual, p, seed, offset,
+                                               offset_device, Y, _stream(stream))
+    if status:
+        _check(status, "gemm_epi_dropout")
 
 
 def gemm_epi_free(plan):

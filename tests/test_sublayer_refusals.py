@@ -1,5 +1,7 @@
 """The RMS norm, 4-bit-weight and dropout calls: what they refuse, and the empty problems they
 accept, before any device is touched (no GPU)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -140,3 +142,30 @@ def test_binding_refuses_tensors_it_cannot_pass():
         gemm_epi.gemm_epi_rmsnorm(4, 64, "bf16", x, None, x, 1e-6, None, x, stream=0)
     with pytest.raises(ValueError, match="CUDA"):
         gemm_epi.gemm_epi_dropout(256, "bf16", x, None, 0.5, 1, 2, x, stream=0)
+
+
+def test_both_marshalling_paths_agree():
+    """The C marshalling is there (its sources build with the library) and answers as the ctypes
+    path does: the same statuses, the same refusals of arguments."""
+    fast = gemm_epi._bind_calls()
+    assert fast.__name__.endswith("_fastcall")
+    slow = gemm_epi._CtypesCalls(gemm_epi.load_library())
+    rows = [("rmsnorm", (0, 64, 1, None, None, None, 1e-6, None, None, None, 0), 0),
+            ("rmsnorm", (4, 12, 1, P, None, P, 1e-6, None, P, None, 0), SHAPE),
+            ("rmsnorm", (4, 64, 1, P, None, P, -1.0, None, P, None, 0), INVALID),
+            ("rmsnorm_e4m3", (4, 64, 1, P, None, P, 1e-6, None, 2 * P, 1, P, None, None, 0), INVALID),
+            ("rmsnorm_backward", (4, 64, 1, P, P, P, P, None, P + 8, P, P, 0), MISALIGNED),
+            ("w4_matmul", (65, 64, 64, 64, 1, 0, P, P, P, None, P, None, P, 0), SHAPE),
+            ("w4_dequantize", (64, 64, 64, 1, P, P, P + 4, P, 0), MISALIGNED),
+            ("dropout", (0, 1, None, None, 0.5, 2 ** 64 + 3, -1, None, None, 0), 0),
+            ("dropout", (8, 1, P, None, 1.5, 1, 2, None, P, 0), INVALID)]
+    for name, args, want in rows:
+        assert getattr(fast, name)(*args) == want == getattr(slow, name)(*args), name
+    for bad in (torch.zeros(4, 64, dtype=torch.bfloat16), "x", 1.5):
+        for calls in (fast, slow):
+            with pytest.raises((ValueError, TypeError, AttributeError, ctypes.ArgumentError)):
+                calls.dropout(8, 1, bad, None, 0.5, 1, 2, None, P, 0)
+    with pytest.raises(TypeError):
+        fast.rmsnorm(1, 2, 3)
+    with pytest.raises((TypeError, OverflowError)):
+        fast.rmsnorm(2 ** 70, 64, 1, P, None, P, 1e-6, None, P, None, 0)
