@@ -312,12 +312,13 @@ struct W4Args {
     const void* residual;
     void* D;
     int m, n, k, group, epilog;
+    int streams;  // w4_dequantize: B is larger than L2
 };
 constexpr int kW4MaxM = 64;
 cudaError_t w4_matmul_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
 // (csrc/w4_tensor.cu) the product for 9 to 64 rows of A, k > 0
 cudaError_t w4_tensor_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
-cudaError_t w4_dequantize_launch(const W4Args& a, bool bf16, cudaStream_t stream);
+cudaError_t w4_dequantize_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
 
 // Dropout (csrc/dropout.cu): an element is kept when its 16 random bits are >= drop.
 struct DropoutArgs {

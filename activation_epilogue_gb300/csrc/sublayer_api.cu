@@ -175,7 +175,7 @@ gemm_epi_status gemm_epi_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t grou
     int sms = 0;
     st = device_sms(&sms);
     if (st != GEMM_EPI_OK) return st;
-    W4Args a;
+    W4Args a = {};
     a.A = A;
     a.W = W;
     a.scales = scales;
@@ -212,7 +212,7 @@ gemm_epi_status gemm_epi_w4_dequantize(int64_t n, int64_t k, int64_t group,
     a.n = static_cast<int>(n);
     a.k = static_cast<int>(k);
     a.group = static_cast<int>(group);
-    return launched(w4_dequantize_launch(a, dtype == GEMM_EPI_BF16, stream));
+    return launched(w4_dequantize_launch(a, dtype == GEMM_EPI_BF16, sms, stream));
 }
 
 gemm_epi_status gemm_epi_dropout(int64_t count, gemm_epi_dtype dtype, const void* X,
