@@ -31,10 +31,13 @@ gemm_epi_status device_sms(int* sms)
 
 gemm_epi_status launched(cudaError_t e) { return e == cudaSuccess ? GEMM_EPI_OK : GEMM_EPI_ERR_LAUNCH; }
 
+// (widths to 2^30: the kernels step through them in 32 bits)
+constexpr int64_t kMaxWidth = 1ll << 30;
+
 bool norm_shape_ok(int64_t t, int64_t d)
 {
     const int64_t kMax = (1ll << 31) - 1;
-    return t >= 0 && d >= 8 && d % 8 == 0 && t <= kMax && d <= kMax && t * d <= (1ll << 40);
+    return t >= 0 && d >= 8 && d % 8 == 0 && t <= kMax && d <= kMaxWidth && t * d <= (1ll << 40);
 }
 
 int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
@@ -78,10 +81,9 @@ gemm_epi_status rmsnorm(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* 
 
 gemm_epi_status w4_checked(int64_t n, int64_t k, int64_t group, gemm_epi_dtype dtype)
 {
-    const int64_t kMax = (1ll << 31) - 1;
     if (!is_16bit(dtype)) return GEMM_EPI_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return GEMM_EPI_ERR_UNSUPPORTED_SHAPE;
-    if (n < 0 || k < 0 || n > kMax || k > kMax || n % 8 != 0 || k % group != 0 || n * k > (1ll << 40))
+    if (n < 0 || k < 0 || n > kMaxWidth || k > kMaxWidth || n % 8 != 0 || k % group != 0 || n * k > (1ll << 40))
         return GEMM_EPI_ERR_UNSUPPORTED_SHAPE;
     return GEMM_EPI_OK;
 }

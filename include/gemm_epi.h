@@ -353,7 +353,7 @@ gemm_epi_status gemm_epi_layernorm_fold(int64_t d, int64_t f, gemm_epi_dtype dty
  *     rstd_i = 1 / sqrt(mean_j H_ij^2 + eps),      Y_ij = H_ij rstd_i gamma_j.
  * The norm is of the rounded H, the values that the next sub-layer and the backward pass
  * read; sums and rstd are fp32, Y is rounded once.  X, residual, H, Y: t x d; gamma: d
- * elements; all of `dtype` (F16 or BF16), d a multiple of 8 and >= 8, 16-byte aligned.  H is
+ * elements; all of `dtype` (F16 or BF16), d a multiple of 8, 8 to 2^30, 16-byte aligned.  H is
  * given exactly when the residual is.  H and Y may each be X or the residual itself, but not
  * the same buffer; no other overlap.  rstd: t fp32, 4-byte aligned, or NULL (the backward
  * pass reads it).  eps >= 0.  A NaN or an infinity in a row of H makes that row of Y NaN (or,
@@ -406,14 +406,16 @@ int64_t gemm_epi_rmsnorm_workspace(int64_t t, int64_t d);
  * contiguous along k, two values per byte, the lower half first; q in 0..15), scales is
  * k/group rows of n values of `dtype`, and zeros k/group rows of n bytes (0..15), or NULL for
  * z = 8 everywhere; s and z are those of row i / group and column j.  group is 32, 64 or 128;
- * k a multiple of group, n a multiple of 8.  For decoding: m is 1 to 64 rows of A (0 launches
+ * k a multiple of group, n a multiple of 8, both at most 2^30.  For decoding: m is 1 to 64 rows of A (0 launches
  * nothing); for more, gemm_epi_w4_dequantize and a plan.  A: m x k, bias: n elements (the
  * (1,n) layout), residual and D: m x n, of `dtype` (F16 or BF16); epilogs BIAS, RELU_BIAS,
  * GELU_BIAS, TANH_BIAS, BIAS_RESIDUAL and NONE as for plans; bias is NULL exactly for NONE,
  * the residual given exactly for BIAS_RESIDUAL, and D may be the residual itself.  The
  * differences q - z are exact in 16 bits and their products with A are summed in fp32, group
  * by group, with the scales applied in fp32.  A, W, scales, residual and D 16-byte aligned,
- * zeros 8-byte, bias 2-byte.  No workspace, no plan; asynchronous on `stream` as above. */
+ * zeros 8-byte, bias 2-byte.  No workspace, no plan; asynchronous on `stream` as above.  (The
+ * kernel for more than a few rows waits for its own copies and products with a limit of two
+ * seconds; should one run out, it ends and writes NaN.) */
 gemm_epi_status gemm_epi_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group,
                                    gemm_epi_dtype dtype, gemm_epi_epilog epilog, const void* A,
                                    const void* W, const void* scales, const uint8_t* zeros,

@@ -50,6 +50,17 @@ def test_w4_matmul(m, n, k, group, dtype):
     _check(ref.w4_problem(m, n, k, group, dtype, (m + group // 32) % 2 == 0, m + n + k), group, dtype, epilog)
 
 
+@pytest.mark.parametrize("m,n,k", [(9, 4104, 4096), (16, 12296, 1152), (13, 1536, 8320), (24, 4232, 4096),
+                                   (48, 19600, 672), (64, 1160, 12320), (3, 16392, 1056), (8, 5000, 4224)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_larger_weights(m, n, k, group):
+    # weights large enough for the other choices of kernel and of k's split, with more tiles of
+    # columns than SMs among them
+    k = -(-k // group) * group
+    dtype, epilog = ("bf16", "GELU_BIAS") if group == 64 else ("f16", "BIAS_RESIDUAL")
+    _check(ref.w4_problem(m, n, k, group, dtype, group != 64, m + n), group, dtype, epilog)
+
+
 @pytest.mark.parametrize("epilog", EPILOGS)
 @pytest.mark.parametrize("m", [1, 5, 12, 40])
 @pytest.mark.parametrize("zeros", [False, True])
@@ -60,7 +71,7 @@ def test_w4_epilogs(epilog, m, zeros):
 
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("m", [1, 11])
+@pytest.mark.parametrize("m", [1, 11, 37])
 def test_w4_integers_are_exact(group, dtype, m):
     # integer activations and unit scales: every sum is an integer that fp32 holds, and small
     # enough for the output type (a wrong or missing term shows as a whole number)
@@ -152,7 +163,8 @@ def test_w4_in_a_graph_and_on_a_stream():
     assert torch.equal(D.cpu(), want)
 
 
-@pytest.mark.parametrize("n,k", [(8, 32), (40, 96), (64, 64), (72, 1056), (264, 384), (1000, 2048)])
+@pytest.mark.parametrize("n,k", [(8, 32), (40, 96), (64, 64), (72, 1056), (264, 384), (1000, 2048),
+                                 (4104, 2912), (8200, 4128)])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("dtype,zeros", [("bf16", True), ("f16", False)])
 def test_w4_dequantize(n, k, group, dtype, zeros):

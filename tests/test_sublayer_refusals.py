@@ -29,7 +29,7 @@ NORM = dict(t=4, d=64, dtype="bf16", X=P, residual=P, gamma=P, eps=1e-6, H=P, Y=
 
 @pytest.mark.parametrize("change,status", [
     (dict(dtype="e4m3"), INVALID), (dict(t=-1), SHAPE), (dict(d=12), SHAPE), (dict(d=0), SHAPE),
-    (dict(t=2 ** 31), SHAPE), (dict(t=2 ** 30, d=8192), SHAPE), (dict(eps=-1.0), INVALID),
+    (dict(t=2 ** 31), SHAPE), (dict(t=1, d=2 ** 30 + 8), SHAPE), (dict(t=2 ** 30, d=8192), SHAPE), (dict(eps=-1.0), INVALID),
     (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID), (dict(X=None), INVALID),
     (dict(gamma=None), INVALID), (dict(Y=None), INVALID), (dict(H=None), INVALID),
     (dict(residual=None), INVALID), (dict(Y=P, H=P), INVALID), (dict(X=P + 8), MISALIGNED),
@@ -92,7 +92,8 @@ W4 = dict(m=2, n=64, k=128, group=32, dtype="bf16", epilog="BIAS", A=P, W=P, sca
 @pytest.mark.parametrize("change,status", [
     (dict(group=16), SHAPE), (dict(group=0), SHAPE), (dict(k=48), SHAPE), (dict(n=12), SHAPE),
     (dict(m=65), SHAPE), (dict(m=-1), SHAPE), (dict(n=-8), SHAPE), (dict(k=-32), SHAPE),
-    (dict(n=2 ** 31), SHAPE), (dict(dtype="e4m3"), INVALID), (dict(epilog="RELU_AUX_BIAS"), INVALID),
+    (dict(n=2 ** 31), SHAPE), (dict(n=8, k=2 ** 30 + 32), SHAPE),
+    (dict(dtype="e4m3"), INVALID), (dict(epilog="RELU_AUX_BIAS"), INVALID),
     (dict(epilog="GELU_AUX_BIAS"), INVALID), (dict(epilog="LN_GELU_BIAS"), INVALID),
     (dict(epilog="DRELU_BGRAD"), INVALID), (dict(A=None), INVALID), (dict(W=None), INVALID),
     (dict(scales=None), INVALID), (dict(D=None), INVALID), (dict(bias=None), INVALID),
