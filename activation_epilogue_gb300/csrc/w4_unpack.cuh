@@ -119,13 +119,30 @@ struct W4UnpackInOrder {
 // one not, `failed` is set after two seconds and the block writes NaN.
 constexpr unsigned long long kW4WaitNs = 2000ull * 1000 * 1000;
 
+// One try suspends the thread for up to kW4TryNs: a waiting warp takes no issue slots from the
+// warps that work.
+constexpr uint32_t kW4TryNs = 100 * 1000;
+
+__device__ __forceinline__ bool w4_try_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred P1;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, P1;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(kW4TryNs)
+        : "memory");
+    return done != 0;
+}
+
 __device__ __forceinline__ bool w4_wait(uint32_t bar, uint32_t parity, volatile int* failed)
 {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (w4_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (unsigned long long poll = 1; poll < kW4WaitNs / 8; ++poll) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((poll & 63) == 0 && (*failed || globaltimer_ns() - t0 > kW4WaitNs)) break;
+        if (w4_try_wait(bar, parity)) return true;
+        if (*failed || globaltimer_ns() - t0 > kW4WaitNs) break;
     }
     *failed = 1;
     return false;
