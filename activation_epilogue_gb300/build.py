@@ -10,6 +10,7 @@ shared-memory reports are kept in ``_build/ptxas.log``.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -29,9 +30,10 @@ SOURCES = ["api.cu", "host_exec.cu", "ffn_api.cu", "layernorm_api.cu", "gemm_pai
            "gemm_smallm.cu", "ffn_onchip.cu", "elementwise.cu", "layernorm.cu",
            "sublayer_api.cu", "rmsnorm.cu", "w4.cu", "w4_tensor.cu",
            "dropout.cu"]
-# The binding's marshalling in C (needs Python's headers; without them the binding uses ctypes).
+# The binding's marshalling in C++ (needs the headers of Python and torch; without them the
+# binding goes through ctypes).
 FASTCALL = os.path.join(PKG, "_fastcall.so")
-FASTCALL_SRC = os.path.join(CSRC, "fastcall.c")
+FASTCALL_SRC = os.path.join(CSRC, "fastcall.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,27 +51,44 @@ def _deps() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or (_python_include() and not os.path.exists(FASTCALL)):
+    if not os.path.exists(LIB) or (not os.path.exists(FASTCALL) and _fastcall_paths()):
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(f) > t for f in _deps() + [__file__])
 
 
-def _python_include() -> str | None:
-    path = sysconfig.get_path("include")
-    return path if path and os.path.exists(os.path.join(path, "Python.h")) else None
+def _fastcall_paths() -> tuple[list[str], str] | None:
+    """(include folders, torch's library folder), or None where a header is missing."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    torch_dir = spec.submodule_search_locations[0]
+    nvcc = _nvcc()
+    includes = [sysconfig.get_path("include"), os.path.join(torch_dir, "include"),
+                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
+    needed = [os.path.join(includes[0], "Python.h"),
+              os.path.join(includes[1], "torch", "csrc", "autograd", "python_variable.h"),
+              os.path.join(includes[3], "cuda_runtime_api.h")]
+    if not all(os.path.exists(f) for f in needed):
+        return None
+    return includes, os.path.join(torch_dir, "lib")
 
 
 def _compile_fastcall() -> None:
-    include = _python_include()
-    if include is None:
+    paths = _fastcall_paths()
+    if paths is None:
         return
+    includes, libdir = paths
     tmp = FASTCALL + f".tmp{os.getpid()}"
-    cmd = ["gcc", "-O2", "-std=gnu11", "-Wall", "-shared", "-fPIC", "-I", include, "-I", INCLUDE,
-           FASTCALL_SRC, "-o", tmp]
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE]
+    for folder in includes:
+        cmd += ["-isystem", folder]
+    cmd += [FASTCALL_SRC, "-L", libdir, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            f"-Wl,-rpath,{libdir}", "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on fastcall.c:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on fastcall.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, FASTCALL)
 
 
@@ -88,9 +107,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
-    _compile_fastcall()
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        fastcall = ex.submit(_compile_fastcall)
         results = list(ex.map(lambda s: _compile(nvcc, s), SOURCES))
+        fastcall.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as fh:
         for src, (_, log) in zip(SOURCES, results):
             fh.write(f"==== {src}\n{log}\n")

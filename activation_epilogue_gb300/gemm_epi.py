@@ -323,48 +323,50 @@ def gemm_epi_ffn_execute_layernorm(plan, X, eps: float, W1_folded, colsum, b1_fo
 
 
 class _CtypesCalls:
-    """The calls below through ctypes, with the arguments of the C ABI in order."""
+    """The calls below through ctypes, with the arguments of the C ABI in order (stream: a handle,
+    or None for the current torch stream)."""
 
     def __init__(self, lib):
         self._lib = lib
 
     def rmsnorm(self, t, d, dtype, X, residual, gamma, eps, H, Y, rstd, stream):
         return self._lib.gemm_epi_rmsnorm(t, d, dtype, _dev(X), _dev(residual), _dev(gamma), eps,
-                                          _dev(H), _dev(Y), _dev(rstd), stream)
+                                          _dev(H), _dev(Y), _dev(rstd), _stream(stream))
 
     def rmsnorm_e4m3(self, t, d, dtype, X, residual, gamma, eps, H, Q, mode, scale, rstd,
                      workspace, stream):
         return self._lib.gemm_epi_rmsnorm_e4m3(t, d, dtype, _dev(X), _dev(residual), _dev(gamma),
                                                eps, _dev(H), _dev(Q), mode, _dev(scale),
-                                               _dev(rstd), _dev(workspace), stream)
+                                               _dev(rstd), _dev(workspace), _stream(stream))
 
     def rmsnorm_backward(self, t, d, dtype, dY, H, gamma, rstd, dH, dX, dgamma, workspace, stream):
         return self._lib.gemm_epi_rmsnorm_backward(t, d, dtype, _dev(dY), _dev(H), _dev(gamma),
                                                    _dev(rstd), _dev(dH), _dev(dX), _dev(dgamma),
-                                                   _dev(workspace), stream)
+                                                   _dev(workspace), _stream(stream))
 
     def w4_matmul(self, m, n, k, group, dtype, epilog, A, W, scales, zeros, bias, residual, D,
                   stream):
         return self._lib.gemm_epi_w4_matmul(m, n, k, group, dtype, epilog, _dev(A), _dev(W),
                                             _dev(scales), _dev(zeros), _dev(bias), _dev(residual),
-                                            _dev(D), stream)
+                                            _dev(D), _stream(stream))
 
     def w4_dequantize(self, n, k, group, dtype, W, scales, zeros, B, stream):
         return self._lib.gemm_epi_w4_dequantize(n, k, group, dtype, _dev(W), _dev(scales),
-                                                _dev(zeros), _dev(B), stream)
+                                                _dev(zeros), _dev(B), _stream(stream))
 
     def dropout(self, count, dtype, X, residual, p, seed, offset, offset_device, Y, stream):
         return self._lib.gemm_epi_dropout(count, dtype, _dev(X), _dev(residual), p, seed, offset,
-                                          _dev(offset_device), _dev(Y), stream)
+                                          _dev(offset_device), _dev(Y), _stream(stream))
 
 
 _calls = None
 
 
 def _bind_calls():
-    """The per-token calls, through the C marshalling where it was built, else ctypes."""
+    """The per-token calls, through the C++ marshalling where it was built, else ctypes."""
     global _calls
     lib = load_library()
+    import torch  # noqa: F401  (the marshalling links against the loaded torch)
     try:
         from activation_epilogue_gb300 import _fastcall
     except ImportError:
@@ -377,10 +379,15 @@ def _bind_calls():
     return _calls
 
 
+def _handle(stream):
+    """A stream object's or number's handle; None (the current stream) stays None."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
+
+
 def gemm_epi_rmsnorm(t: int, d: int, dtype: str, X, residual, gamma, eps: float, H, Y, rstd=None,
                      stream=None):
     status = (_calls or _bind_calls()).rmsnorm(t, d, DTYPE[dtype], X, residual, gamma, eps, H, Y,
-                                               rstd, _stream(stream))
+                                               rstd, _handle(stream))
     if status:
         _check(status, "gemm_epi_rmsnorm")
 
@@ -390,7 +397,7 @@ def gemm_epi_rmsnorm_e4m3(t: int, d: int, dtype: str, X, residual, gamma, eps: f
     """mode: "ROW" (t scales written), "TENSOR" (one, needs workspace) or "GIVEN" (one, read)."""
     status = (_calls or _bind_calls()).rmsnorm_e4m3(t, d, DTYPE[dtype], X, residual, gamma, eps, H,
                                                     Q, SCALE_MODE[mode], scale, rstd, workspace,
-                                                    _stream(stream))
+                                                    _handle(stream))
     if status:
         _check(status, "gemm_epi_rmsnorm_e4m3")
 
@@ -398,7 +405,7 @@ def gemm_epi_rmsnorm_e4m3(t: int, d: int, dtype: str, X, residual, gamma, eps: f
 def gemm_epi_rmsnorm_backward(t: int, d: int, dtype: str, dY, H, gamma, rstd, dH, dX, dgamma,
                               workspace, stream=None):
     status = (_calls or _bind_calls()).rmsnorm_backward(t, d, DTYPE[dtype], dY, H, gamma, rstd, dH,
-                                                        dX, dgamma, workspace, _stream(stream))
+                                                        dX, dgamma, workspace, _handle(stream))
     if status:
         _check(status, "gemm_epi_rmsnorm_backward")
 
@@ -412,7 +419,7 @@ def gemm_epi_w4_matmul(m: int, n: int, k: int, group: int, dtype: str, epilog: s
                        zeros, bias, residual, D, stream=None):
     status = (_calls or _bind_calls()).w4_matmul(m, n, k, group, DTYPE[dtype], EPILOG[epilog], A,
                                                  W, scales, zeros, bias, residual, D,
-                                                 _stream(stream))
+                                                 _handle(stream))
     if status:
         _check(status, "gemm_epi_w4_matmul")
 
@@ -420,7 +427,7 @@ def gemm_epi_w4_matmul(m: int, n: int, k: int, group: int, dtype: str, epilog: s
 def gemm_epi_w4_dequantize(n: int, k: int, group: int, dtype: str, W, scales, zeros, B,
                            stream=None):
     status = (_calls or _bind_calls()).w4_dequantize(n, k, group, DTYPE[dtype], W, scales, zeros,
-                                                     B, _stream(stream))
+                                                     B, _handle(stream))
     if status:
         _check(status, "gemm_epi_w4_dequantize")
 
@@ -429,7 +436,7 @@ def gemm_epi_dropout(count: int, dtype: str, X, residual, p: float, seed: int, o
                      offset_device=None, stream=None):
     """seed and offset are taken mod 2^64; offset_device: an int64 CUDA tensor of one value."""
     status = (_calls or _bind_calls()).dropout(count, DTYPE[dtype], X, residual, p, seed, offset,
-                                               offset_device, Y, _stream(stream))
+                                               offset_device, Y, _handle(stream))
     if status:
         _check(status, "gemm_epi_dropout")
 
