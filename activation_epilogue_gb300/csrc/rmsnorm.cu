@@ -1,4 +1,18 @@
 // RMS norm with the residual's addition, forward (16-bit or E4M3 output) and backward.
+//
+//   H = X + residual (rounded), rstd = 1 / sqrt(mean H^2 + eps), Y = H rstd gamma;
+//   g = dY gamma, xh = H rstd: dX = rstd (g - xh mean(g xh)) + dH, dgamma = sum dY xh.
+//
+// Everything is bound by the bytes: a row is read once into registers (16-byte accesses, every
+// load of the row before the first use), its sum of squares and, for E4M3, its largest value are
+// reduced over the row's threads, and the row is written.  Squares, sums, rstd, maxima and the
+// sums of dgamma are fp32; H, Y and dX are rounded once each, E4M3 codes once from fp32 (they are
+// y times the reciprocal of the scale, which may differ from the quotient in its last fp32 bit).
+// Measured (bf16, 6.79 TB/s copy): 16384 x 8192 with the residual to 16 bits 152 us and to E4M3
+// with a scale per row 133 us (104 % of the copy rate), backward 163 us (97 %); 2039 x 4096 to
+// E4M3 12 us (70 %: two waves of short blocks), one row of 4096 1.5 us.  One scale for the tensor
+// has to read H a second time: 177 us for 16384 x 8192, at the copy rate for the 9 bytes an
+// element that it moves.
 #include <cuda_fp8.h>
 
 #include "kernel_params.h"

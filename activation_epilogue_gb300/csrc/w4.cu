@@ -6,19 +6,24 @@
 // and every weight is unpacked once for up to 64 rows.  For a few rows that is 4 bits of
 // traffic per 2 m flops, bound by the weight's bytes.
 //
-//   * A block takes 16 MT CW columns of D and all of k, in stages of 128 KW values of k
-//     (CW KW = 8 warps): the stage's weights, rows of A, scales and zero points are copied
+//   * A block takes 16 MT CW columns of D and all of k (or a cluster's share of it), in stages of
+//     128 KW values of k (CW KW = 8 warps): the stage's weights, rows of A, scales and zero points are copied
 //     with cp.async into a ring, each byte by one thread.
 //   * Warp (cw, kw) multiplies its 16 MT columns by its 128 values of k.  In a row's 64 bytes
 //     of those, chunk i (16 bytes) holds k = 32 i .. 32 i + 31, and ldmatrix hands word t of
 //     row r to lane 4 r + t: eight values of k for MMA row r.  A word's halves-apart nibbles
-//     (j, j + 4) become a register pair of 16-bit values by one shift and one and-or with the
-//     bits of 128 (bf16) or 1024 (f16), whose last mantissa bit is 1; subtracting 128 + z
-//     (1024 + z) leaves q - z, exactly.  The rows of A are paired in the same order (the order
+//     (j, j + 4) become a register pair of 16-bit values by a shift and one and-or with the bits
+//     of a power of two whose last mantissa bits hold them; a subtraction leaves q - z, exactly
+//     (W4Unpack).  The rows of A are paired in the same order (the order
 //     of k inside an MMA is free as long as both operands have it).
 //   * A group's sum is complete in the accumulator (groups are whole MMAs, all of whose lanes
 //     are in one group), so the scale multiplies an fp32 sum, and no weight is ever rounded.
 //   * The KW warps' sums meet in shared memory, in order; then the epilogue.
+// Measured (one row, bf16 or f16): 8192 x 16384 and 16384 x 8192 22.7 us (46 % of the copy rate
+// for the weight's bytes; the loads alone 13.4, the arithmetic alone 17.6; 256 or 512 blocks on
+// 152 SMs leave a sixth of them idle at the end), 4096 x 4096 4.4, 4096 x 1024 2.3 us.  Tried and
+// left: bulk copies of rows by one warp (33 us: 75 cycles for each copy of 512 bytes), 16 warps a
+// block (26.6), 256 values of k per warp and stage (22.8).
 #include "kernel_params.h"
 #include "launch.h"
 #include "ptx.cuh"
