@@ -368,7 +368,7 @@ gemm_epi_status gemm_epi_rmsnorm(int64_t t, int64_t d, gemm_epi_dtype dtype, con
 typedef enum {
     GEMM_EPI_SCALE_ROW = 0,    /* scale[i] = max_j |Y_ij| / 448, t values written */
     GEMM_EPI_SCALE_TENSOR = 1, /* scale[0] = max_ij |Y_ij| / 448, one value written */
-    GEMM_EPI_SCALE_GIVEN = 2   /* scale[0] is read: a calibrated scale, > 0 */
+    GEMM_EPI_SCALE_GIVEN = 2   /* scale[0] is read: a calibrated scale, 2^-126 or more */
 } gemm_epi_scale_mode;
 
 /* The same norm with Y in E4M3 for an E4M3 plan: Q_ij = Y_ij / scale rounded once from fp32 to

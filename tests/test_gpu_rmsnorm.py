@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 # rows shorter than a warp's width of vectors, odd widths, and widths on both sides of every
 # power of two that a kernel may hold a row in
 SHAPES = [(1, 8), (3, 72), (37, 264), (5, 1000), (300, 1024), (2, 2048), (7, 4104), (129, 4096),
-          (1, 8192), (3, 8200), (2, 16384), (1, 16392), (2, 40000)]
+          (11, 2056), (4, 4088), (1, 8192), (3, 8200), (2, 16384), (1, 16392), (2, 40000)]
 MODES = ["ROW", "TENSOR", "GIVEN"]
 
 

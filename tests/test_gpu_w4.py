@@ -131,23 +131,25 @@ def test_w4_in_place_residual_and_repeatable():
     assert torch.equal(R, first) and torch.equal(_run(p, 128, "bf16", "BIAS_RESIDUAL"), first)
 
 
-def test_w4_k_zero_is_the_epilogue_alone():
+@pytest.mark.parametrize("m", [3, 12, 40])
+def test_w4_k_zero_is_the_epilogue_alone(m):
     bias = torch.randn(64, generator=torch.Generator().manual_seed(1)).to(torch.float16)
-    D = torch.full((3, 64), float("nan"), dtype=torch.float16, device="cuda")
-    gemm_epi.gemm_epi_w4_matmul(3, 64, 0, 64, "f16", "RELU_BIAS", None, None, None, None, bias.cuda(), None, D)
-    assert torch.equal(D.cpu(), bias.clamp(min=0).expand(3, -1))
+    D = torch.full((m, 64), float("nan"), dtype=torch.float16, device="cuda")
+    gemm_epi.gemm_epi_w4_matmul(m, 64, 0, 64, "f16", "RELU_BIAS", None, None, None, None, bias.cuda(), None, D)
+    assert torch.equal(D.cpu(), bias.clamp(min=0).expand(m, -1))
 
 
-def test_w4_in_a_graph_and_on_a_stream():
-    p = ref.w4_problem(2, 264, 1024, 32, "f16", True, 6)
+@pytest.mark.parametrize("m", [2, 45])
+def test_w4_in_a_graph_and_on_a_stream(m):
+    p = ref.w4_problem(m, 264, 1024, 32, "f16", True, 6)
     want = _run(p, 32, "f16", "GELU_BIAS").cpu()
     g = {key: None if v is None else v.cuda() for key, v in p.items() if key != "q"}
-    D = torch.zeros(2, 264, dtype=torch.float16, device="cuda")
+    D = torch.zeros(m, 264, dtype=torch.float16, device="cuda")
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
 
     def call(stream=None):
-        gemm_epi.gemm_epi_w4_matmul(2, 264, 1024, 32, "f16", "GELU_BIAS", g["A"], g["W"], g["scales"],
+        gemm_epi.gemm_epi_w4_matmul(m, 264, 1024, 32, "f16", "GELU_BIAS", g["A"], g["W"], g["scales"],
                                     g["zeros"], g["bias"], None, D, stream)
     with torch.cuda.graph(graph):
         call()
@@ -161,6 +163,29 @@ def test_w4_in_a_graph_and_on_a_stream():
     call(side)
     side.synchronize()
     assert torch.equal(D.cpu(), want)
+
+
+def test_w4_calls_on_two_streams_at_once():
+    # the tcgen05 kernel takes all of an SM's tensor memory: calls that meet on the GPU, with
+    # each other and with a plan's GEMM, wait their turn
+    p = [ref.w4_problem(m, 1000, 2048, 64, "bf16", True, m) for m in (48, 5)]
+    want = [_run(q, 64, "bf16", "BIAS").cpu() for q in p]
+    gpu = [{key: v.cuda() for key, v in q.items() if v is not None and key != "q"} for q in p]
+    D = [torch.zeros_like(w, device="cuda") for w in want]
+    B = torch.randn(2048, 1000, device="cuda").to(torch.bfloat16)
+    C, C0 = (torch.zeros(48, 1000, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    with gemm_epi.Plan(48, 1000, 2048, "bf16", "NONE") as plan:
+        plan.execute(gpu[0]["A"], B, None, C0)
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for s, q, d in zip(streams, gpu, D):
+                gemm_epi.gemm_epi_w4_matmul(q["A"].shape[0], 1000, 2048, 64, "bf16", "BIAS", q["A"], q["W"],
+                                            q["scales"], q["zeros"], q["bias"], None, d, s)
+            plan.execute(gpu[0]["A"], B, None, C, stream=streams[2])
+        torch.cuda.synchronize()
+        assert plan.sync_status() == 0
+    assert all(torch.equal(d.cpu(), w) for d, w in zip(D, want)) and torch.equal(C, C0)
 
 
 @pytest.mark.parametrize("n,k", [(8, 32), (40, 96), (64, 64), (72, 1056), (264, 384), (1000, 2048),
