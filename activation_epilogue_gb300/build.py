@@ -28,7 +28,7 @@ SOURCES = ["api.cu", "host_exec.cu", "ffn_api.cu", "layernorm_api.cu", "gemm_pai
            "gemm_rowtile.cu", "gemm_swapped.cu", "gemm_fwd_bias.cu", "gemm_fwd_relu.cu",
            "gemm_fwd_gelu.cu", "gemm_fwd_relu_aux.cu", "gemm_fwd_residual.cu",
            "gemm_smallm.cu", "ffn_onchip.cu", "elementwise.cu", "layernorm.cu",
-           "sublayer_api.cu", "rmsnorm.cu", "w4.cu", "w4_tensor.cu",
+           "sublayer_api.cu", "rmsnorm.cu", "w4.cu", "w4_stream.cu", "w4_tensor.cu",
            "dropout.cu"]
 # The binding's marshalling in C++ (needs the headers of Python and torch; without them the
 # binding goes through ctypes).

@@ -19,15 +19,17 @@
 //   * A group's sum is complete in the accumulator (groups are whole MMAs, all of whose lanes
 //     are in one group), so the scale multiplies an fp32 sum, and no weight is ever rounded.
 //   * The KW warps' sums meet in shared memory, in order; then the epilogue.
-// Measured (one row, bf16 or f16): 8192 x 16384 and 16384 x 8192 22.7 us (46 % of the copy rate
-// for the weight's bytes; the loads alone 13.4, the arithmetic alone 17.6; 256 or 512 blocks on
-// 152 SMs leave a sixth of them idle at the end), 4096 x 4096 4.4, 4096 x 1024 2.3 us.  Tried and
-// left: bulk copies of rows by one warp (33 us: 75 cycles for each copy of 512 bytes), 16 warps a
-// block (26.6), 256 values of k per warp and stage (22.8).
+// Measured (bf16, groups of 128): 4096 x 4096 with one row 4.4 us, 4096 x 1024 2.3; 8 rows of
+// 8192 x 8192 13.9 and of 16384 x 8192 26.3 us (39 % of the copy rate for the weight's bytes; with
+// one row the loads alone took 13.4 us, the arithmetic alone 17.6, both 22.7: the larger weights
+// of up to 4 rows have a kernel of their own, w4_stream.cu).  Tried and left: bulk copies of rows
+// by one warp (33 us: 75 cycles for each copy of 512 bytes), 16 warps a block (26.6), 256 values
+// of k per warp and stage (22.8).
 #include "kernel_params.h"
 #include "launch.h"
 #include "ptx.cuh"
 #include "vec16.cuh"
+#include "w4_mma.cuh"
 #include "w4_unpack.cuh"
 
 namespace gemm_epi {
@@ -45,22 +47,6 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr)
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
-}
-
-template <bool BF16>
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    if constexpr (BF16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-                     "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-                     "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // One stage in shared memory for m rows of A, in bytes.  Rows are padded so that eight rows'
@@ -330,11 +316,17 @@ cudaError_t w4_launch_group(const W4Args& a, int sms, cudaStream_t stream)
 template <bool BF16>
 cudaError_t w4_launch_type(const W4Args& a, int sms, cudaStream_t stream)
 {
+    const long long weights = static_cast<long long>(a.n) * a.k;
+    // up to 4 rows of a large weight: without the stages in shared memory (one row, groups of
+    // 128: 8192x8192 10.6 us there, 12.4 here, 4096x4096 4.3 and 4.4, 4096x1024 2.8 and 2.3;
+    // groups of 64: 8192x8192 12.1 and 12.9, 5120x5120 8.2 and 8.2; 8 rows 16.0 and 13.9)
+    if (a.m <= 4 && a.group >= 64 && weights >= (a.group == 128 ? 20ll : 60ll) << 20)
+        return w4_stream_launch(a, BF16, sms, stream);
     if (a.m <= 4) return w4_launch_group<BF16, 1, 2, 1, 4>(a, sms, stream);
     if (a.m <= 8) return w4_launch_group<BF16, 1, 2, 1, 3>(a, sms, stream);
     // 9 to 16 rows: this kernel's second tile of rows costs a small weight less than tcgen05's
     // longer start (4096x1024: 4.4 us here, 6.0 there), a large one more (8192x8192: 26.8, 18.4)
-    if (a.m <= 16 && static_cast<long long>(a.n) * a.k <= 12ll << 20)
+    if (a.m <= 16 && weights <= 12ll << 20)
         return w4_launch_group<BF16, 2, 1, 4, 4>(a, sms, stream);
     return w4_tensor_launch(a, BF16, sms, stream);
 }

@@ -1,0 +1,310 @@
+// Products with a large 4-bit weight for up to 4 rows of A: the weight streams from memory straight
+// to the registers of the warps that multiply it.
+//
+// D^T = W A^T with W's rows (columns of D) as the 16 MMA rows of mma.m16n8k16 and the rows of A as
+// its 8 columns, as in the kernel that stages everything in shared memory (w4.cu).  Bound by the
+// weight's bytes and, near them, by the instructions that unpack it; so what surrounds those is
+// kept small:
+//
+//   * A block takes 32 columns of D, its eight warps every eighth 128 values of k.  A lane loads
+//     its own words of its four rows (16 or 8 bytes at a time: as much as keeps the lanes of an
+//     MMA inside one group of the scales), three blocks of 128 k ahead, in registers; no barrier
+//     and no copy through shared memory.  The order of k inside an MMA is free as long as both
+//     operands have it.
+//   * The rows of A, scales and zero points of a long stretch of k are put in shared memory once,
+//     A in the order that the unpacked words come in (eight values of k as the pairs (j, j + 4)),
+//     so that one 16-byte load serves two MMAs.
+//   * A group's sum is complete in the accumulator, so the scale multiplies an fp32 sum, and
+//     no weight is ever rounded.
+//   * The warps' sums meet in shared memory in order, those of a cluster that splits k over
+//     distributed shared memory; then the epilogue.
+// Measured (bf16, groups of 128, one row; the staged kernel in brackets): 8192 columns, k 16384
+// 18.0 us (22.7), 16384 x 8192 20.7 (23.4), 8192 x 8192 10.6 (12.4), 5120 x 5120 6.8 (8.0);
+// 4096 x 1024 2.8 (2.3: its longer code and its first barrier cost a short call more).  57 % of
+// the copy rate at best; the 256 blocks of 8192 columns leave 48 of 152 SMs with one block where
+// the others have two.  Two steps ahead 19.9, four (168 registers' worth in 128) 21.9.
+#include "kernel_params.h"
+#include "launch.h"
+#include "ptx.cuh"
+#include "vec16.cuh"
+#include "w4_mma.cuh"
+#include "w4_unpack.cuh"
+
+namespace gemm_epi {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kCols = 32;                     // columns of D per block
+constexpr int kBlockK = 128;                  // k per warp at a time
+constexpr int kStepK = kWarps * kBlockK;      // k per step of the block
+constexpr int kAhead = 3;                     // steps loaded ahead
+constexpr int kUnroll = kAhead + 1;
+constexpr int kMaxSmem = 100 * 1024;          // two blocks per SM
+
+// Words (8 values of k) of a lane in a block of 128 k: word i of lane t holds k = k_of(t, i) ..
+// + 7.  With groups of 128 a lane has 32 consecutive values, of 64 twice 16.
+template <int G>
+__device__ __forceinline__ int k_of(int t, int i)
+{
+    static_assert(G == 128 || G == 64, "groups");
+    return G == 128 ? 32 * t + 8 * i : 64 * (i >> 1) + 16 * t + 8 * (i & 1);
+}
+
+// The four words of one row (src: the row's first byte of the block), zeros from `left` on.
+template <int G>
+__device__ __forceinline__ void load_words(const uint8_t* src, int t, int left, uint32_t (&w)[4])
+{
+    if constexpr (G == 128) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + t * 16));
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint2 v = make_uint2(0, 0);
+            if (64 * h < left) v = __ldg(reinterpret_cast<const uint2*>(src + 32 * h + t * 8));
+            w[2 * h] = v.x;
+            w[2 * h + 1] = v.y;
+        }
+    }
+}
+
+// Shared memory of a segment of `steps` steps for m rows of A.  A row is padded, and with groups of
+// 128 its 16-byte pieces exchanged in pairs, so that the eight lanes that read at a time (two rows,
+// four pieces) find eight different banks.
+template <int G>
+struct Segment {
+    static constexpr int kPad = G == 128 ? 32 : 16;
+    static constexpr int kGroups = kStepK / G;  // per step
+    static __host__ __device__ int pitch(int steps) { return steps * kStepK * 2 + kPad; }
+    static __host__ __device__ int scales(int m, int steps) { return (m * pitch(steps) + 15) / 16 * 16; }
+    static __host__ __device__ int zeros(int m, int steps) { return scales(m, steps) + steps * kGroups * kCols * 2; }
+    static __host__ __device__ int bytes(int m, int steps) { return zeros(m, steps) + steps * kGroups * kCols; }
+};
+
+template <bool BF16, int G>
+__global__ void __launch_bounds__(kThreads, 2) w4_stream_kernel(const W4Args a, int cluster, int seg_steps)
+{
+    using S = Segment<G>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r = lane >> 2, t = lane & 3;
+    const int rank = static_cast<int>(blockIdx.x) % cluster;
+    const int n0 = static_cast<int>(blockIdx.x) / cluster * kCols;
+    const int all_steps = (a.k + kStepK - 1) / kStepK;
+    const int first = static_cast<int>(static_cast<long long>(all_steps) * rank / cluster);
+    const int steps = static_cast<int>(static_cast<long long>(all_steps) * (rank + 1) / cluster) - first;
+    const int k0 = first * kStepK + warp * kBlockK;  // this warp's first
+    const int mine = min(steps, (a.k - k0 + kStepK - 1) / kStepK);  // steps in which it has any
+
+    const uint8_t* src[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)  // (columns past n: the last one's, whose sums nobody reads)
+        src[q] = static_cast<const uint8_t*>(a.W) +
+                 (static_cast<long long>(min(n0 + q * 8 + r, a.n - 1)) * a.k + k0) / 2;
+    int load_left = a.k - k0, loaded = 0;
+    uint32_t w[kUnroll][4][4];
+    auto load = [&](uint32_t (&to)[4][4]) {
+        if (loaded < mine) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                load_words<G>(src[q], t, load_left, to[q]);
+                src[q] += kStepK / 2;
+            }
+        }
+        load_left -= kStepK;
+        ++loaded;
+    };
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load(w[u]);
+
+    float total[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) total[i][e] = 0.0f;
+
+    for (int seg = 0; seg < steps; seg += seg_steps) {
+        const int count = min(seg_steps, steps - seg);
+        const int kseg = (first + seg) * kStepK;
+        const int pitch = S::pitch(count), o_scales = S::scales(a.m, count), o_zeros = S::zeros(a.m, count);
+        if (seg > 0) __syncthreads();  // every warp is done with the segment before
+        // scales and zero points: 8 columns of one group at a time
+        const int groups = count * S::kGroups, g0 = kseg / G, g_end = a.k / G;
+        for (int i = tid; i < groups * (kCols / 8); i += kThreads) {
+            const int g = i / (kCols / 8), c = i % (kCols / 8) * 8;
+            uint8_t* s_at = smem + o_scales + (g * kCols + c) * 2;
+            if (g0 + g < g_end && n0 + c < a.n) {
+                const long long at = static_cast<long long>(g0 + g) * a.n + n0 + c;
+                cp_async_16(smem_u32(s_at), static_cast<const uint16_t*>(a.scales) + at);
+                if (a.zeros) cp_async_8(smem_u32(smem + o_zeros + g * kCols + c), a.zeros + at);
+            } else {
+                *reinterpret_cast<uint4*>(s_at) = make_uint4(0, 0, 0, 0);
+            }
+        }
+        // rows of A: 8 values at a time, four loads in flight per thread
+        const int chunks = count * (kStepK / 8);
+        int row = 0, c = tid;
+        while (c >= chunks) {
+            c -= chunks;
+            ++row;
+        }
+        while (row < a.m) {
+            uint4 v[4];
+            int to[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                to[j] = -1;
+                v[j] = make_uint4(0, 0, 0, 0);  // (zeros past the end of k)
+                if (row < a.m) {
+                    to[j] = row * pitch + (G == 128 ? c ^ (c >> 3 & 1) : c) * 16;
+                    if (kseg + c * 8 < a.k)
+                        v[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.A) +
+                                                                    static_cast<long long>(row) * a.k + kseg + c * 8));
+                }
+                c += kThreads;
+                while (c >= chunks) {
+                    c -= chunks;
+                    ++row;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (to[j] >= 0)
+                    *reinterpret_cast<uint4*>(smem + to[j]) =
+                        make_uint4(__byte_perm(v[j].x, v[j].z, 0x5410), __byte_perm(v[j].x, v[j].z, 0x7632),
+                                   __byte_perm(v[j].y, v[j].w, 0x5410), __byte_perm(v[j].y, v[j].w, 0x7632));
+        }
+        cp_async_wait_all();
+        __syncthreads();
+        // (rows past m: columns of the product that nobody reads)
+        const uint8_t* act = smem + min(r, a.m - 1) * pitch + warp * (kBlockK * 2);
+        const uint8_t* sp = smem + o_scales + (warp * (kBlockK / G) * kCols + r) * 2;
+        const uint8_t* zp = smem + o_zeros + warp * (kBlockK / G) * kCols + r;
+        for (int s4 = seg; s4 < seg + count; s4 += kUnroll) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (s4 + u >= mine || s4 + u >= seg + count) break;
+                load(w[(u + kAhead) % kUnroll]);
+                float part[2][4];
+                W4Unpack<BF16> unpack[2][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    constexpr int kWords = G / 32;  // of a lane in a group
+                    const int g = i / kWords;
+                    if (i % kWords == 0) {
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt) {
+                            unpack[mt][0].set(a.zeros ? zp[g * kCols + mt * 16] : 8u);
+                            unpack[mt][1].set(a.zeros ? zp[g * kCols + mt * 16 + 8] : 8u);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) part[mt][e] = 0.0f;
+                        }
+                    }
+                    const int c = k_of<G>(t, i) / 8;
+                    const uint4 b = *reinterpret_cast<const uint4*>(act + (G == 128 ? c ^ (c >> 3 & 1) : c) * 16);
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        uint32_t p[4], q[4];
+                        unpack[mt][0](w[u][2 * mt][i], p);
+                        unpack[mt][1](w[u][2 * mt + 1][i], q);
+                        mma_16816<BF16>(part[mt], p[0], q[0], p[1], q[1], b.x, b.y);
+                        mma_16816<BF16>(part[mt], p[2], q[2], p[3], q[3], b.z, b.w);
+                    }
+                    if ((i + 1) % kWords == 0) {
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt) {
+                            const uint16_t* s16 = reinterpret_cast<const uint16_t*>(sp) + g * kCols + mt * 16;
+                            const float s0 = decode16<BF16>(s16[0]), s1 = decode16<BF16>(s16[8]);
+                            total[mt][0] = fmaf(part[mt][0], s0, total[mt][0]);
+                            total[mt][1] = fmaf(part[mt][1], s0, total[mt][1]);
+                            total[mt][2] = fmaf(part[mt][2], s1, total[mt][2]);
+                            total[mt][3] = fmaf(part[mt][3], s1, total[mt][3]);
+                        }
+                    }
+                }
+                act += kStepK * 2;
+                sp += S::kGroups * kCols * 2;
+                zp += S::kGroups * kCols;
+            }
+        }
+    }
+
+    // The warps' sums: [warp][row of A][column], then one thread per element adds them in order.
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem);
+    constexpr int kRedRow = kCols + 1;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            red[(warp * 8 + 2 * t + (e & 1)) * kRedRow + mt * 16 + r + (e >> 1) * 8] = total[mt][e];
+    __syncthreads();
+    const int elements = a.m * kCols;  // (at most one per thread)
+    float v = 0.0f;
+    const int row = tid / kCols, col = n0 + tid % kCols, at_red = row * kRedRow + tid % kCols;
+    if (tid < elements) {
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) v += red[q * 8 * kRedRow + at_red];
+    }
+    if (cluster > 1) {
+        if (tid < elements) red[at_red] = v;  // (its own eight values: no other thread reads them)
+        cluster_sync_all();
+        if (tid < elements && tid % cluster == rank) {
+            v = 0.0f;
+            for (int q = 0; q < cluster; ++q) v += ld_shared_cluster_f32(map_shared_rank(sbase + at_red * 4, q));
+        }
+    }
+    if (tid < elements && tid % cluster == rank && col < a.n) {
+        const long long at = static_cast<long long>(row) * a.n + col;
+        if (a.bias) v += decode16<BF16>(static_cast<const uint16_t*>(a.bias)[col]);
+        const float res = a.residual ? decode16<BF16>(static_cast<const uint16_t*>(a.residual)[at]) : 0.0f;
+        static_cast<uint16_t*>(a.D)[at] = encode16<BF16>(w4_epilogue(v, a.epilog, res));
+    }
+    if (cluster > 1) cluster_sync_all();  // the peers' shared memory stays until it is read
+}
+
+template <bool BF16, int G>
+cudaError_t launch_one(const W4Args& a, int sms, cudaStream_t stream)
+{
+    using S = Segment<G>;
+    auto kernel = w4_stream_kernel<BF16, G>;
+    static std::atomic<unsigned long long> prepared;
+    const cudaError_t e = allow_smem(kernel, kMaxSmem, prepared);
+    if (e != cudaSuccess) return e;
+    const int steps = (a.k + kStepK - 1) / kStepK, tiles = (a.n + kCols - 1) / kCols;
+    // k split over a cluster while that leaves an SM for every block
+    int cluster = 1;
+    while (cluster < 8 && tiles * cluster * 2 <= sms && steps >= 2 * cluster) cluster *= 2;
+    int seg = ((steps + cluster - 1) / cluster + kUnroll - 1) / kUnroll * kUnroll;
+    if (seg < kUnroll) seg = kUnroll;
+    while (S::bytes(a.m, seg) > kMaxSmem) seg -= kUnroll;
+    int smem = S::bytes(a.m, seg);
+    constexpr int kRed = kWarps * 8 * (kCols + 1) * 4;
+    if (smem < kRed) smem = kRed;
+    return launch_dependent(kernel, tiles * cluster, kThreads, smem, stream, cluster, a, cluster, seg);
+}
+
+template <bool BF16>
+cudaError_t launch_type(const W4Args& a, int sms, cudaStream_t stream)
+{
+    if (a.group == 64) return launch_one<BF16, 64>(a, sms, stream);
+    return launch_one<BF16, 128>(a, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t w4_stream_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream)
+{
+    return bf16 ? launch_type<true>(a, sm_count, stream) : launch_type<false>(a, sm_count, stream);
+}
+
+}  // namespace gemm_epi

@@ -61,6 +61,32 @@ def test_w4_larger_weights(m, n, k, group):
     _check(ref.w4_problem(m, n, k, group, dtype, group != 64, m + n), group, dtype, epilog)
 
 
+@pytest.mark.parametrize("m,n,k,group", [(1, 5128, 4224, 128), (4, 2056, 10368, 128), (2, 264, 81920, 128),
+                                         (3, 21856, 1024, 128), (1, 40, 600064, 128), (3, 4104, 15424, 64),
+                                         (4, 512, 122944, 64)])
+@pytest.mark.parametrize("dtype,zeros", [("bf16", False), ("f16", True)])
+def test_w4_few_rows_of_a_large_weight(m, n, k, group, dtype, zeros):
+    _check(ref.w4_problem(m, n, k, group, dtype, zeros, m + n), group, dtype, "BIAS_RESIDUAL" if zeros else "TANH_BIAS")
+
+
+def test_w4_few_rows_of_a_large_weight_exact_and_untouched():
+    # integers as above at the larger sizes, and rows behind the last left as they were
+    g = torch.Generator().manual_seed(3)
+    m, n, k = 3, 1032, 21248
+    for group in (128, 64):
+        n = 1032 if group == 128 else 2968
+        q = torch.full((n, k), 8)
+        at = torch.randint(0, k, (n, 9), generator=g)
+        q.scatter_(1, at, torch.randint(0, 16, (n, 9), generator=g))
+        A = torch.randint(-2, 3, (m, k), generator=g).to(torch.bfloat16)
+        p = dict(q=q, W=ref.w4_pack(q), scales=torch.ones(k // group, n, dtype=torch.bfloat16), zeros=None, A=A,
+                 bias=None, R=None)
+        D = torch.full((m + 2, n), 7.0, dtype=torch.bfloat16, device="cuda")
+        _run(p, group, "bf16", "NONE", D=D[:m])
+        want = A.double() @ ref.w4_weight(q, p["scales"], None, group)
+        assert torch.equal(D[:m].double().cpu(), want) and (D[m:] == 7.0).all()
+
+
 @pytest.mark.parametrize("epilog", EPILOGS)
 @pytest.mark.parametrize("m", [1, 5, 12, 40])
 @pytest.mark.parametrize("zeros", [False, True])
