@@ -86,33 +86,29 @@ struct Segment {
     static __host__ __device__ int bytes(int m, int steps) { return zeros(m, steps) + steps * kGroups * kCols; }
 };
 
-template <bool BF16, int G>
-__global__ void __launch_bounds__(kThreads, 2) w4_stream_kernel(const W4Args a, int cluster, int seg_steps)
+// The sums of this block's share of k: NQ groups of 8 columns (MMA rows 0-7, 8-15 of one or two
+// MMAs; the upper half of the last is zeros where NQ is odd).
+template <bool BF16, int G, int NQ>
+__device__ __forceinline__ void stream_columns(const W4Args& a, uint8_t* smem, int n0, int first, int steps,
+                                               int seg_steps, float (&total)[2][4])
 {
     using S = Segment<G>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    const uint32_t sbase = smem_u32(smem);
+    constexpr int kMT = (NQ + 1) / 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, t = lane & 3;
-    const int rank = static_cast<int>(blockIdx.x) % cluster;
-    const int n0 = static_cast<int>(blockIdx.x) / cluster * kCols;
-    const int all_steps = (a.k + kStepK - 1) / kStepK;
-    const int first = static_cast<int>(static_cast<long long>(all_steps) * rank / cluster);
-    const int steps = static_cast<int>(static_cast<long long>(all_steps) * (rank + 1) / cluster) - first;
     const int k0 = first * kStepK + warp * kBlockK;  // this warp's first
     const int mine = min(steps, (a.k - k0 + kStepK - 1) / kStepK);  // steps in which it has any
 
-    const uint8_t* src[4];
+    const uint8_t* src[NQ];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)  // (columns past n: the last one's, whose sums nobody reads)
-        src[q] = static_cast<const uint8_t*>(a.W) +
-                 (static_cast<long long>(min(n0 + q * 8 + r, a.n - 1)) * a.k + k0) / 2;
+    for (int q = 0; q < NQ; ++q)
+        src[q] = static_cast<const uint8_t*>(a.W) + (static_cast<long long>(n0 + q * 8 + r) * a.k + k0) / 2;
     int load_left = a.k - k0, loaded = 0;
-    uint32_t w[kUnroll][4][4];
-    auto load = [&](uint32_t (&to)[4][4]) {
+    uint32_t w[kUnroll][NQ][4];
+    auto load = [&](uint32_t (&to)[NQ][4]) {
         if (loaded < mine) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < NQ; ++q) {
                 load_words<G>(src[q], t, load_left, to[q]);
                 src[q] += kStepK / 2;
             }
@@ -126,12 +122,6 @@ __global__ void __launch_bounds__(kThreads, 2) w4_stream_kernel(const W4Args a, 
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) load(w[u]);
 
-    float total[2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) total[i][e] = 0.0f;
-
     for (int seg = 0; seg < steps; seg += seg_steps) {
         const int count = min(seg_steps, steps - seg);
         const int kseg = (first + seg) * kStepK;
@@ -142,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_stream_kernel(const W4Args a, 
         for (int i = tid; i < groups * (kCols / 8); i += kThreads) {
             const int g = i / (kCols / 8), c = i % (kCols / 8) * 8;
             uint8_t* s_at = smem + o_scales + (g * kCols + c) * 2;
-            if (g0 + g < g_end && n0 + c < a.n) {
+            if (g0 + g < g_end && c < NQ * 8) {
                 const long long at = static_cast<long long>(g0 + g) * a.n + n0 + c;
                 cp_async_16(smem_u32(s_at), static_cast<const uint16_t*>(a.scales) + at);
                 if (a.zeros) cp_async_8(smem_u32(smem + o_zeros + g * kCols + c), a.zeros + at);
@@ -194,15 +184,15 @@ __global__ void __launch_bounds__(kThreads, 2) w4_stream_kernel(const W4Args a, 
             for (int u = 0; u < kUnroll; ++u) {
                 if (s4 + u >= mine || s4 + u >= seg + count) break;
                 load(w[(u + kAhead) % kUnroll]);
-                float part[2][4];
-                W4Unpack<BF16> unpack[2][2];
+                float part[kMT][4];
+                W4Unpack<BF16> unpack[kMT][2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     constexpr int kWords = G / 32;  // of a lane in a group
                     const int g = i / kWords;
                     if (i % kWords == 0) {
 #pragma unroll
-                        for (int mt = 0; mt < 2; ++mt) {
+                        for (int mt = 0; mt < kMT; ++mt) {
                             unpack[mt][0].set(a.zeros ? zp[g * kCols + mt * 16] : 8u);
                             unpack[mt][1].set(a.zeros ? zp[g * kCols + mt * 16 + 8] : 8u);
 #pragma unroll
@@ -212,16 +202,20 @@ __global__ void __launch_bounds__(kThreads, 2) w4_stream_kernel(const W4Args a, 
                     const int c = k_of<G>(t, i) / 8;
                     const uint4 b = *reinterpret_cast<const uint4*>(act + (G == 128 ? c ^ (c >> 3 & 1) : c) * 16);
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        uint32_t p[4], q[4];
+                    for (int mt = 0; mt < kMT; ++mt) {
+                        uint32_t p[4], q[4] = {0, 0, 0, 0};
                         unpack[mt][0](w[u][2 * mt][i], p);
-                        unpack[mt][1](w[u][2 * mt + 1][i], q);
+                        if constexpr (NQ % 2 == 0) {
+                            unpack[mt][1](w[u][2 * mt + 1][i], q);
+                        } else {
+                            if (2 * mt + 1 < NQ) unpack[mt][1](w[u][2 * mt + 1 < NQ ? 2 * mt + 1 : 0][i], q);
+                        }
                         mma_16816<BF16>(part[mt], p[0], q[0], p[1], q[1], b.x, b.y);
                         mma_16816<BF16>(part[mt], p[2], q[2], p[3], q[3], b.z, b.w);
                     }
                     if ((i + 1) % kWords == 0) {
 #pragma unroll
-                        for (int mt = 0; mt < 2; ++mt) {
+                        for (int mt = 0; mt < kMT; ++mt) {
                             const uint16_t* s16 = reinterpret_cast<const uint16_t*>(sp) + g * kCols + mt * 16;
                             const float s0 = decode16<BF16>(s16[0]), s1 = decode16<BF16>(s16[8]);
                             total[mt][0] = fmaf(part[mt][0], s0, total[mt][0]);
@@ -237,6 +231,34 @@ __global__ void __launch_bounds__(kThreads, 2) w4_stream_kernel(const W4Args a, 
             }
         }
     }
+}
+
+template <bool BF16, int G>
+__global__ void __launch_bounds__(kThreads, 2) w4_stream_kernel(const W4Args a, int cluster, int seg_steps)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r = lane >> 2, t = lane & 3;
+    const int rank = static_cast<int>(blockIdx.x) % cluster;
+    // this block's columns: the n / 8 groups of 8 spread evenly over the blocks, 1 to 4 each
+    const int tile = static_cast<int>(blockIdx.x) / cluster, tiles = static_cast<int>(gridDim.x) / cluster;
+    const int each = a.n / 8 / tiles, more = a.n / 8 % tiles;
+    const int n0 = (tile * each + min(tile, more)) * 8, nq = each + (tile < more);
+    const int all_steps = (a.k + kStepK - 1) / kStepK;
+    const int first = static_cast<int>(static_cast<long long>(all_steps) * rank / cluster);
+    const int steps = static_cast<int>(static_cast<long long>(all_steps) * (rank + 1) / cluster) - first;
+    float total[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) total[i][e] = 0.0f;
+    switch (nq) {
+    case 4: stream_columns<BF16, G, 4>(a, smem, n0, first, steps, seg_steps, total); break;
+    case 3: stream_columns<BF16, G, 3>(a, smem, n0, first, steps, seg_steps, total); break;
+    case 2: stream_columns<BF16, G, 2>(a, smem, n0, first, steps, seg_steps, total); break;
+    default: stream_columns<BF16, G, 1>(a, smem, n0, first, steps, seg_steps, total); break;
+    }
 
     // The warps' sums: [warp][row of A][column], then one thread per element adds them in order.
     __syncthreads();
@@ -251,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_stream_kernel(const W4Args a, 
     const int elements = a.m * kCols;  // (at most one per thread)
     float v = 0.0f;
     const int row = tid / kCols, col = n0 + tid % kCols, at_red = row * kRedRow + tid % kCols;
+    const bool stored = tid < elements && tid % cluster == rank && tid % kCols < nq * 8;
     if (tid < elements) {
 #pragma unroll
         for (int q = 0; q < kWarps; ++q) v += red[q * 8 * kRedRow + at_red];
@@ -258,12 +281,12 @@ __global__ void __launch_bounds__(kThreads, 2) w4_stream_kernel(const W4Args a, 
     if (cluster > 1) {
         if (tid < elements) red[at_red] = v;  // (its own eight values: no other thread reads them)
         cluster_sync_all();
-        if (tid < elements && tid % cluster == rank) {
+        if (stored) {
             v = 0.0f;
             for (int q = 0; q < cluster; ++q) v += ld_shared_cluster_f32(map_shared_rank(sbase + at_red * 4, q));
         }
     }
-    if (tid < elements && tid % cluster == rank && col < a.n) {
+    if (stored) {
         const long long at = static_cast<long long>(row) * a.n + col;
         if (a.bias) v += decode16<BF16>(static_cast<const uint16_t*>(a.bias)[col]);
         const float res = a.residual ? decode16<BF16>(static_cast<const uint16_t*>(a.residual)[at]) : 0.0f;
@@ -280,10 +303,17 @@ cudaError_t launch_one(const W4Args& a, int sms, cudaStream_t stream)
     static std::atomic<unsigned long long> prepared;
     const cudaError_t e = allow_smem(kernel, kMaxSmem, prepared);
     if (e != cudaSuccess) return e;
-    const int steps = (a.k + kStepK - 1) / kStepK, tiles = (a.n + kCols - 1) / kCols;
-    // k split over a cluster while that leaves an SM for every block
+    const int steps = (a.k + kStepK - 1) / kStepK;
+    int tiles = (a.n + kCols - 1) / kCols;
+    // k split over a cluster while that leaves an SM for every block; otherwise as many blocks as
+    // give every SM the same number, the columns spread evenly over them (5120 columns: 304 blocks
+    // of 16 or 24 columns, not 160 of 32 on 152 SMs)
     int cluster = 1;
     while (cluster < 8 && tiles * cluster * 2 <= sms && steps >= 2 * cluster) cluster *= 2;
+    if (cluster == 1) {
+        tiles = (tiles + sms - 1) / sms * sms;
+        if (tiles > a.n / 8) tiles = a.n / 8;
+    }
     int seg = ((steps + cluster - 1) / cluster + kUnroll - 1) / kUnroll * kUnroll;
     if (seg < kUnroll) seg = kUnroll;
     while (S::bytes(a.m, seg) > kMaxSmem) seg -= kUnroll;
