@@ -28,6 +28,7 @@ decltype(&gemm_epi_dropout) p_dropout;
 struct Args {
     PyObject* const* args;
     bool bad = false;
+    int device = -1;  // the current device, asked for once a call
 
     void* fail(PyObject* type, const char* what)
     {
@@ -36,7 +37,7 @@ struct Args {
         return nullptr;
     }
 
-    // A CUDA tensor's first element, a raw address, or None.
+    // The first element of a tensor on the current device, a raw address, or None.
     void* pointer(int i)
     {
         PyObject* o = args[i];
@@ -44,6 +45,9 @@ struct Args {
         if (THPVariable_Check(o)) {
             const at::Tensor& t = THPVariable_Unpack(o);
             if (!t.is_cuda()) return fail(PyExc_ValueError, "tensors must be CUDA tensors");
+            if (device < 0) device = c10::cuda::current_device();
+            if (t.get_device() != device)
+                return fail(PyExc_ValueError, "tensors must be on the current CUDA device");
             if (!t.is_contiguous()) return fail(PyExc_ValueError, "tensors must be contiguous (row-major)");
             return t.data_ptr();
         }

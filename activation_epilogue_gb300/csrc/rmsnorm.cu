@@ -607,7 +607,7 @@ cudaError_t rmsnorm_launch_width(const RmsnormArgs& a, cudaStream_t stream)
     // A block per row (four for T = 32): 16384x8192 with E4M3 rows 133 us, against 145-163 with
     // 304 to 1024 blocks that walk the rows.  The first pass of the tensor scale walks, since
     // its blocks' maxima are read by every block of the second.
-    const int grid = even_grid(a.t, kRows, a.mode == kRmsTensor ? 912 : 1ll << 31);
+    const int grid = even_grid(a.t, kRows, a.mode == kRmsTensor ? 912 : (1ll << 31) - 1);
     switch (a.mode) {
     case kRms16: return launch_dependent(rmsnorm_kernel<BF16, T, V, kRms16>, grid, kBlock, 0, stream, 1, a);
     case kRmsRow: return launch_dependent(rmsnorm_kernel<BF16, T, V, kRmsRow>, grid, kBlock, 0, stream, 1, a);

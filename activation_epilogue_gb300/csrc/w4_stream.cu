@@ -6,8 +6,9 @@
 // weight's bytes and, near them, by the instructions that unpack it; so what surrounds those is
 // kept small:
 //
-//   * A block takes 32 columns of D, its eight warps every eighth 128 values of k.  A lane loads
-//     its own words of its four rows (16 or 8 bytes at a time: as much as keeps the lanes of an
+//   * A block takes 8 to 32 columns of D, in groups of 8 spread evenly over blocks that are a
+//     multiple of the SMs, and its eight warps every eighth 128 values of k.  A lane loads
+//     its own words of its rows (one in each group) (16 or 8 bytes at a time: as much as keeps the lanes of an
 //     MMA inside one group of the scales), three blocks of 128 k ahead, in registers; no barrier
 //     and no copy through shared memory.  The order of k inside an MMA is free as long as both
 //     operands have it.
@@ -19,10 +20,12 @@
 //   * The warps' sums meet in shared memory in order, those of a cluster that splits k over
 //     distributed shared memory; then the epilogue.
 // Measured (bf16, groups of 128, one row; the staged kernel in brackets): 8192 columns, k 16384
-// 18.0 us (22.7), 16384 x 8192 20.7 (23.4), 8192 x 8192 10.6 (12.4), 5120 x 5120 6.8 (8.0);
-// 4096 x 1024 2.8 (2.3: its longer code and its first barrier cost a short call more).  57 % of
-// the copy rate at best; the 256 blocks of 8192 columns leave 48 of 152 SMs with one block where
-// the others have two.  Two steps ahead 19.9, four (168 registers' worth in 128) 21.9.
+// 18.0 us (22.7), 16384 x 8192 20.7 (23.4), 8192 x 8192 10.6 (12.4), 5120 x 5120 5.5 (8.0);
+// 4096 x 1024 2.8 (2.3: its longer code and its first barrier cost a short call more).  For
+// 8192 columns with k 16384 that is 57 % of the copy rate; the loads alone take 14.9 us (a kernel
+// that only reads as many bytes in order: 14.3), the arithmetic alone 14.9.  Two steps ahead
+// 19.9, four (168 registers' worth in 128) 21.9; several blocks of 128 k in a row per warp, for
+// longer pieces of a row of W, 18.9 to 19.1.
 #include "kernel_params.h"
 #include "launch.h"
 #include "ptx.cuh"

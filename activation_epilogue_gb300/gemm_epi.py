@@ -181,14 +181,22 @@ def _ptr(t):
 
 
 def _dev(t):
-    """As _ptr, for calls that run without a plan: a tensor of another device is refused."""
+    """As _ptr, for calls that run without a plan, on the current device: a tensor of the host or
+    of another device is refused."""
     if t is None or isinstance(t, int):
         return t
     if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
+    if t.get_device() != _current_device():
+        raise ValueError("tensors must be on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous (row-major)")
     return t.data_ptr()
+
+
+def _current_device():
+    import torch
+    return torch.cuda.current_device()
 
 
 def _stream(stream):

@@ -145,6 +145,27 @@ def test_binding_refuses_tensors_it_cannot_pass():
         gemm_epi.gemm_epi_dropout(256, "bf16", x, None, 0.5, 1, 2, x, stream=0)
 
 
+def test_binding_refuses_tensors_of_another_device(monkeypatch):
+    class Tensor:
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return P
+
+    monkeypatch.setattr(gemm_epi, "_current_device", lambda: 0)
+    slow = gemm_epi._CtypesCalls(gemm_epi.load_library())
+    with pytest.raises(ValueError, match="current CUDA device"):
+        slow.dropout(0, 1, Tensor(), None, 0.5, 1, 2, None, P, 0)
+    monkeypatch.setattr(gemm_epi, "_current_device", lambda: 1)
+    assert slow.dropout(0, 1, Tensor(), None, 0.5, 1, 2, None, P, 0) == 0
+
+
 def test_both_marshalling_paths_agree():
     """The C marshalling is there (its sources build with the library) and answers as the ctypes
     path does: the same statuses, the same refusals of arguments."""
