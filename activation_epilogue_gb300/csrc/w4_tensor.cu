@@ -11,24 +11,25 @@
 //
 //   * The producer (one thread) copies blocks of 128 k of A by TMA (128-byte swizzle, rows past
 //     m and k past the end read as zeros).
-//   * Four chains take every fourth block each, with a block of tensor memory (two halves), one
-//     or two accumulators and an issuing thread of their own.  (One issuer's own instructions
-//     took 1300 cycles a block, nearly all of a call: 48 us for 16384x8192 with 48 rows; two
-//     chains 31 us, four 26.6.)
+//   * Four chains (three with groups below 128) take every fourth block each, with a block of
+//     tensor memory (two halves), one or two accumulators and an issuing warp of their own.
+//     (One issuer's own instructions took 1300 cycles a block, nearly all of a call: 48 us for
+//     16384x8192 with 48 rows; two chains 31 us, four 26.6, and 25.1 with a group's MMAs issued
+//     in a row, without a check between them.)
 //   * A chain's four unpacking warps have a quarter of the 128 rows each: a block's 2 KB of a
 //     quarter come through a ring of the warp's own in shared memory (cp.async, no barrier but
 //     the warp's), each thread unpacks its row's 64 bytes to q - z, exactly, two neighbouring k
 //     per 32-bit word, and stores them to tensor memory, half a block at a time.
 //   * The chain's issuer runs the MMAs of one group of the scales after another.
-//   * Eight warps (a quarter of the lanes, half of the rows of A each) read the groups' sums, of
-//     the chains in turn, multiply them by the group's scales (one per lane: the lane is the
+//   * Eight warps (a quarter of the lanes, half of the rows of A each), with groups below 128 two
+//     times eight with every other group each, read the groups' sums, of the chains in turn, multiply them by the group's scales (one per lane: the lane is the
 //     column of D) and add them up in fp32, two rows of A per instruction; at the end all
 //     threads apply the epilogue and store D.
 // A chain's waits are for its own earlier blocks alone, in order, so that no wait can take an
 // older phase of a barrier for the one it needs.
-// Measured (16384x8192, bf16, 48 rows): 26.6 us with groups of 128, 32 with 64, 46 with 32
+// Measured (16384x8192, bf16, 48 rows): 25.1 us with groups of 128, 30.7 with 64, 39.8 with 32
 // (a group's hand-over from the issuer to the summing warps costs more than its MMAs); about
-// 6 us of each is start and end (4096x1024: 6.4 us), the rest 630 cycles a block of 128 x 128
+// 6 us of each is start and end (4096x1024: 6.4 us), the rest 580 cycles a block of 128 x 128
 // against some 370 for the unpacking instructions alone and for the weight's bytes.
 #include "kernel_params.h"
 #include "launch.h"
@@ -42,50 +43,59 @@ namespace {
 
 constexpr int kCols = 128;                  // columns of D per block: MMA rows
 constexpr int kBlockK = 128;                // k per block of the pipeline
-constexpr int kChains = 4;
-constexpr int kSumWarps = 8;                // warps 0-7: a quarter of the lanes, half of the rows of A
-constexpr int kUnpackWarps = 4 * kChains;   // warps 8-23: a quarter of the lanes of one chain
-constexpr int kProducerWarp = kSumWarps + kUnpackWarps;
-constexpr int kIssuerWarp = kProducerWarp + 1;  // warps 25-28, one thread each
-constexpr int kThreads = 32 * (kIssuerWarp + kChains);
+constexpr int kMostChains = 4;
 constexpr int kWDepth = 3;                  // blocks in flight per unpacking warp
-constexpr int kHalves = 2 * kChains;        // half blocks (64 k) of unpacked weight in tensor memory
-constexpr int kMaxAcc = 2 * kChains;        // accumulators
 constexpr int kMaxBSlots = 8;               // blocks of A in shared memory (most)
 constexpr int kScaleDepth = 3;              // rounds of the chains' scales in flight per summing warp
-constexpr int kTmemA = 0, kTmemAcc = 256;   // columns of tensor memory; 512 allocated
 
 // barriers (8 bytes each), then the tensor memory address and the failure flag
 enum : int {
     kAFull = 0,
-    kAEmpty = kAFull + kHalves,
-    kBFull = kAEmpty + kHalves,
+    kAEmpty = kAFull + 2 * kMostChains,
+    kBFull = kAEmpty + 2 * kMostChains,
     kBEmpty = kBFull + kMaxBSlots,
     kAccFull = kBEmpty + kMaxBSlots,
-    kAccEmpty = kAccFull + kMaxAcc,
-    kDrain = kAccEmpty + kMaxAcc,
-    kBars = kDrain + kChains
+    kAccEmpty = kAccFull + 2 * kMostChains,
+    kDrain = kAccEmpty + 2 * kMostChains,
+    kBars = kDrain + kMostChains
 };
 constexpr int kHeader = 512;
 static_assert(kBars * 8 + 8 <= kHeader, "header");
 
-// Shared memory: blocks of A, a ring of each unpacking warp (32 rows' 64 bytes of W, and the
-// groups' zero points), a ring of each summing warp (the groups' scales of its 32 columns).
 template <int NP, int G>
 struct Layout {
     static constexpr int kGroups = kBlockK / G;
+    // Warps.  With groups of 128 the unpacking bounds a call: four chains.  With smaller groups the
+    // summing does (some 240 cycles of waiting for a group, and two for each of its columns): three
+    // chains, which leave room for a second set of summing warps, each with every other group.
+    // 16384x8192 with 16, 32, 48 and 64 rows, groups of 64: 26.7, 29.0, 30.7 and 36.7 us (four
+    // chains and one set 27.3, 29.9, 33.6, 36.7), of 32: 31.4, 34.9, 39.8, 51.5 (39.7, 44.2, 47.1, 54.8).
+    static constexpr int kChains = G == 128 ? 4 : 3;
+    static constexpr int kSets = G == 128 ? 1 : 2;
+    static constexpr int kSumWarps = 8 * kSets;       // set, half of the rows of A, quarter of the lanes
+    static constexpr int kUnpackWarps = 4 * kChains;  // chain, quarter of the lanes
+    static constexpr int kProducerWarp = kSumWarps + kUnpackWarps;
+    static constexpr int kIssuerWarp = kProducerWarp + 1;  // one thread each
+    static constexpr int kThreads = 32 * (kIssuerWarp + kChains);
+    // Tensor memory: a block of the unpacked weight for each chain, then its accumulators.
+    static constexpr int kTmemAcc = kChains * (kBlockK / 2);
+    static constexpr int kAccPer = 2 * kChains * NP <= 512 - kTmemAcc ? 2 : 1;
+    static constexpr int kBarPer = kAccPer > kSets ? kAccPer : kSets;  // barriers for them, in turn
+    static_assert(kChains <= kMostChains && kTmemAcc + kChains * kAccPer * NP <= 512, "tensor memory");
+    // Shared memory: blocks of A, a ring of each unpacking warp (32 rows' 64 bytes of W, and the
+    // groups' zero points), a ring of each summing warp (its groups' scales of its 32 columns).
     static constexpr int kB = NP * kBlockK * 2;
-    static constexpr int kBSlots = NP == 64 ? 4 : kMaxBSlots;  // (a multiple of the chains)
-    static constexpr int kAccPer = NP <= 32 ? 2 : 1;           // accumulators of a chain
-    static constexpr int kAccCols = 64 / kAccPer;
+    static constexpr int kBSlots = NP == 64 ? kChains : 2 * kChains;  // (a multiple of the chains)
     static constexpr int kWSlot = 32 * 64 + kGroups * 32;
-    static constexpr int kSSlot = kChains * kGroups * 64;
+    static constexpr int kSetGroups = kGroups / kSets;                // of a block, for each set
+    static constexpr int kSSlot = kChains * kSetGroups * 64;
     static constexpr int kOffW = kBSlots * kB;
     static constexpr int kOffS = kOffW + kUnpackWarps * kWDepth * kWSlot;
     static constexpr int kOffBar = kOffS + kSumWarps * kScaleDepth * kSSlot;
     static constexpr int kBytes = 1024 + kOffBar + kHeader;  // (1024: alignment)
+    static_assert(kBSlots <= kMaxBSlots, "slots");
     static_assert(kBytes <= 227 * 1024, "shared memory");
-    static_assert(kOffBar >= NP * kCols * 4, "the sums fit the rings");
+    static_assert(kOffBar >= kSets * NP * kCols * 4, "the sums fit the rings");
 };
 
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -97,6 +107,18 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 // Store 16 words of this thread's lane (no wait).
@@ -144,7 +166,7 @@ __device__ __forceinline__ void fma2(float& x, float& y, uint32_t a, uint32_t b,
 
 
 template <bool BF16, int NP, int G>
-__global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_constant__ W4Args a,
+__global__ void __launch_bounds__(Layout<NP, G>::kThreads, 1) w4_tensor_kernel(const __grid_constant__ W4Args a,
                                                                 const __grid_constant__ CUtensorMap tm_A,
                                                                 int cluster)
 {
@@ -154,6 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
     using L = Layout<NP, G>;
     constexpr int kB = L::kB, kBSlots = L::kBSlots;
     constexpr int kGroups = L::kGroups;  // per block
+    constexpr int kChains = L::kChains, kSets = L::kSets, kSumWarps = L::kSumWarps, kBarPer = L::kBarPer;
+    constexpr int kProducerWarp = L::kProducerWarp, kIssuerWarp = L::kIssuerWarp, kThreads = L::kThreads;
     const uint32_t bar0 = sbase + L::kOffBar;
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + L::kOffBar + kBars * 8);
     volatile int* failed = reinterpret_cast<volatile int*>(holder + 1);
@@ -166,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
     const int groups = min(blocks * kGroups, a.k / G - first * kGroups);  // of this block's part of k
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kHalves; ++i) {
+        for (int i = 0; i < 2 * kChains; ++i) {
             mbar_init(bar0 + 8 * (kAFull + i), 4);
             mbar_init(bar0 + 8 * (kAEmpty + i), 1);
         }
@@ -174,9 +198,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
             mbar_init(bar0 + 8 * (kBFull + i), 1);
             mbar_init(bar0 + 8 * (kBEmpty + i), 1);
         }
-        for (int i = 0; i < kMaxAcc; ++i) {
+        for (int i = 0; i < kChains * kBarPer; ++i) {
             mbar_init(bar0 + 8 * (kAccFull + i), 1);
-            mbar_init(bar0 + 8 * (kAccEmpty + i), kSumWarps);
+            mbar_init(bar0 + 8 * (kAccEmpty + i), 8);
         }
         for (int i = 0; i < kChains; ++i) mbar_init(bar0 + 8 * (kDrain + i), 1);
         *failed = 0;
@@ -218,63 +242,74 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
         }
         __syncwarp();
     } else if (warp >= kIssuerWarp) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = make_idesc_f16(BF16 ? 1u : 0u, 0u, 0u, kCols, NP);
-            bool issued = false;
-            const uint64_t desc0 = make_sdesc_sw128(sbase, 0, 1024);
-            const int chain = warp - kIssuerWarp;
-            int last = -1, n = 0;  // n: groups of this chain so far
-            int bs = chain;
-            uint32_t phase = 0, b_phase = 0;
-            bool ok = true;
-            for (int i = chain; i < blocks && ok; i += kChains, phase ^= 1) {
-                const uint64_t desc = desc0 + static_cast<uint32_t>(bs * kB >> 4);
-                uint32_t d_tmem = 0;
+        // The whole warp runs the loop, so that what the instructions take is uniform over it (in
+        // one thread's branch each MMA's operands are moved to uniform registers first); one
+        // elected lane issues.
+        const bool elected = elect_one();
+        constexpr uint32_t idesc = make_idesc_f16(BF16 ? 1u : 0u, 0u, 0u, kCols, NP);
+        bool issued = false;
+        const uint64_t desc0 = make_sdesc_sw128(sbase, 0, 1024);
+        const int chain = __shfl_sync(0xFFFFFFFFu, warp - kIssuerWarp, 0);
+        int last = -1, n = 0;  // n: groups of this chain so far
+        int bs = chain;
+        uint32_t phase = 0, b_phase = 0;
+        bool ok = true;
+        for (int i = chain; i < blocks && ok; i += kChains, phase ^= 1) {
+            const uint64_t desc = desc0 + static_cast<uint32_t>(bs * kB >> 4);
+            uint32_t d_tmem = 0;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    ok = ok && w4_wait(bar0 + 8 * (kAFull + 2 * chain + h), phase, failed);
-                    if (h == 0) ok = ok && w4_wait(bar0 + 8 * (kBFull + bs), b_phase, failed);
-                    if (!ok) break;
-                    tcgen05_fence_after_sync();
+            for (int h = 0; h < 2; ++h) {
+                ok = ok && w4_wait(bar0 + 8 * (kAFull + 2 * chain + h), phase, failed);
+                if (h == 0) ok = ok && w4_wait(bar0 + 8 * (kBFull + bs), b_phase, failed);
+                if (!ok) break;
+                tcgen05_fence_after_sync();
+                constexpr int kSteps = G / 16 < 4 ? G / 16 : 4;  // of a group, in half a block
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const int k16 = 4 * h + s;        // 16 k within the block
-                        constexpr int kSteps = G / 16;    // of a group
-                        if (i * kGroups + k16 / kSteps >= groups) break;
-                        if (k16 % kSteps == 0) {
-                            const int acc = chain * L::kAccPer + n % L::kAccPer;
-                            ok = w4_wait(bar0 + 8 * (kAccEmpty + acc), (n / L::kAccPer & 1) ^ 1, failed);
-                            if (!ok) break;
-                            tcgen05_fence_after_sync();
-                            d_tmem = tmem + kTmemAcc + acc * L::kAccCols;
-                        }
-                        mma_f16_ts(d_tmem, tmem + kTmemA + chain * 64 + k16 * 8,
-                                   desc + ((h * (kB / 2) + s * 32) >> 4), idesc, k16 % kSteps > 0);
-                        issued = true;
-                        if ((k16 + 1) % kSteps == 0) {
-                            mma_commit(bar0 + 8 * (kAccFull + chain * L::kAccPer + n % L::kAccPer));
-                            ++n;
-                        }
+                for (int s = 0; s < 4; s += kSteps) {
+                    const int k16 = 4 * h + s;  // 16 k within the block
+                    if (i * kGroups + k16 * 16 / G >= groups) break;
+                    if (k16 * 16 % G == 0) {
+                        const int before = n - L::kAccPer;  // the group that this accumulator held
+                        if (before >= 0)
+                            ok = w4_wait(bar0 + 8 * (kAccEmpty + chain * kBarPer + before % kBarPer),
+                                         before / kBarPer & 1, failed);
+                        if (!ok) break;
+                        tcgen05_fence_after_sync();
+                        d_tmem = tmem + L::kTmemAcc + (chain * L::kAccPer + n % L::kAccPer) * NP;
                     }
-                    if (!ok) break;
-                    mma_commit(bar0 + 8 * (kAEmpty + 2 * chain + h));
+                    const bool whole = (k16 + kSteps) * 16 % G == 0;  // the group ends here
+                    if (elected) {
+#pragma unroll
+                        for (int j = 0; j < kSteps; ++j)
+                            mma_f16_ts(d_tmem, tmem + chain * 64 + (k16 + j) * 8,
+                                       desc + ((h * (kB / 2) + (s + j) * 32) >> 4), idesc,
+                                       (k16 + j) * 16 % G > 0);
+                        if (whole) mma_commit(bar0 + 8 * (kAccFull + chain * kBarPer + n % kBarPer));
+                    }
+                    issued = true;
+                    if (whole) ++n;
                 }
                 if (!ok) break;
-                mma_commit(bar0 + 8 * (kBEmpty + bs));
-                last = i;
-                bs += kChains;
-                if (bs >= kBSlots) {
-                    bs -= kBSlots;
-                    b_phase ^= 1;
+                if (elected) {
+                    mma_commit(bar0 + 8 * (kAEmpty + 2 * chain + h));
+                    if (h == 1) mma_commit(bar0 + 8 * (kBEmpty + bs));
                 }
             }
-            // (the last commits arrive before the block leaves)
-            if (last >= 0 && !*failed) w4_wait(bar0 + 8 * (kBEmpty + last % kBSlots), last / kBSlots & 1, failed);
-            if (*failed && issued) {
-                // every MMA issued completes before tensor memory is released
-                mma_commit(bar0 + 8 * (kDrain + chain));
-                w4_drain(bar0 + 8 * (kDrain + chain), 0);
+            if (!ok) break;
+            last = i;
+            bs += kChains;
+            if (bs >= kBSlots) {
+                bs -= kBSlots;
+                b_phase ^= 1;
             }
+        }
+        // (the last commits arrive before the block leaves)
+        if (last >= 0 && !*failed) w4_wait(bar0 + 8 * (kBEmpty + last % kBSlots), last / kBSlots & 1, failed);
+        __syncwarp();
+        if (*failed && issued) {
+            // every MMA issued completes before tensor memory is released
+            if (elected) mma_commit(bar0 + 8 * (kDrain + chain));
+            w4_drain(bar0 + 8 * (kDrain + chain), 0);
         }
         __syncwarp();
     } else if (warp >= kSumWarps) {
@@ -314,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
             if (j < mine) fetch(j);
             cp_async_commit();
         }
-        const uint32_t t_lane = tmem + kTmemA + chain * 64 + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t t_lane = tmem + chain * 64 + (static_cast<uint32_t>(quarter * 32) << 16);
         int slot = 0, fill = kWDepth - 1;
         uint32_t phase = 1;
         bool ok = true;
@@ -355,22 +390,25 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
         cp_async_wait_group<0>();
     } else {
         // ---- the groups' sums, scaled and added ----
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, set = warp >> 3;
         const int ring = L::kOffS + warp * (kScaleDepth * L::kSSlot);
-        const int sgroup = lane >> 2, scol = (lane & 3) * 8;
-        const bool copies = sgroup < kChains * kGroups && n0 + quarter * 32 + scol < a.n;
-        constexpr int kPasses = kChains * kGroups > 8 ? kChains * kGroups / 8 : 1;
+        // group q of the set in a round of the chains' blocks: of chain q / kSetGroups
+        auto in_round = [&](int q) { return q / L::kSetGroups * kGroups + q % L::kSetGroups * kSets + set; };
+        const int scol = (lane & 3) * 8;
+        const bool copies = n0 + quarter * 32 + scol < a.n;
         const uint16_t* src = static_cast<const uint16_t*>(a.scales) +
-                              static_cast<long long>(first * kGroups + sgroup) * a.n + n0 + quarter * 32 + scol;
+                              static_cast<long long>(first * kGroups) * a.n + n0 + quarter * 32 + scol;
         const long long s_step = static_cast<long long>(kChains * kGroups) * a.n;
         const int rounds = (blocks + kChains - 1) / kChains;
-        int left = groups;  // from the next pair of blocks to copy on
+        int left = groups;  // from the next round to copy on
         auto fetch = [&](int slot) {
 #pragma unroll
-            for (int j = 0; j < kPasses; ++j)
-                if (copies && sgroup + 8 * j < left)
-                    cp_async_16(sbase + ring + slot * L::kSSlot + (sgroup + 8 * j) * 64 + scol * 2,
-                                src + static_cast<long long>(8 * j) * a.n);
+            for (int j = 0; j < kChains * L::kSetGroups; j += 8) {
+                const int q = j + (lane >> 2);
+                if (copies && q < kChains * L::kSetGroups && in_round(q) < left)
+                    cp_async_16(sbase + ring + slot * L::kSSlot + q * 64 + scol * 2,
+                                src + static_cast<long long>(in_round(q)) * a.n);
+            }
             src += s_step;
             left -= kChains * kGroups;
         };
@@ -379,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
             if (j < rounds) fetch(j);
             cp_async_commit();
         }
-        const uint32_t t_lane = tmem + kTmemAcc + (static_cast<uint32_t>(quarter * 32) << 16) + (warp >> 2) * (NP / 2);
+        const uint32_t t_lane = tmem + L::kTmemAcc + (static_cast<uint32_t>(quarter * 32) << 16) + (warp >> 2 & 1) * (NP / 2);
         for (int i = 0; i < rounds; ++i) {
             if (i + kScaleDepth - 1 < rounds) fetch((i + kScaleDepth - 1) % kScaleDepth);
             cp_async_commit();
@@ -388,19 +426,19 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
             const uint16_t* scales = reinterpret_cast<const uint16_t*>(smem + ring + (i % kScaleDepth) * L::kSSlot) + lane;
             bool ok = true;
 #pragma unroll
-            for (int p = 0; p < kChains * kGroups; ++p) {
-                const int chain = p % kChains;              // the chains in turn
-                const int in_round = chain * kGroups + p / kChains;  // group within the round of blocks
-                if (i * kChains * kGroups + in_round >= groups) continue;
-                const int n = i * kGroups + p / kChains;    // of the chain
-                const int acc = chain * L::kAccPer + n % L::kAccPer;
-                const float sc = decode16<BF16>(scales[in_round * 32]);
-                if (!w4_wait(bar0 + 8 * (kAccFull + acc), n / L::kAccPer & 1, failed)) {
+            for (int p = 0; p < kChains * L::kSetGroups; ++p) {
+                const int chain = p % kChains;  // the chains in turn
+                const int q = chain * L::kSetGroups + p / kChains;
+                if (i * kChains * kGroups + in_round(q) >= groups) continue;
+                const int n = i * kGroups + p / kChains * kSets + set;  // of the chain
+                const int bar = chain * kBarPer + n % kBarPer;
+                const float sc = decode16<BF16>(scales[q * 32]);
+                if (!w4_wait(bar0 + 8 * (kAccFull + bar), n / kBarPer & 1, failed)) {
                     ok = false;
                     break;
                 }
                 tcgen05_fence_after_sync();
-                const uint32_t t_acc = t_lane + acc * L::kAccCols;
+                const uint32_t t_acc = t_lane + (chain * L::kAccPer + n % L::kAccPer) * NP;
                 uint32_t r[2][8];
                 tmem_load_8cols_async(t_acc, r[0]);
 #pragma unroll
@@ -411,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
                     } else {
                         tcgen05_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar0 + 8 * (kAccEmpty + acc));
+                        if (lane == 0) mbar_arrive(bar0 + 8 * (kAccEmpty + bar));
                     }
 #pragma unroll
                     for (int e = 0; e < 8; e += 2)
@@ -438,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
         const bool gave_up = *failed != 0;
 #pragma unroll
         for (int j = 0; j < NP / 2; ++j)
-            red[((warp >> 2) * (NP / 2) + j) * kCols + (warp & 3) * 32 + lane] = gave_up ? __int_as_float(0x7FC00000) : total[j];
+            red[((warp >> 3) * NP + (warp >> 2 & 1) * (NP / 2) + j) * kCols + (warp & 3) * 32 + lane] = gave_up ? __int_as_float(0x7FC00000) : total[j];
     }
     if (cluster > 1)
         cluster_sync_all();
@@ -459,10 +497,15 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tensor_kernel(const __grid_con
             float2 v = make_float2(0.0f, 0.0f);
             const int at_red = row * kCols + c2;
             if (cluster == 1) {
-                v = *reinterpret_cast<const float2*>(red + at_red);
+#pragma unroll
+                for (int set = 0; set < kSets; ++set) {
+                    const float2 w = *reinterpret_cast<const float2*>(red + set * NP * kCols + at_red);
+                    v.x += w.x;
+                    v.y += w.y;
+                }
             } else {
-                for (int q = 0; q < cluster; ++q) {
-                    const float2 w = ld_shared_cluster_f32x2(map_shared_rank(sbase + at_red * 4, q));
+                for (int q = 0; q < cluster * kSets; ++q) {
+                    const float2 w = ld_shared_cluster_f32x2(map_shared_rank(sbase + (q % kSets * NP * kCols + at_red) * 4, q / kSets));
                     v.x += w.x;
                     v.y += w.y;
                 }
@@ -489,7 +532,7 @@ cudaError_t launch_one(const W4Args& a, const CUtensorMap& map, int sms, cudaStr
     if (cluster > 8) cluster = 8;
     if (cluster > blocks / 4) cluster = blocks / 4;
     if (cluster < 1) cluster = 1;
-    return launch_dependent(kernel, tiles * cluster, kThreads, Layout<NP, G>::kBytes, stream, cluster, a, map, cluster);
+    return launch_dependent(kernel, tiles * cluster, Layout<NP, G>::kThreads, Layout<NP, G>::kBytes, stream, cluster, a, map, cluster);
 }
 
 template <bool BF16, int NP>
