@@ -27,10 +27,14 @@
 //     threads apply the epilogue and store D.
 // A chain's waits are for its own earlier blocks alone, in order, so that no wait can take an
 // older phase of a barrier for the one it needs.
-// Measured (16384x8192, bf16, 48 rows): 25.1 us with groups of 128, 30.7 with 64, 39.8 with 32
+// Measured (16384x8192, bf16, 48 rows): 25.1 us with groups of 128, 30.5 with 64, 39.2 with 32
 // (a group's hand-over from the issuer to the summing warps costs more than its MMAs); about
 // 6 us of each is start and end (4096x1024: 6.4 us), the rest 580 cycles a block of 128 x 128
-// against some 370 for the unpacking instructions alone and for the weight's bytes.
+// against some 370 for the unpacking instructions alone and for the weight's bytes.  A block takes
+// 2000 warp instructions with groups of 128, 2600 with 64 (1080 of them unpacking), on 66 to 70 %
+// of the issue slots.  Tried and left: all columns of a group loaded at once (64: 32.2 us, 32:
+// 45.6), the sums as 64-bit pairs throughout (32.3, 42.2: more moves), one fma a column (31.4,
+// 40.4), 1024 threads with 96 registers for eight summing warps of all columns (37.1, 53.5).
 #include "kernel_params.h"
 #include "launch.h"
 #include "plan.h"
@@ -68,8 +72,8 @@ struct Layout {
     // Warps.  With groups of 128 the unpacking bounds a call: four chains.  With smaller groups the
     // summing does (some 240 cycles of waiting for a group, and two for each of its columns): three
     // chains, which leave room for a second set of summing warps, each with every other group.
-    // 16384x8192 with 16, 32, 48 and 64 rows, groups of 64: 26.7, 29.0, 30.7 and 36.7 us (four
-    // chains and one set 27.3, 29.9, 33.6, 36.7), of 32: 31.4, 34.9, 39.8, 51.5 (39.7, 44.2, 47.1, 54.8).
+    // 16384x8192 with 16, 32, 48 and 64 rows, groups of 64: 26.7, 29.0, 30.5 and 36.7 us (four
+    // chains and one set 27.3, 29.9, 33.6, 36.7), of 32: 31.0, 34.6, 39.2, 51.2 (39.7, 44.2, 47.1, 54.8).
     static constexpr int kChains = G == 128 ? 4 : 3;
     static constexpr int kSets = G == 128 ? 1 : 2;
     static constexpr int kSumWarps = 8 * kSets;       // set, half of the rows of A, quarter of the lanes
@@ -250,7 +254,8 @@ __global__ void __launch_bounds__(Layout<NP, G>::kThreads, 1) w4_tensor_kernel(c
         bool issued = false;
         const uint64_t desc0 = make_sdesc_sw128(sbase, 0, 1024);
         const int chain = __shfl_sync(0xFFFFFFFFu, warp - kIssuerWarp, 0);
-        int last = -1, n = 0;  // n: groups of this chain so far
+        int last = -1;
+        uint32_t n = 0;  // groups of this chain so far
         int bs = chain;
         uint32_t phase = 0, b_phase = 0;
         bool ok = true;
@@ -269,8 +274,8 @@ __global__ void __launch_bounds__(Layout<NP, G>::kThreads, 1) w4_tensor_kernel(c
                     const int k16 = 4 * h + s;  // 16 k within the block
                     if (i * kGroups + k16 * 16 / G >= groups) break;
                     if (k16 * 16 % G == 0) {
-                        const int before = n - L::kAccPer;  // the group that this accumulator held
-                        if (before >= 0)
+                        const uint32_t before = n - L::kAccPer;  // the group that this accumulator held
+                        if (n >= L::kAccPer)
                             ok = w4_wait(bar0 + 8 * (kAccEmpty + chain * kBarPer + before % kBarPer),
                                          before / kBarPer & 1, failed);
                         if (!ok) break;
@@ -424,14 +429,16 @@ __global__ void __launch_bounds__(Layout<NP, G>::kThreads, 1) w4_tensor_kernel(c
             cp_async_wait_group<kScaleDepth - 1>();
             __syncwarp();
             const uint16_t* scales = reinterpret_cast<const uint16_t*>(smem + ring + (i % kScaleDepth) * L::kSSlot) + lane;
+            const int here = groups - i * (kChains * kGroups);  // groups from this round on
             bool ok = true;
 #pragma unroll
             for (int p = 0; p < kChains * L::kSetGroups; ++p) {
                 const int chain = p % kChains;  // the chains in turn
                 const int q = chain * L::kSetGroups + p / kChains;
-                if (i * kChains * kGroups + in_round(q) >= groups) continue;
-                const int n = i * kGroups + p / kChains * kSets + set;  // of the chain
-                const int bar = chain * kBarPer + n % kBarPer;
+                if (in_round(q) >= here) continue;
+                // (unsigned: its remainders are masks)
+                const uint32_t n = i * kGroups + p / kChains * kSets + set;  // of the chain
+                const uint32_t bar = chain * kBarPer + n % kBarPer;
                 const float sc = decode16<BF16>(scales[q * 32]);
                 if (!w4_wait(bar0 + 8 * (kAccFull + bar), n / kBarPer & 1, failed)) {
                     ok = false;
