@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(WARPS * 32) rmsnorm_dgamma_kernel(const float*
 }
 
 constexpr int kRmsMaxWidth = 16384;  // widest row held in registers
-constexpr int kFewRows = 2048;       // backward, d <= 1024: a block per row up to here
+constexpr int kFewRows = 2048;       // backward, d <= 512: a block per row, not a warp, up to here
 
 // Blocks for `rows` rows, kRows at a time, at most `cap`, all with the same number of rounds.
 int even_grid(long long rows, int rows_per_block, long long cap)
@@ -652,10 +652,13 @@ struct BackwardShape {
 
 BackwardShape backward_shape(long long t, long long d)
 {
-    // (most blocks, measured: 4096x1024 12.9 us with 456, 18.6 with 1216; 16384x2048 45.8 with
+    // (most blocks, measured: 1024x1024 4.7 us with 456, 5.3 with 608 and 912; 4096x1024 10.1 with
+    // 760, 10.6 with 912, 32768x1024 47.7 and 45.3, with a warp per row 12.4 and 48.4; 4096x512
+    // 7.1 with a warp per row, 7.9 with a block; 16384x2048 45.8 with
     // 608, 61.4 with 304; 16384x4096 82.9 with 456, 87.6 with 304; 16384x8192 164 with 304, 175
     // with 228; 8192x16384 161 with 152, 171 with 456)
-    if (d <= 1024) return t <= kFewRows ? BackwardShape{1, 456} : BackwardShape{4, 456};
+    if (d <= 512) return t <= kFewRows ? BackwardShape{1, 456} : BackwardShape{4, 456};
+    if (d <= 1024) return {1, t <= kFewRows ? 456 : 912};
     if (d <= 2048) return {1, 608};
     if (d <= 4096) return {1, 456};
     if (d <= 8192) return {1, 304};
@@ -676,11 +679,9 @@ cudaError_t backward_launch_width(const RmsnormBackwardArgs& a, int parts, cudaS
 template <bool BF16>
 cudaError_t backward_launch_type(const RmsnormBackwardArgs& a, int parts, cudaStream_t stream)
 {
-    // few rows: a block per row, not a warp
-    if (a.d <= 1024 && a.t <= kFewRows) return backward_launch_width<BF16, 128, 1>(a, parts, stream);
+    if (a.d <= 1024 && (a.d > 512 || a.t <= kFewRows)) return backward_launch_width<BF16, 128, 1>(a, parts, stream);
     if (a.d <= 256) return backward_launch_width<BF16, 32, 1>(a, parts, stream);
     if (a.d <= 512) return backward_launch_width<BF16, 32, 2>(a, parts, stream);
-    if (a.d <= 1024) return backward_launch_width<BF16, 32, 4>(a, parts, stream);
     if (a.d <= 2048) return backward_launch_width<BF16, 128, 2>(a, parts, stream);
     if (a.d <= 4096) return backward_launch_width<BF16, 256, 2>(a, parts, stream);
     if (a.d <= 8192) return backward_launch_width<BF16, 256, 4>(a, parts, stream);
