@@ -234,6 +234,17 @@ def test_rmsnorm_backward(t, d, dtype, with_dh):
     _check_bwd(dX, dgamma, dy, h, gamma, rstd, dh, dtype)
 
 
+@pytest.mark.parametrize("t,d", [(2049, 264), (4100, 72), (5000, 512), (2049, 520), (3001, 1000), (6000, 1024),
+                                 (1900, 2048), (1000, 4096), (700, 8192)])
+def test_rmsnorm_backward_many_rows(t, d):
+    """Several rounds of every block, the last of them not full."""
+    dy, h, gamma, rstd, dh = _bwd_inputs(t, d, "bf16", t + d)
+    dX, dgamma = _backward(dy, h, gamma, rstd, dh, "bf16")
+    _check_bwd(dX, dgamma, dy, h, gamma, rstd, dh, "bf16")
+    again = _backward(dy, h, gamma, rstd, dh, "bf16")
+    assert torch.equal(dX, again[0]) and torch.equal(dgamma, again[1])
+
+
 @pytest.mark.parametrize("dx", ["dY", "dH"])
 @pytest.mark.parametrize("t,d", [(40, 1000), (400, 1024), (3, 20000)])
 def test_rmsnorm_backward_in_place_and_repeatable(t, d, dx):
