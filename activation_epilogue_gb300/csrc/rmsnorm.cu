@@ -562,9 +562,10 @@ __global__ void __launch_bounds__(kThreadsPerRow) rmsnorm_backward_columns_kerne
 // columns, its warp w rows w, w + WARPS, ..., and the warps' sums meet in order.  Many parts
 // take 32 warps (1024 rows of 1024 columns: 10 us with 8, 3 with 32), few 8 (64 rows of 4096:
 // a whole call 3.9 us with 8, 4.8 with 32).  A warp's loads are issued together, the last one's
-// row again past the end (333 x 1000: a call 4.5 -> 3.8 us, 2000 x 1024 7.2 -> 6.6).
+// row again past the end (333 x 1000: a call 4.5 -> 3.8 us, 2000 x 1024 7.2 -> 6.6), from 32
+// registers a thread, so that an SM holds 64 warps (8000 x 2048: 29.4 -> 26.4, 500 x 4096 8.4 -> 7.2).
 template <int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) rmsnorm_dgamma_kernel(const float* ws, int parts, int d,
+__global__ void __launch_bounds__(WARPS * 32, 64 / WARPS) rmsnorm_dgamma_kernel(const float* ws, int parts, int d,
                                                                     float* dgamma)
 {
     constexpr int kAtOnce = WARPS == 32 ? 12 : 16;
