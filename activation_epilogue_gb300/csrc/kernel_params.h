@@ -318,7 +318,7 @@ constexpr int kW4MaxM = 64;
 cudaError_t w4_matmul_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
 // (csrc/w4_stream.cu) the product for up to 4 rows of A, groups of 64 or 128
 cudaError_t w4_stream_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
-// (csrc/w4_tensor.cu) the product for 9 to 64 rows of A
+// (csrc/w4_tensor.cu) the product for 9 to 64 rows of A, from 5 on of the largest weights
 cudaError_t w4_tensor_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
 cudaError_t w4_dequantize_launch(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
 

@@ -20,7 +20,7 @@
 //     are in one group), so the scale multiplies an fp32 sum, and no weight is ever rounded.
 //   * The KW warps' sums meet in shared memory, in order; then the epilogue.
 // Measured (bf16, groups of 128): 4096 x 4096 with one row 4.4 us, 4096 x 1024 2.3; 8 rows of
-// 8192 x 8192 13.9 and of 16384 x 8192 26.3 us (39 % of the copy rate for the weight's bytes; with
+// 8192 x 8192 14.2 us, with groups of 64 of 16384 x 8192 26.9 (37 % of the copy rate for the weight's bytes; with
 // one row the loads alone took 13.4 us, the arithmetic alone 17.6, both 22.7: the larger weights
 // of up to 4 rows have a kernel of their own, w4_stream.cu).  Tried and left: bulk copies of rows
 // by one warp (33 us: 75 cycles for each copy of 512 bytes), 16 warps a block (26.6), 256 values
@@ -323,9 +323,14 @@ cudaError_t w4_launch_type(const W4Args& a, int sms, cudaStream_t stream)
     if (a.m <= 4 && a.group >= 64 && weights >= (a.group == 128 ? 20ll : 60ll) << 20)
         return w4_stream_launch(a, BF16, sms, stream);
     if (a.m <= 4) return w4_launch_group<BF16, 1, 2, 1, 4>(a, sms, stream);
-    if (a.m <= 8) return w4_launch_group<BF16, 1, 2, 1, 3>(a, sms, stream);
+    // 5 to 8 rows: tcgen05's lower rate of instructions outweighs its longer start only where the
+    // weight is large and the groups are few (8 rows, groups of 128: 16384x8192 26.6 us here, 23.0
+    // there, 8192x16384 25.7 and 24.3, 8192x8192 14.2 and 14.9; groups of 64: 26.9 and 26.6, 26.2
+    // and 27.8)
+    if (a.m <= 8 && (a.group < 128 || weights < 96ll << 20)) return w4_launch_group<BF16, 1, 2, 1, 3>(a, sms, stream);
     // 9 to 16 rows: this kernel's second tile of rows costs a small weight less than tcgen05's
-    // longer start (4096x1024: 4.4 us here, 6.0 there), a large one more (8192x8192: 26.8, 18.4)
+    // longer start (12 rows: 4096x1024 4.4 us here, 5.4 there, 1024x4096 4.9 and 6.2), a large one
+    // more (4096x4096 8.4 and 7.7, 8192x8192 24.6 and 15.0)
     if (a.m <= 16 && weights <= 12ll << 20)
         return w4_launch_group<BF16, 2, 1, 4, 4>(a, sms, stream);
     return w4_tensor_launch(a, BF16, sms, stream);

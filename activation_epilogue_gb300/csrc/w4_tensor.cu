@@ -1,5 +1,5 @@
-// Products with 4-bit weights for 9 to 64 rows of A, on tcgen05: D^T = W A^T with 128 columns of
-// D as the MMA's rows and the rows of A as its columns.
+// Products with 4-bit weights for 9 to 64 rows of A (from 5 on of the largest weights), on tcgen05:
+// D^T = W A^T with 128 columns of D as the MMA's rows and the rows of A as its columns.
 //
 // mma.sync takes 16 cycles for 16 x 8 x 16 on this part, an eighth of tcgen05's rate, so that
 // from two 8-row tiles of A on it, and not the weight's bytes, bounds a product (16384x8192,

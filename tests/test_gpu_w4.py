@@ -69,6 +69,10 @@ def test_w4_few_rows_of_a_large_weight(m, n, k, group, dtype, zeros):
     _check(ref.w4_problem(m, n, k, group, dtype, zeros, m + n), group, dtype, "BIAS_RESIDUAL" if zeros else "TANH_BIAS")
 
 
+def test_w4_eight_rows_of_the_largest_weights():
+    _check(ref.w4_problem(6, 16392, 6144, 128, "bf16", True, 5), 128, "bf16", "GELU_BIAS")
+
+
 def test_w4_few_rows_of_a_large_weight_exact_and_untouched():
     # integers as above at the larger sizes, and rows behind the last left as they were
     g = torch.Generator().manual_seed(3)
