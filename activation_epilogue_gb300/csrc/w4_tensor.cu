@@ -125,6 +125,17 @@ __device__ __forceinline__ bool elect_one()
     return one != 0;
 }
 
+// mbar_arrive in the lanes that `take` part, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool take)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(static_cast<uint32_t>(take))
+        : "memory");
+}
+
 // Store 16 words of this thread's lane (no wait).
 __device__ __forceinline__ void tmem_store_16cols_async(uint32_t taddr, const uint32_t (&r)[16])
 {
@@ -389,7 +400,7 @@ __global__ void __launch_bounds__(Layout<NP, G>::kThreads, 1) w4_tensor_kernel(c
                 tmem_wait_st();
                 tcgen05_fence_before_sync();
                 __syncwarp();  // (also: the slot is read before its next copy is issued)
-                if (lane == 0) mbar_arrive(bar0 + 8 * (kAFull + 2 * chain + h));
+                mbar_arrive_if(bar0 + 8 * (kAFull + 2 * chain + h), lane == 0);
             }
         }
         cp_async_wait_group<0>();
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(Layout<NP, G>::kThreads, 1) w4_tensor_kernel(c
                     } else {
                         tcgen05_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar0 + 8 * (kAccEmpty + bar));
+                        mbar_arrive_if(bar0 + 8 * (kAccEmpty + bar), lane == 0);
                     }
 #pragma unroll
                     for (int e = 0; e < 8; e += 2)
