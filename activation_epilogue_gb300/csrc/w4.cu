@@ -318,8 +318,8 @@ cudaError_t w4_launch_type(const W4Args& a, int sms, cudaStream_t stream)
 {
     const long long weights = static_cast<long long>(a.n) * a.k;
     // up to 4 rows of a large weight: without the stages in shared memory (one row, groups of
-    // 128: 8192x8192 10.6 us there, 12.4 here, 4096x4096 4.3 and 4.4, 4096x1024 2.8 and 2.3;
-    // groups of 64: 8192x8192 12.1 and 12.9, 5120x5120 8.2 and 8.2; 8 rows 16.0 and 13.9)
+    // 128: 8192x8192 10.0 us there, 12.4 here, 4096x4096 4.3 and 4.4, 4096x1024 2.8 and 2.3;
+    // groups of 64: 8192x8192 11.4 and 12.9, 5120x5120 8.2 and 8.2; 8 rows 16.0 and 13.9)
     if (a.m <= 4 && a.group >= 64 && weights >= (a.group == 128 ? 20ll : 60ll) << 20)
         return w4_stream_launch(a, BF16, sms, stream);
     if (a.m <= 4) return w4_launch_group<BF16, 1, 2, 1, 4>(a, sms, stream);

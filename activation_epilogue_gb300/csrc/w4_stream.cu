@@ -20,12 +20,12 @@
 //   * The warps' sums meet in shared memory in order, those of a cluster that splits k over
 //     distributed shared memory; then the epilogue.
 // Measured (bf16, groups of 128, one row; the staged kernel in brackets): 8192 columns, k 16384
-// 18.0 us (22.7), 16384 x 8192 20.7 (23.4), 8192 x 8192 10.6 (12.4), 5120 x 5120 5.5 (8.0);
+// 17.2 us (22.7), 16384 x 8192 19.7 (23.4), 8192 x 8192 10.0 (12.4), 5120 x 5120 5.5 (8.0);
 // 4096 x 1024 2.8 (2.3: its longer code and its first barrier cost a short call more).  For
-// 8192 columns with k 16384 that is 57 % of the copy rate; the loads alone take 14.9 us (a kernel
-// that only reads as many bytes in order: 14.3), the arithmetic alone 14.9.  Two steps ahead
-// 19.9, four (168 registers' worth in 128) 21.9; several blocks of 128 k in a row per warp, for
-// longer pieces of a row of W, 18.9 to 19.1.
+// 8192 columns with k 16384 that is 59 % of the copy rate; the loads alone take 14.9 us (a kernel
+// that only reads as many bytes in order: 14.3), the arithmetic alone 14.9.  Tried at 18.0 us, before
+// the hint to L2: two steps loaded ahead 19.9, four (168 registers' worth in 128) 21.9; several
+// blocks of 128 k in a row per warp, for longer pieces of a row of W, 18.9 to 19.1.
 #include "kernel_params.h"
 #include "launch.h"
 #include "ptx.cuh"
@@ -45,6 +45,12 @@ constexpr int kStepK = kWarps * kBlockK;      // k per step of the block
 constexpr int kAhead = 3;                     // steps loaded ahead
 constexpr int kUnroll = kAhead + 1;
 constexpr int kMaxSmem = 100 * 1024;          // two blocks per SM
+
+// Ask for `bytes` (a multiple of 16) from src (16-byte aligned) to be brought into L2.
+__device__ __forceinline__ void prefetch_l2_bulk(const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 
 // Words (8 values of k) of a lane in a block of 128 k: word i of lane t holds k = k_of(t, i) ..
 // + 7.  With groups of 128 a lane has 32 consecutive values, of 64 twice 16.
@@ -120,6 +126,14 @@ __device__ __forceinline__ void stream_columns(const W4Args& a, uint8_t* smem, i
         ++loaded;
     };
 
+    // Ahead of the wait only L2 is asked for the first words of each row (a hint: what is written
+    // until the wait ends is read after it).  From 8 steps on: 8192 x 8192 10.5 -> 10.0 us, 8192
+    // columns with k 16384 18.1 -> 17.2, 16384 x 8192 20.6 -> 19.7; with 4 steps 11264 x 4096
+    // 10.2 -> 10.7.  One step 17.4, six 17.9 (k 16384), all of a row 20.8.
+    if (steps >= 8 && tid < NQ * 8)
+        prefetch_l2_bulk(static_cast<const uint8_t*>(a.W) +
+                             (static_cast<long long>(n0 + tid) * a.k + static_cast<long long>(first) * kStepK) / 2,
+                         kAhead * kStepK / 2);
     grid_dependency_wait();
     grid_launch_dependents();
 #pragma unroll

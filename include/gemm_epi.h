@@ -413,7 +413,8 @@ int64_t gemm_epi_rmsnorm_workspace(int64_t t, int64_t d);
  * the residual given exactly for BIAS_RESIDUAL, and D may be the residual itself.  The
  * differences q - z are exact in 16 bits and their products with A are summed in fp32, group
  * by group, with the scales applied in fp32.  A, W, scales, residual and D 16-byte aligned,
- * zeros 8-byte, bias 2-byte.  No workspace, no plan; asynchronous on `stream` as above.  (The
+ * zeros 8-byte, bias 2-byte.  No workspace, no plan; asynchronous on `stream` as above (ahead of the
+ * wait L2 may be asked for a part of W, which is read after it).  (The
  * kernel for more than a few rows waits for its own copies and products with a limit of two
  * seconds; should one run out, it ends and writes NaN.) */
 gemm_epi_status gemm_epi_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group,
