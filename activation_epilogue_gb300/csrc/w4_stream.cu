@@ -26,6 +26,10 @@
 // that only reads as many bytes in order: 14.3), the arithmetic alone 14.9.  Tried at 18.0 us, before
 // the hint to L2: two steps loaded ahead 19.9, four (168 registers' worth in 128) 21.9; several
 // blocks of 128 k in a row per warp, for longer pieces of a row of W, 18.9 to 19.1.
+// A further row of A costs some 0.8 us at k 8192 and 1.5 at 16384: every block reads all of A from
+// L2.  Blocks of twice the warps and columns, one an SM, halve that (4 rows, 8192 columns, k 16384:
+// 23.0 -> 21.3 us), but a call no longer overlaps the end of the one before (one row: 16384 x 8192
+// 20.0 -> 21.9, 5120 x 5120 5.5 -> 6.3), nor does loading A ahead of W's first words help (19.5).
 #include "kernel_params.h"
 #include "launch.h"
 #include "ptx.cuh"
