@@ -20,11 +20,11 @@
 //     are in one group), so the scale multiplies an fp32 sum, and no weight is ever rounded.
 //   * The KW warps' sums meet in shared memory, in order; then the epilogue.
 // Measured (bf16, groups of 128): 4096 x 4096 with one row 4.4 us, 4096 x 1024 2.3; 8 rows of
-// 8192 x 8192 14.2 us, with groups of 64 of 16384 x 8192 26.9 (37 % of the copy rate for the weight's bytes; with
-// one row the loads alone took 13.4 us, the arithmetic alone 17.6, both 22.7: the larger weights
-// of up to 4 rows have a kernel of their own, w4_stream.cu).  Tried and left: bulk copies of rows
-// by one warp (33 us: 75 cycles for each copy of 512 bytes), 16 warps a block (26.6), 256 values
-// of k per warp and stage (22.8).
+// 8192 x 8192 14.2 us, with groups of 64 of 16384 x 8192 26.9 (37 % of the copy rate for the
+// weight's bytes; with one row of 8192 columns, k 16384, the loads alone took 13.4 us, the
+// arithmetic alone 17.6, both 22.7: the larger weights of up to 4 rows have a kernel of their own,
+// w4_stream.cu).  Tried and left: bulk copies of rows by one warp (33 us: 75 cycles for each copy of
+// 512 bytes), 16 warps a block (26.6), 256 values of k per warp and stage (22.8).
 #include "kernel_params.h"
 #include "launch.h"
 #include "ptx.cuh"

@@ -11,7 +11,7 @@
 //
 //   * The producer (one thread) copies blocks of 128 k of A by TMA (128-byte swizzle, rows past
 //     m and k past the end read as zeros).
-//   * Four chains (three with groups below 128) take every fourth block each, with a block of
+//   * Four chains (three with groups below 128) take every fourth (third) block each, with a block of
 //     tensor memory (two halves), one or two accumulators and an issuing warp of their own.
 //     (One issuer's own instructions took 1300 cycles a block, nearly all of a call: 48 us for
 //     16384x8192 with 48 rows; two chains 31 us, four 26.6, and 25.1 with a group's MMAs issued
@@ -22,9 +22,10 @@
 //     per 32-bit word, and stores them to tensor memory, half a block at a time.
 //   * The chain's issuer runs the MMAs of one group of the scales after another.
 //   * Eight warps (a quarter of the lanes, half of the rows of A each), with groups below 128 two
-//     times eight with every other group each, read the groups' sums, of the chains in turn, multiply them by the group's scales (one per lane: the lane is the
-//     column of D) and add them up in fp32, two rows of A per instruction; at the end all
-//     threads apply the epilogue and store D.
+//     times eight with every other group each, read the groups' sums, of the chains in turn,
+//     multiply them by the group's scales (one per lane: the lane is the column of D) and add them
+//     up in fp32, two rows of A per instruction; at the end all threads apply the epilogue and
+//     store D.
 // A chain's waits are for its own earlier blocks alone, in order, so that no wait can take an
 // older phase of a barrier for the one it needs.
 // Measured (16384x8192, bf16, 48 rows): 25.1 us with groups of 128, 30.5 with 64, 39.2 with 32
