@@ -161,6 +161,24 @@ def test_w4_in_place_residual_and_repeatable():
     assert torch.equal(R, first) and torch.equal(_run(p, 128, "bf16", "BIAS_RESIDUAL"), first)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_w4_gelu_over_its_range(dtype):
+    """k = 0: D = GELU(bias) = max(v, 0) - |v| Phi(-|v|), for every finite 16-bit value.  The tail's
+    exponent, up to 13^2 / (2 ln 2) = 122, is rounded to fp32 twice: 2 * 122 * 2^-24 * ln 2 = 1.0e-5
+    of the tail; fp32 roundings of the two terms; 1e-37 where the tail leaves fp32's range."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(TD[dtype])
+    bias = torch.where(bits.isfinite(), bits, torch.zeros_like(bits)).cuda()
+    D = torch.full((2, 65536), float("nan"), dtype=TD[dtype], device="cuda")
+    gemm_epi.gemm_epi_w4_matmul(2, 65536, 0, 128, dtype, "GELU_BIAS", None, None, None, None, bias, None, D)
+    v = bias.double()
+    # Phi(v) = erfc(-v / sqrt 2) / 2, accurate in relative terms for negative v as well
+    want = v * 0.5 * torch.special.erfc(-v / 2.0 ** 0.5)
+    assert torch.equal(D[0], D[1])
+    tail = v.abs() * 0.5 * torch.special.erfc(v.abs() / 2.0 ** 0.5)
+    error = (1.0e-5 + 4 * ref.F32) * tail + 2 * ref.F32 * v.clamp(min=0) + 1e-37
+    ref.check_16(D[0].cpu(), want.cpu(), dtype, error.cpu(), "GELU")
+
+
 @pytest.mark.parametrize("m", [3, 12, 40])
 def test_w4_k_zero_is_the_epilogue_alone(m):
     bias = torch.randn(64, generator=torch.Generator().manual_seed(1)).to(torch.float16)
