@@ -69,6 +69,51 @@ def test_w4_few_rows_of_a_large_weight(m, n, k, group, dtype, zeros):
     _check(ref.w4_problem(m, n, k, group, dtype, zeros, m + n), group, dtype, "BIAS_RESIDUAL" if zeros else "TANH_BIAS")
 
 
+def _integer_problem(m, n, k, group, dtype, zeros, seed):
+    """Integer activations, weights and scales whose sums fp32 holds exactly in any order, and a residual
+    that takes each sum down to what its rounding to 16 bits left: D is a small whole number, exactly,
+    and one wrong, missing or doubled term shows in it."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randint(0, 16, (n, k), generator=g, dtype=torch.uint8)
+    z = torch.randint(0, 16, (k // group, n), generator=g).to(torch.uint8) if zeros else None
+    scales = torch.randint(1, 3, (k // group, n), generator=g).to(TD[dtype])
+    A = torch.randint(-1, 2, (m, k), generator=g).to(TD[dtype])
+    B = ref.w4_weight(q, scales, z, group)
+    # every partial sum is a whole number below 2^24
+    assert (A.double().abs() @ B.abs()).max() < 2 ** 24
+    total = A.double() @ B
+    R = (-total).to(TD[dtype])
+    want = total + R.double()
+    assert torch.equal(want.to(TD[dtype]).double(), want)
+    return dict(q=q, W=ref.w4_pack(q), scales=scales, zeros=z, A=A, bias=torch.zeros(n, dtype=TD[dtype]), R=R), want
+
+
+@pytest.mark.parametrize("m,n,k,group", [(1, 40, 600064, 128), (2, 264, 98432, 128), (4, 264, 81920, 128),
+                                         (1, 104, 604992, 64), (4, 512, 122944, 64)])
+@pytest.mark.parametrize("dtype,zeros", [("bf16", False), ("f16", True)])
+def test_w4_stretches_of_k_are_exact(m, n, k, group, dtype, zeros):
+    """k of several stretches of shared memory in each block of the streaming kernel (100 KB hold 36
+    times 1024 values of k for one row with groups of 128, 8 for four rows), the last one shorter."""
+    p, want = _integer_problem(m, n, k, group, dtype, zeros, m + n)
+    D = torch.full((m + 1, n), 7.0, dtype=TD[dtype], device="cuda")
+    _run(p, group, dtype, "BIAS_RESIDUAL", D=D[:m])
+    assert torch.equal(D[:m].double().cpu(), want) and (D[m:] == 7.0).all()
+
+
+@pytest.mark.parametrize("m,n,k,group", [(1, 40, 600064, 128), (4, 264, 81920, 128), (4, 512, 122944, 64)])
+@pytest.mark.parametrize("dtype,zeros", [("bf16", False), ("f16", True)])
+def test_w4_stretches_of_k_within_the_sum_s_own_chain(m, n, k, group, dtype, zeros):
+    p = ref.w4_problem(m, n, k, group, dtype, zeros, m + n)
+    B, A = ref.w4_weight(p["q"], p["scales"], p["zeros"], group), p["A"].double()
+    want = A @ B
+    # the chain of a sum: the matrix instructions of one group (16 k each; they may truncate, a whole
+    # step), a group's sum scaled and added for each of the warp's groups (an eighth of k or less), then
+    # the eight warps and up to eight blocks
+    error = (group / 16 + k / (8 * group) + 1 + 16) * 2 * ref.F32 * (A.abs() @ B.abs())
+    assert error.mean() < 0.1 * want.abs().mean()  # (a bound that a wrong sum does not keep)
+    ref.check_16(_run(p, group, dtype, "NONE"), want, dtype, error, "D")
+
+
 def test_w4_eight_rows_of_the_largest_weights():
     _check(ref.w4_problem(6, 16392, 6144, 128, "bf16", True, 5), 128, "bf16", "GELU_BIAS")
 
