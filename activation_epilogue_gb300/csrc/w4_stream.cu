@@ -35,20 +35,21 @@
 #include "ptx.cuh"
 #include "vec16.cuh"
 #include "w4_mma.cuh"
+#include "w4_segment.h"
 #include "w4_unpack.cuh"
 
 namespace gemm_epi {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = kStreamWarps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCols = 32;                     // columns of D per block
-constexpr int kBlockK = 128;                  // k per warp at a time
-constexpr int kStepK = kWarps * kBlockK;      // k per step of the block
-constexpr int kAhead = 3;                     // steps loaded ahead
-constexpr int kUnroll = kAhead + 1;
-constexpr int kMaxSmem = 100 * 1024;          // two blocks per SM
+constexpr int kCols = kStreamCols;
+constexpr int kBlockK = kStreamBlockK;
+constexpr int kStepK = kStreamStepK;
+constexpr int kUnroll = kStreamUnroll;
+constexpr int kAhead = kUnroll - 1;           // steps loaded ahead
+constexpr int kMaxSmem = kStreamMaxSmem;
 
 // Ask for `bytes` (a multiple of 16) from src (16-byte aligned) to be brought into L2.
 __device__ __forceinline__ void prefetch_l2_bulk(const void* src, uint32_t bytes)
@@ -85,19 +86,6 @@ __device__ __forceinline__ void load_words(const uint8_t* src, int t, int left, 
         }
     }
 }
-
-// Shared memory of a segment of `steps` steps for m rows of A.  A row is padded, and with groups of
-// 128 its 16-byte pieces exchanged in pairs, so that the eight lanes that read at a time (two rows,
-// four pieces) find eight different banks.
-template <int G>
-struct Segment {
-    static constexpr int kPad = G == 128 ? 32 : 16;
-    static constexpr int kGroups = kStepK / G;  // per step
-    static __host__ __device__ int pitch(int steps) { return steps * kStepK * 2 + kPad; }
-    static __host__ __device__ int scales(int m, int steps) { return (m * pitch(steps) + 15) / 16 * 16; }
-    static __host__ __device__ int zeros(int m, int steps) { return scales(m, steps) + steps * kGroups * kCols * 2; }
-    static __host__ __device__ int bytes(int m, int steps) { return zeros(m, steps) + steps * kGroups * kCols; }
-};
 
 // The sums of this block's share of k: NQ groups of 8 columns (MMA rows 0-7, 8-15 of one or two
 // MMAs; the upper half of the last is zeros where NQ is odd).
@@ -335,9 +323,7 @@ cudaError_t launch_one(const W4Args& a, int sms, cudaStream_t stream)
         tiles = (tiles + sms - 1) / sms * sms;
         if (tiles > a.n / 8) tiles = a.n / 8;
     }
-    int seg = ((steps + cluster - 1) / cluster + kUnroll - 1) / kUnroll * kUnroll;
-    if (seg < kUnroll) seg = kUnroll;
-    while (S::bytes(a.m, seg) > kMaxSmem) seg -= kUnroll;
+    const int seg = S::steps_for(a.m, (steps + cluster - 1) / cluster);
     int smem = S::bytes(a.m, seg);
     constexpr int kRed = kWarps * 8 * (kCols + 1) * 4;
     if (smem < kRed) smem = kRed;
