@@ -2,6 +2,7 @@
 // with 4-bit weights and dropout.  Argument checks and launches; nothing is kept between calls.
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 
 #include "plan.h"
 
@@ -40,6 +41,27 @@ bool norm_shape_ok(int64_t t, int64_t d)
     return t >= 0 && d >= 8 && d % 8 == 0 && t <= kMax && d <= kMaxWidth && t * d <= (1ll << 40);
 }
 
+struct Buffer {
+    const void* p;
+    int64_t bytes;
+};
+
+bool meet(const Buffer& a, const Buffer& b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x && y && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+
+// An output overlaps none of `others`, and those that it may be (of its own extent) not in part.
+bool apart(const Buffer& out, std::initializer_list<Buffer> others, std::initializer_list<Buffer> may_be = {})
+{
+    for (const Buffer& b : others)
+        if (meet(out, b)) return false;
+    for (const Buffer& b : may_be)
+        if (b.p != out.p && meet(out, b)) return false;
+    return true;
+}
+
 int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 gemm_epi_status rmsnorm(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* X,
@@ -59,6 +81,16 @@ gemm_epi_status rmsnorm(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* 
         !aligned(Y, 16) || !aligned(scale, 4) || !aligned(rstd, 4) ||
         (mode == kRmsTensor && !aligned(workspace, 16)))
         return GEMM_EPI_ERR_MISALIGNED;
+    {
+        const Buffer x = {X, 2 * t * d}, r = {residual, 2 * t * d}, g = {gamma, 2 * d}, h = {H, 2 * t * d};
+        const Buffer y = {Y, (mode == kRms16 ? 2 : 1) * t * d}, rs = {rstd, 4 * t};
+        const Buffer sc = {scale, mode == kRmsRow ? 4 * t : 4};
+        const Buffer ws = {mode == kRmsTensor ? workspace : nullptr, gemm_epi_rmsnorm_workspace(t, d)};
+        const bool ok = apart(h, {g, y, rs, sc, ws}, {x, r}) && apart(rs, {x, r, g, sc, ws}) && apart(ws, {x, r, g, sc}) &&
+                        (mode == kRmsGiven || apart(sc, {x, r, g})) &&
+                        (mode == kRms16 ? apart(y, {g, rs}, {x, r}) : apart(y, {g, rs, sc, ws, x, r}));
+        if (!ok) return GEMM_EPI_ERR_INVALID_ARG;
+    }
     int sms = 0;
     const gemm_epi_status st = device_sms(&sms);
     if (st != GEMM_EPI_OK) return st;
@@ -126,6 +158,10 @@ gemm_epi_status gemm_epi_rmsnorm_backward(int64_t t, int64_t d, gemm_epi_dtype d
         if (!aligned(dY, 16) || !aligned(H, 16) || !aligned(gamma, 16) || !aligned(rstd, 4) ||
             !aligned(dH, 16) || !aligned(dX, 16) || !aligned(workspace, 16))
             return GEMM_EPI_ERR_MISALIGNED;
+        const Buffer y = {dY, 2 * t * d}, h = {H, 2 * t * d}, g = {gamma, 2 * d}, rs = {rstd, 4 * t}, z = {dH, 2 * t * d};
+        const Buffer dx = {dX, 2 * t * d}, dg = {dgamma, 4 * d}, ws = {workspace, gemm_epi_rmsnorm_workspace(t, d)};
+        if (!apart(dx, {h, g, rs, dg, ws}, {y, z}) || !apart(dg, {y, h, g, rs, z, ws}) || !apart(ws, {y, h, g, rs, z}))
+            return GEMM_EPI_ERR_INVALID_ARG;
     }
     int sms = 0;
     const gemm_epi_status st = device_sms(&sms);
@@ -174,6 +210,11 @@ gemm_epi_status gemm_epi_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t grou
     if (!aligned(A, 16) || !aligned(W, 16) || !aligned(scales, 16) || !aligned(zeros, 8) ||
         !aligned(bias, 2) || !aligned(residual, 16) || !aligned(D, 16))
         return GEMM_EPI_ERR_MISALIGNED;
+    // (blocks write columns of D while others still read all of A)
+    const int64_t scaled = k / group * n;
+    if (!apart({D, 2 * m * n}, {{A, 2 * m * k}, {W, n * k / 2}, {scales, 2 * scaled}, {zeros, scaled}, {bias, 2 * n}},
+               {{residual, 2 * m * n}}))
+        return GEMM_EPI_ERR_INVALID_ARG;
     int sms = 0;
     st = device_sms(&sms);
     if (st != GEMM_EPI_OK) return st;
@@ -203,6 +244,8 @@ gemm_epi_status gemm_epi_w4_dequantize(int64_t n, int64_t k, int64_t group,
     if (!W || !scales || !B) return GEMM_EPI_ERR_INVALID_ARG;
     if (!aligned(W, 16) || !aligned(scales, 16) || !aligned(zeros, 8) || !aligned(B, 16))
         return GEMM_EPI_ERR_MISALIGNED;
+    const int64_t scaled = k / group * n;
+    if (!apart({B, 2 * n * k}, {{W, n * k / 2}, {scales, 2 * scaled}, {zeros, scaled}})) return GEMM_EPI_ERR_INVALID_ARG;
     int sms = 0;
     st = device_sms(&sms);
     if (st != GEMM_EPI_OK) return st;
@@ -228,6 +271,7 @@ gemm_epi_status gemm_epi_dropout(int64_t count, gemm_epi_dtype dtype, const void
     if (!X || !Y) return GEMM_EPI_ERR_INVALID_ARG;
     if (!aligned(X, 16) || !aligned(residual, 16) || !aligned(Y, 16) || !aligned(offset_device, 8))
         return GEMM_EPI_ERR_MISALIGNED;
+    if (!apart({Y, 2 * count}, {{offset_device, 8}}, {{X, 2 * count}, {residual, 2 * count}})) return GEMM_EPI_ERR_INVALID_ARG;
     int sms = 0;
     const gemm_epi_status st = device_sms(&sms);
     if (st != GEMM_EPI_OK) return st;

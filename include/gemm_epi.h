@@ -355,7 +355,7 @@ gemm_epi_status gemm_epi_layernorm_fold(int64_t d, int64_t f, gemm_epi_dtype dty
  * read; sums and rstd are fp32, Y is rounded once.  X, residual, H, Y: t x d; gamma: d
  * elements; all of `dtype` (F16 or BF16), d a multiple of 8, 8 to 2^30, 16-byte aligned.  H is
  * given exactly when the residual is.  H and Y may each be X or the residual itself, but not
- * the same buffer; no other overlap.  rstd: t fp32, 4-byte aligned, or NULL (the backward
+ * the same buffer; any other overlap of an output is ERR_INVALID_ARG, here and in the calls below.  rstd: t fp32, 4-byte aligned, or NULL (the backward
  * pass reads it).  eps >= 0.  A NaN or an infinity in a row of H makes that row of Y NaN (or,
  * finite / infinite, 0) as the formula does.  t == 0 launches nothing.  Asynchronous on
  * `stream`, launched as programmatic dependents of its previous work (which they wait for
@@ -389,7 +389,7 @@ gemm_epi_status gemm_epi_rmsnorm_e4m3(int64_t t, int64_t d, gemm_epi_dtype dtype
  *     g_ij = dY_ij gamma_j,   xh_ij = H_ij rstd_i,
  *     dX_ij = rstd_i (g_ij - xh_ij mean_j(g_ij xh_ij)) + dH_ij,   dgamma_j = sum_i dY_ij xh_ij.
  * dX is the gradient of X and of the residual alike.  dH, the gradient that reaches H past the
- * norm, may be NULL (zero).  dY, H, dH, dX: t x d of `dtype`, dX may be dY or dH; dgamma: d
+ * norm, may be NULL (zero).  dY, H, dH, dX: t x d of `dtype`, dX may be dY or dH itself; dgamma: d
  * fp32, summed in an order that depends on (t, d) alone (the same inputs give the same bits);
  * t == 0 writes zeros to it.  workspace as above, always needed (t > 0). */
 gemm_epi_status gemm_epi_rmsnorm_backward(int64_t t, int64_t d, gemm_epi_dtype dtype,
@@ -410,8 +410,8 @@ int64_t gemm_epi_rmsnorm_workspace(int64_t t, int64_t d);
  * nothing); for more, gemm_epi_w4_dequantize and a plan.  A: m x k, bias: n elements (the
  * (1,n) layout), residual and D: m x n, of `dtype` (F16 or BF16); epilogs BIAS, RELU_BIAS,
  * GELU_BIAS, TANH_BIAS, BIAS_RESIDUAL and NONE as for plans; bias is NULL exactly for NONE,
- * the residual given exactly for BIAS_RESIDUAL, and D may be the residual itself.  The
- * differences q - z are exact in 16 bits and their products with A are summed in fp32, group
+ * the residual given exactly for BIAS_RESIDUAL, and D may be the residual itself (and overlaps
+ * nothing else: ERR_INVALID_ARG).  The differences q - z are exact in 16 bits and their products with A are summed in fp32, group
  * by group, with the scales applied in fp32.  A, W, scales, residual and D 16-byte aligned,
  * zeros 8-byte, bias 2-byte.  No workspace, no plan; asynchronous on `stream` as above (ahead of the
  * wait L2 may be asked for a part of W, which is read after it).  (The

@@ -127,6 +127,52 @@ def test_dropout_refusals(change, status):
     assert _status(gemm_epi.gemm_epi_dropout, **{**base, **change}) == status
 
 
+def _apart(**kw):
+    """kw with an address of its own, 16 MiB apart, for every buffer that is True."""
+    at = iter(range(16, 10 ** 6, 16))
+    return {k: next(at) << 20 if v is True else v for k, v in kw.items()}
+
+
+NORM_A = _apart(t=4, d=64, dtype="bf16", X=True, residual=True, gamma=True, eps=1e-6, H=True, Y=True, rstd=True)
+NORM8_A = dict({k: v for k, v in NORM_A.items() if k != "Y"}, Q=500 << 20, scale=501 << 20, workspace=502 << 20)
+BWD_A = _apart(t=4, d=64, dtype="bf16", dY=True, H=True, gamma=True, rstd=True, dH=True, dX=True,
+               dgamma=True, workspace=True)
+W4_A = _apart(m=2, n=128, k=128, group=32, dtype="bf16", epilog="BIAS_RESIDUAL", A=True, W=True, scales=True,
+              zeros=True, bias=True, residual=True, D=True)
+DEQ_A = _apart(n=128, k=128, group=32, dtype="bf16", W=True, scales=True, zeros=True, B=True)
+DROP_A = _apart(count=256, dtype="bf16", X=True, residual=True, p=0.1, seed=1, offset=0, Y=True,
+                offset_device=True)
+
+
+@pytest.mark.parametrize("call,base,out,over,by", [
+    # (output, what it may not overlap, bytes into that): the whole of it, or its last 16 bytes
+    *[("rmsnorm", NORM_A, out, over, by) for out, over, by in (
+        ("H", "X", 16), ("H", "residual", 496), ("Y", "X", 496), ("Y", "residual", 16), ("H", "Y", 0), ("Y", "H", 496),
+        ("H", "gamma", 0), ("Y", "gamma", 112), ("rstd", "X", 508), ("rstd", "gamma", 0), ("rstd", "H", 0),
+        ("rstd", "Y", 508))],
+    *[("rmsnorm_e4m3", dict(NORM8_A, mode=mode), out, over, by) for mode in ("ROW", "TENSOR", "GIVEN") for out, over, by in (
+        ("Q", "X", 0), ("Q", "residual", 496), ("H", "Q", 240), ("Q", "gamma", 0), ("scale", "H", 0),
+        ("scale", "Q", 252), ("scale", "rstd", 0))],
+    ("rmsnorm_e4m3", dict(NORM8_A, mode="ROW"), "scale", "X", 0),
+    ("rmsnorm_e4m3", dict(NORM8_A, mode="ROW"), "rstd", "scale", 12),
+    ("rmsnorm_e4m3", dict(NORM8_A, mode="TENSOR"), "workspace", "X", 496),
+    ("rmsnorm_e4m3", dict(NORM8_A, mode="TENSOR"), "Q", "workspace", 16),
+    *[("rmsnorm_backward", BWD_A, out, over, by) for out, over, by in (
+        ("dX", "H", 0), ("dX", "H", 496), ("dX", "dY", 16), ("dX", "dH", 496), ("dX", "gamma", 0), ("dX", "rstd", 0),
+        ("dgamma", "dX", 0), ("dgamma", "dY", 508), ("dgamma", "gamma", 0), ("workspace", "dY", 0),
+        ("dgamma", "workspace", 0))],
+    *[("w4_matmul", W4_A, "D", over, by) for over, by in (
+        ("A", 0), ("A", 496), ("W", 0), ("W", 8176), ("scales", 0), ("zeros", 496), ("bias", 0), ("residual", 16))],
+    *[("w4_dequantize", DEQ_A, "B", over, by) for over, by in (("W", 0), ("W", 8176), ("scales", 0), ("zeros", 496))],
+    *[("dropout", DROP_A, "Y", over, by) for over, by in (("X", 16), ("residual", 496), ("offset_device", 0))],
+])
+def test_overlaps_are_refused(call, base, out, over, by):
+    assert _status(getattr(gemm_epi, "gemm_epi_" + call), **{**base, out: base[over] + by}) == INVALID
+    if by == 0 and out not in ("rstd", "scale"):  # (those end within 16 bytes)
+        # the other way round: the output begins first
+        assert _status(getattr(gemm_epi, "gemm_epi_" + call), **{**base, over: base[out] + 16}) == INVALID
+
+
 def test_empty_problems_launch_nothing():
     none = dict(stream=0)
     gemm_epi.gemm_epi_rmsnorm(0, 64, "bf16", None, None, None, 1e-6, None, None, **none)
