@@ -85,10 +85,13 @@ gemm_epi_status rmsnorm(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* 
         const Buffer x = {X, 2 * t * d}, r = {residual, 2 * t * d}, g = {gamma, 2 * d}, h = {H, 2 * t * d};
         const Buffer y = {Y, (mode == kRms16 ? 2 : 1) * t * d}, rs = {rstd, 4 * t};
         const Buffer sc = {scale, mode == kRmsRow ? 4 * t : 4};
-        const Buffer ws = {mode == kRmsTensor ? workspace : nullptr, gemm_epi_rmsnorm_workspace(t, d)};
-        const bool ok = apart(h, {g, y, rs, sc, ws}, {x, r}) && apart(rs, {x, r, g, sc, ws}) && apart(ws, {x, r, g, sc}) &&
-                        (mode == kRmsGiven || apart(sc, {x, r, g})) &&
-                        (mode == kRms16 ? apart(y, {g, rs}, {x, r}) : apart(y, {g, rs, sc, ws, x, r}));
+        const Buffer ws = mode == kRmsTensor ? Buffer{workspace, gemm_epi_rmsnorm_workspace(t, d)} : Buffer{nullptr, 0};
+        bool ok = apart(h, {g, y, rs}, {x, r}) && apart(rs, {x, r, g, y});
+        if (mode == kRms16)
+            ok = ok && apart(y, {g}, {x, r});
+        else
+            ok = ok && apart(y, {g, x, r, sc, ws}) && apart(sc, {h, rs, ws}) && apart(ws, {h, rs, x, r, g}) &&
+                 (mode == kRmsGiven || apart(sc, {x, r, g}));
         if (!ok) return GEMM_EPI_ERR_INVALID_ARG;
     }
     int sms = 0;
