@@ -180,9 +180,16 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _dev(t):
+# What a buffer of the plan-less calls holds: elements of a 16-bit type, fp32, E4M3 codes, 64-bit
+# counters, or bytes of any tensor; the floating-point type's name in torch and the bytes of one.
+_KIND = {"f16": ("float16", 2), "bf16": ("bfloat16", 2), "f32": ("float32", 4),
+         "e4m3": ("float8_e4m3fn", 1), "int64": (None, 8), "bytes": (None, 1)}
+
+
+def _dev(t, kind: str = "bytes", count: int = 0):
     """As _ptr, for calls that run without a plan, on the current device: a tensor of the host or
-    of another device is refused."""
+    of another device is refused, and one that does not hold `count` elements of `kind` (a tensor of
+    whole numbers of the same size stands for the bits it holds)."""
     if t is None or isinstance(t, int):
         return t
     if not t.is_cuda:
@@ -191,7 +198,23 @@ def _dev(t):
         raise ValueError("tensors must be on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous (row-major)")
+    if count > 0:
+        name, size = _KIND[kind]
+        if kind != "bytes" and (t.element_size() != size or t.is_complex() or
+                                (t.is_floating_point() and str(t.dtype) != f"torch.{name}")):
+            raise ValueError("a tensor's type is not the one the call reads or writes there")
+        if t.numel() * t.element_size() < count * size:
+            raise ValueError("a tensor has fewer elements than the call's shape")
     return t.data_ptr()
+
+
+def _kind16(dtype: int) -> str:
+    return ("f16", "bf16")[dtype] if dtype in (0, 1) else "bytes"
+
+
+def _times(a: int, b: int) -> int:
+    """a * b; 0 where either is negative (such a shape is the library's to refuse)."""
+    return a * b if a > 0 and b > 0 else 0
 
 
 def _current_device():
@@ -338,33 +361,59 @@ class _CtypesCalls:
         self._lib = lib
 
     def rmsnorm(self, t, d, dtype, X, residual, gamma, eps, H, Y, rstd, stream):
-        return self._lib.gemm_epi_rmsnorm(t, d, dtype, _dev(X), _dev(residual), _dev(gamma), eps,
-                                          _dev(H), _dev(Y), _dev(rstd), _stream(stream))
+        k, td = _kind16(dtype), _times(t, d)
+        return self._lib.gemm_epi_rmsnorm(t, d, dtype, _dev(X, k, td), _dev(residual, k, td),
+                                          _dev(gamma, k, d if t > 0 else 0), eps, _dev(H, k, td),
+                                          _dev(Y, k, td), _dev(rstd, "f32", t), _stream(stream))
 
     def rmsnorm_e4m3(self, t, d, dtype, X, residual, gamma, eps, H, Q, mode, scale, rstd,
                      workspace, stream):
-        return self._lib.gemm_epi_rmsnorm_e4m3(t, d, dtype, _dev(X), _dev(residual), _dev(gamma),
-                                               eps, _dev(H), _dev(Q), mode, _dev(scale),
-                                               _dev(rstd), _dev(workspace), _stream(stream))
+        k, td = _kind16(dtype), _times(t, d)
+        scales = t if mode == SCALE_MODE["ROW"] else int(t > 0)
+        ws = 0
+        if mode == SCALE_MODE["TENSOR"] and t > 0:
+            ws = self._lib.gemm_epi_rmsnorm_workspace(t, d)
+        return self._lib.gemm_epi_rmsnorm_e4m3(t, d, dtype, _dev(X, k, td), _dev(residual, k, td),
+                                               _dev(gamma, k, d if t > 0 else 0), eps,
+                                               _dev(H, k, td), _dev(Q, "e4m3", td), mode,
+                                               _dev(scale, "f32", scales), _dev(rstd, "f32", t),
+                                               _dev(workspace, "bytes", ws), _stream(stream))
 
     def rmsnorm_backward(self, t, d, dtype, dY, H, gamma, rstd, dH, dX, dgamma, workspace, stream):
-        return self._lib.gemm_epi_rmsnorm_backward(t, d, dtype, _dev(dY), _dev(H), _dev(gamma),
-                                                   _dev(rstd), _dev(dH), _dev(dX), _dev(dgamma),
-                                                   _dev(workspace), _stream(stream))
+        k, td = _kind16(dtype), _times(t, d)
+        ws = self._lib.gemm_epi_rmsnorm_workspace(t, d) if t > 0 else 0
+        return self._lib.gemm_epi_rmsnorm_backward(t, d, dtype, _dev(dY, k, td), _dev(H, k, td),
+                                                   _dev(gamma, k, d if t > 0 else 0),
+                                                   _dev(rstd, "f32", t), _dev(dH, k, td),
+                                                   _dev(dX, k, td), _dev(dgamma, "f32", d),
+                                                   _dev(workspace, "bytes", ws), _stream(stream))
 
     def w4_matmul(self, m, n, k, group, dtype, epilog, A, W, scales, zeros, bias, residual, D,
                   stream):
-        return self._lib.gemm_epi_w4_matmul(m, n, k, group, dtype, epilog, _dev(A), _dev(W),
-                                            _dev(scales), _dev(zeros), _dev(bias), _dev(residual),
-                                            _dev(D), _stream(stream))
+        kind, any_, mn = _kind16(dtype), int(m > 0), _times(m, n)
+        scaled = any_ * _times(k // group, n) if group > 0 else 0
+        return self._lib.gemm_epi_w4_matmul(m, n, k, group, dtype, epilog,
+                                            _dev(A, kind, _times(m, k)),
+                                            _dev(W, "bytes", any_ * _times(k // 2, n)),
+                                            _dev(scales, kind, scaled), _dev(zeros, "bytes", scaled),
+                                            _dev(bias, kind, any_ * n), _dev(residual, kind, mn),
+                                            _dev(D, kind, mn), _stream(stream))
 
     def w4_dequantize(self, n, k, group, dtype, W, scales, zeros, B, stream):
-        return self._lib.gemm_epi_w4_dequantize(n, k, group, dtype, _dev(W), _dev(scales),
-                                                _dev(zeros), _dev(B), _stream(stream))
+        kind = _kind16(dtype)
+        scaled = _times(k // group, n) if group > 0 else 0
+        return self._lib.gemm_epi_w4_dequantize(n, k, group, dtype,
+                                                _dev(W, "bytes", _times(k // 2, n)),
+                                                _dev(scales, kind, scaled),
+                                                _dev(zeros, "bytes", scaled),
+                                                _dev(B, kind, _times(k, n)), _stream(stream))
 
     def dropout(self, count, dtype, X, residual, p, seed, offset, offset_device, Y, stream):
-        return self._lib.gemm_epi_dropout(count, dtype, _dev(X), _dev(residual), p, seed, offset,
-                                          _dev(offset_device), _dev(Y), _stream(stream))
+        kind = _kind16(dtype)
+        return self._lib.gemm_epi_dropout(count, dtype, _dev(X, kind, count),
+                                          _dev(residual, kind, count), p, seed, offset,
+                                          _dev(offset_device, "int64", int(count > 0)),
+                                          _dev(Y, kind, count), _stream(stream))
 
 
 _calls = None
@@ -382,7 +431,7 @@ def _bind_calls():
         return _calls
     _fastcall.bind(*(ctypes.cast(getattr(lib, "gemm_epi_" + name), ctypes.c_void_p).value
                      for name in ("rmsnorm", "rmsnorm_e4m3", "rmsnorm_backward", "w4_matmul",
-                                  "w4_dequantize", "dropout")))
+                                  "w4_dequantize", "dropout", "rmsnorm_workspace")))
     _calls = _fastcall
     return _calls
 

@@ -9,6 +9,7 @@ import sublayer_reference as ref
 from activation_epilogue_gb300 import gemm_epi
 from parity_helpers import TOL, rel_err
 from sublayer_reference import TD
+from test_sublayer_refusals import typed_refusals
 
 pytestmark = pytest.mark.gpu
 
@@ -210,3 +211,27 @@ def test_training_sublayer():
     dU64 = (keep * dO.double() * scale)
     size = ((dU64.abs() @ W.double().abs().t()) * (h.detach() * rstd.cpu().double()[:, None]).abs()).sum(0)
     assert ((dgamma.cpu().double() - g64.grad).abs() <= 2.1 * 2.0 ** -8 * size).all()
+
+
+def test_both_marshalling_paths_refuse_other_types_and_short_tensors():
+    def tensor(dtype, count):
+        return torch.zeros(count, device="cuda").to(getattr(torch, dtype))
+
+    typed_refusals(gemm_epi._CtypesCalls(gemm_epi.load_library()), tensor)
+    typed_refusals(gemm_epi._bind_calls(), tensor)
+
+
+def test_tensors_of_whole_numbers_stand_for_their_bits():
+    # 16-bit values as int16, codes as uint8: what a program that packs its own buffers passes
+    X, R = (torch.randn(4, 64, device="cuda").to(torch.bfloat16) for _ in range(2))
+    gamma = torch.rand(64, device="cuda").to(torch.bfloat16)
+    outs = []
+    for cast in (lambda v, t: v, lambda v, t: v.view(t)):
+        H = torch.empty_like(X)
+        Q = torch.empty(4, 64, dtype=torch.float8_e4m3fn, device="cuda")
+        scale = torch.empty(4, device="cuda")
+        gemm_epi.gemm_epi_rmsnorm_e4m3(4, 64, "bf16", cast(X, torch.int16), cast(R, torch.int16),
+                                       cast(gamma, torch.int16), 1e-6, cast(H, torch.int16), cast(Q, torch.uint8),
+                                       "ROW", cast(scale, torch.int32))
+        outs.append((H, Q.view(torch.uint8), scale))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))

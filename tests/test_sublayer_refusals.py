@@ -237,3 +237,74 @@ def test_both_marshalling_paths_agree():
         fast.rmsnorm(1, 2, 3)
     with pytest.raises((TypeError, OverflowError)):
         fast.rmsnorm(2 ** 70, 64, 1, P, None, P, 1e-6, None, P, None, 0)
+
+
+# The tensors of one call each, as (argument's place, type, elements); every other argument in order.
+TYPED_CALLS = [
+    ("rmsnorm", (4, 64, 1, None, None, None, 1e-6, None, None, None, 0),
+     {3: ("bfloat16", 256), 4: ("bfloat16", 256), 5: ("bfloat16", 64), 7: ("bfloat16", 256), 8: ("bfloat16", 256),
+      9: ("float32", 4)}),
+    ("rmsnorm_e4m3", (4, 64, 0, None, None, None, 1e-6, None, None, 0, None, None, None, 0),
+     {3: ("float16", 256), 4: ("float16", 256), 5: ("float16", 64), 7: ("float16", 256), 8: ("float8_e4m3fn", 256),
+      10: ("float32", 4), 11: ("float32", 4)}),
+    ("rmsnorm_e4m3", (4, 64, 0, None, None, None, 1e-6, None, None, 1, None, None, None, 0),
+     {3: ("float16", 256), 5: ("float16", 64), 8: ("float8_e4m3fn", 256), 10: ("float32", 1), 12: (None, 4112)}),
+    ("rmsnorm_backward", (4, 64, 1, None, None, None, None, None, None, None, None, 0),
+     {3: ("bfloat16", 256), 4: ("bfloat16", 256), 5: ("bfloat16", 64), 6: ("float32", 4), 7: ("bfloat16", 256),
+      8: ("bfloat16", 256), 9: ("float32", 64), 10: (None, 4112)}),
+    ("w4_matmul", (2, 128, 64, 32, 0, 4, None, None, None, None, None, None, None, 0),
+     {6: ("float16", 128), 7: (None, 4096), 8: ("float16", 256), 9: (None, 256), 10: ("float16", 128),
+      11: ("float16", 256), 12: ("float16", 256)}),
+    ("w4_dequantize", (128, 64, 32, 1, None, None, None, None, 0),
+     {4: (None, 4096), 5: ("bfloat16", 256), 6: (None, 256), 7: ("bfloat16", 8192)}),
+    ("dropout", (100, 1, None, None, 0.5, 1, 2, None, None, 0),
+     {2: ("bfloat16", 100), 3: ("bfloat16", 100), 7: ("int64", 1), 8: ("bfloat16", 100)}),
+]
+
+
+def typed_refusals(calls, tensor):
+    """Calls that are right but for one tensor, of another type or one element short; `tensor` makes one."""
+    for name, args, tensors in TYPED_CALLS:
+        full = list(args)
+        for i, (dtype, count) in tensors.items():
+            full[i] = tensor(dtype or "uint8", count)
+        for i, (dtype, count) in tensors.items():
+            wrong = [tensor(dtype or "uint8", count - 1)]
+            if dtype:
+                wrong += [tensor(other, 2 * count + 8) for other in ("float64", "float16", "bfloat16", "float32", "uint8")
+                          if other != dtype and (other, dtype) != ("uint8", "float8_e4m3fn")]
+            for bad in wrong:
+                with pytest.raises(ValueError, match="type|fewer"):
+                    getattr(calls, name)(*full[:i], bad, *full[i + 1:])
+
+
+def test_binding_refuses_other_types_and_short_tensors(monkeypatch):
+    class Tensor:
+        is_cuda = True
+
+        def __init__(self, dtype, count):
+            self.dtype, self.count = getattr(torch, dtype), count
+
+        def get_device(self):
+            return 0
+
+        def is_contiguous(self):
+            return True
+
+        def element_size(self):
+            return self.dtype.itemsize
+
+        def numel(self):
+            return self.count
+
+        def is_floating_point(self):
+            return self.dtype.is_floating_point
+
+        def is_complex(self):
+            return self.dtype.is_complex
+
+        def data_ptr(self):
+            return P
+
+    monkeypatch.setattr(gemm_epi, "_current_device", lambda: 0)
+    typed_refusals(gemm_epi._CtypesCalls(gemm_epi.load_library()), Tensor)
