@@ -224,6 +224,28 @@ def test_w4_gelu_over_its_range(dtype):
     ref.check_16(D[0].cpu(), want.cpu(), dtype, error.cpu(), "GELU")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [2, 12])
+def test_w4_gelu_of_every_value(m, dtype):
+    """k = 0: every 16-bit pattern, the far tail (below -13), infinities and NaN with it.  The tail's
+    exponent, up to 15^2 / (2 ln 2) = 163, is rounded to fp32 twice: 2 * 163 * 2^-24 * ln 2 = 1.4e-5 of
+    the tail; fp32 roundings of the two terms, and of the smallest numbers of fp32 (2^-149 each)."""
+    bias = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(TD[dtype]).cuda()
+    D = torch.full((m, 65536), 7.0, dtype=TD[dtype], device="cuda")
+    gemm_epi.gemm_epi_w4_matmul(m, 65536, 0, 128, dtype, "GELU_BIAS", None, None, None, None, bias, None, D)
+    v, D = bias.double().cpu(), D.cpu()
+    assert torch.equal(D[:1].expand(m, -1).contiguous().view(torch.int16), D.view(torch.int16))
+    D = D[0]
+    assert D[v.isnan()].isnan().all() and (D[v == float("inf")] == float("inf")).all()
+    assert (D[v < -15] == 0).all() and (D[v == float("-inf")] == 0).all()
+    finite = v.isfinite()
+    v, D = v[finite], D[finite]
+    tail = v.abs() * 0.5 * torch.special.erfc(v.abs() / 2.0 ** 0.5)
+    want = v.clamp(min=0) - tail
+    error = (1.4e-5 + 4 * ref.F32) * tail + 2 * ref.F32 * v.clamp(min=0) + 4 * 2.0 ** -149
+    ref.check_16(D, want, dtype, error, "GELU")
+
+
 @pytest.mark.parametrize("m", [3, 12, 40])
 def test_w4_k_zero_is_the_epilogue_alone(m):
     bias = torch.randn(64, generator=torch.Generator().manual_seed(1)).to(torch.float16)
