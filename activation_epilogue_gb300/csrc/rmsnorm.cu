@@ -62,6 +62,24 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* part)
     return s;
 }
 
+// bf16 has fp32's exponents, so the squares of a row may leave fp32 where the row and its norm do not:
+// then they are summed again of the row times a power of two.  far_factor: that power, or 0 where
+// the sum s stands.  A sum below 2^-80 has lost up to 2^-149 a square (2^-39 of it over 2^30 columns),
+// unless eps is so much larger that the sum does not matter; one past fp32 has a value above 2^48,
+// which 2^-96 leaves above 2^-48 and below 2^32.  An infinity or a NaN in the row stays one.
+__device__ __forceinline__ float far_factor(float s, float eps)
+{
+    if (s > 3.0e38f || s != s) return 1.262177448e-29f;                    // 2^-96
+    return s < 8.271806126e-25f && eps < 8.881784197e-16f ? 1.208925820e24f  // 2^-80, 2^-50: 2^80
+                                                          : 0.0f;
+}
+
+// rstd from the mean of the squares of the row times `factor`.
+__device__ __forceinline__ float far_rstd(float mean, float factor, float eps)
+{
+    return factor / sqrtf(mean + eps * factor * factor);
+}
+
 // scale = amax / 448 and its reciprocal; zero for a row (tensor) with nothing above 2^-100.
 __device__ __forceinline__ void scale_of(float amax, float& scale, float& inv)
 {
@@ -90,31 +108,31 @@ __host__ __device__ constexpr int rms_block()
 }
 
 // Sum (largest bits) over the T threads of a row, the same in every call and in every one of
-// them.  One barrier: the row after next is the first to write this parity's words again, and
-// no thread gets there before all have read them.
+// them.  One barrier: rows take the words `part` in turn, so that the row after next is the first
+// to write these again, and no thread gets there before all have read them.
 template <int T>
-__device__ __forceinline__ float row_sum(float v, float (&part)[2][32], int parity)
+__device__ __forceinline__ float row_sum(float v, float (&part)[32])
 {
     v = warp_sum(v);
     if constexpr (T == 32) return v;
-    if ((threadIdx.x & 31) == 0) part[parity][threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < T / 32; ++w) s += part[parity][w];
+    for (int w = 0; w < T / 32; ++w) s += part[w];
     return s;
 }
 
 template <int T>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (&part)[2][32], int parity)
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (&part)[32])
 {
     v = __reduce_max_sync(0xFFFFFFFFu, v);
     if constexpr (T == 32) return v;
-    if ((threadIdx.x & 31) == 0) part[parity][threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     uint32_t s = 0;
 #pragma unroll
-    for (int w = 0; w < T / 32; ++w) s = max(s, part[parity][w]);
+    for (int w = 0; w < T / 32; ++w) s = max(s, part[w]);
     return s;
 }
 
@@ -142,8 +160,91 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&y)[8], floa
         *reinterpret_cast<uint2*>(p) = q;
 }
 
+// A far row (bf16) from memory, where H (X without a residual) stands as the same threads stored it:
+// what the kernels do for a near one.  It stands behind a near row's code, which stores nothing for it: a
+// branch between the sum and the outputs took the overlap of the sum's wait with the decoding
+// (ROW, 16384 x 2048: 36.9 us, 41.1 with it), a call registers.  Returns the thread's largest bits of Y.
+template <int T>
+__device__ __forceinline__ uint32_t far_row(const RmsnormArgs& a, int mode, long long r, float factor,
+                                            float (&part)[32], uint32_t (&upart)[32])
+{
+    if constexpr (T > 32) __syncthreads();  // (part, upart and a mark in ws_rstd have been read)
+    const uint16_t* gamma = static_cast<const uint16_t*>(a.gamma);
+    const uint16_t* h = static_cast<const uint16_t*>(a.residual ? a.H : a.X) + r * a.d;
+    const int i0 = threadIdx.x % T;
+    float s = 0.0f;
+#pragma unroll 1
+    for (int c = i0 * 8; c < a.d; c += T * 8) {
+        float x[8];
+        decode8<true>(*reinterpret_cast<const uint4*>(h + c), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(x[e] * factor, x[e] * factor, s);
+    }
+    const float rstd = far_rstd(row_sum<T>(s, part) / static_cast<float>(a.d), factor, a.eps);
+    if (i0 == 0) {
+        if (a.rstd) a.rstd[r] = rstd;
+        if (mode == kRmsTensor) a.ws_rstd[r] = rstd;
+    }
+    float inv = mode == kRmsGiven ? 1.0f / a.scale[0] : 0.0f;
+    uint32_t m = 0;
+#pragma unroll 1
+    for (int pass = mode == kRmsRow ? 0 : 1; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int c = i0 * 8; c < a.d; c += T * 8) {
+            float x[8], g[8];
+            decode8<true>(*reinterpret_cast<const uint4*>(h + c), x);
+            decode8<true>(*reinterpret_cast<const uint4*>(gamma + c), g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * g[e];
+            if (mode == kRmsTensor || pass == 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+            } else if (mode == kRms16) {
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.Y) + r * a.d + c) = encode8<true>(x);
+            } else {
+                store_e4m3(static_cast<uint8_t*>(a.Y) + r * a.d + c, x, inv);
+            }
+        }
+        if (mode == kRmsRow && pass == 0) {
+            float scale;
+            scale_of(__uint_as_float(row_max<T>(m, upart)), scale, inv);
+            if (i0 == 0) a.scale[r] = scale;
+        }
+    }
+    return m;
+}
+
+// The far ones of a block's rows, which ws_rstd marks with minus their factor (tensor scale).
+template <int T>
+__device__ __forceinline__ uint32_t far_rows(const RmsnormArgs& a, float (&part)[32], uint32_t (&upart)[32])
+{
+    constexpr int kRows = T == 32 ? rms_block<T>() / T : 1;
+    uint32_t m = 0;
+    if constexpr (T > 32) __syncthreads();
+    __syncwarp();
+#pragma unroll 1
+    for (long long r = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / T; r < a.t;
+         r += static_cast<long long>(gridDim.x) * kRows) {
+        const float factor = -a.ws_rstd[r];
+        if (factor > 0.0f) m = max(m, far_row<T>(a, kRmsTensor, r, factor, part, upart));
+    }
+    return m;
+}
+
+// Blocks an SM (at least; 0: the compiler's choice), by measurement.  One row a block: 2048 x 2048 to 16
+// bits 6.4 us with 8, 6.9 with the compiler's 12 of fewer registers; 2048 x 8192 21.4 with 4, 22.3 with 3;
+// to E4M3 with row scales 18.9 with 3, 20.4 with 4; 2048 x 16384 to 16 bits 40.3 with 2, 46.1 with 1.
+// Walking (tensor scale): 8192 x 4096 45.8 with 6, 52.4 with 5.
 template <bool BF16, int T, int V, int MODE>
-__global__ void __launch_bounds__(rms_block<T>()) rmsnorm_kernel(const RmsnormArgs a)
+constexpr int rms_blocks()
+{
+    if (MODE == kRmsTensor) return !BF16 ? 0 : T == 32 ? (V < 4 ? 6 : 0) : T == 128 ? (V == 2 ? 8 : 6) : T == 256 ? 3 : 0;
+    if (T == 256) return BF16 && MODE != kRmsRow ? 4 : 0;
+    return (T == 128 || T == 32) && V == 2 ? 8 : T == 512 && (BF16 || MODE != kRms16) ? 2 : 0;
+}
+
+template <bool BF16, int T, int V, int MODE>
+__global__ void __launch_bounds__(rms_block<T>(), rms_blocks<BF16, T, V, MODE>()) rmsnorm_kernel(const RmsnormArgs a)
 {
     constexpr int kRows = rms_block<T>() / T;
     __shared__ float part[2][32];
@@ -154,10 +255,11 @@ __global__ void __launch_bounds__(rms_block<T>()) rmsnorm_kernel(const RmsnormAr
     uint4 gamma[V];
     load_row<T, V>(a.gamma, 0, a.d, gamma);
     const float inv_d = 1.0f / static_cast<float>(a.d);
-    float given = 0.0f;
-    if (MODE == kRmsGiven) given = 1.0f / a.scale[0];
+    const float given = MODE == kRmsGiven ? a.scale[0] : 1.0f;
     uint32_t top = 0;
     int parity = 0;
+    bool any_far = false;
+    // (the grid walks for the tensor scale alone)
     for (long long r = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / T; r < a.t;
          r += static_cast<long long>(gridDim.x) * kRows, parity ^= 1) {
         uint4 h[V];
@@ -190,12 +292,17 @@ __global__ void __launch_bounds__(rms_block<T>()) rmsnorm_kernel(const RmsnormAr
 #pragma unroll
             for (int e = 0; e < 8; ++e) s = fmaf(x[e], x[e], s);
         }
-        const float rstd = 1.0f / sqrtf(row_sum<T>(s, part, parity) * inv_d + a.eps);
+        s = row_sum<T>(s, part[parity]);
+        const float rstd = 1.0f / sqrtf(s * inv_d + a.eps);
+        // a far row's outputs are left to far_row
+        const float factor = BF16 ? far_factor(s, a.eps) : 0.0f;  // (the same in all of the row's threads)
+        const bool far = factor != 0.0f;
+        any_far |= far;
         if (i0 == 0) {
             if (a.rstd) a.rstd[r] = rstd;
-            if (MODE == kRmsTensor) a.ws_rstd[r] = rstd;
+            if (MODE == kRmsTensor) a.ws_rstd[r] = far ? -factor : rstd;
         }
-        float inv = given;
+        float inv = 1.0f / given;  // (here: a division ahead of the row's loads would hold them up)
         if constexpr (MODE == kRmsRow || MODE == kRmsTensor) {
             uint32_t m = 0;
 #pragma unroll
@@ -207,30 +314,35 @@ __global__ void __launch_bounds__(rms_block<T>()) rmsnorm_kernel(const RmsnormAr
                 for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e] * rstd * g[e]) & 0x7FFFFFFFu);
             }
             if constexpr (MODE == kRmsTensor) {
-                top = max(top, m);
-                continue;
+                if (!far) top = max(top, m);
+            } else {
+                float scale;
+                scale_of(__uint_as_float(row_max<T>(m, upart[parity])), scale, inv);
+                if (i0 == 0) a.scale[r] = scale;
             }
-            float scale;
-            scale_of(__uint_as_float(row_max<T>(m, upart, parity)), scale, inv);
-            if (i0 == 0) a.scale[r] = scale;
         }
+        if constexpr (MODE != kRmsTensor) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (j * T + i0) * 8;
-            if (c >= a.d) continue;
-            float x[8], g[8];
-            decode8<BF16>(h[j], x);
-            decode8<BF16>(gamma[j], g);
+            for (int j = 0; j < V; ++j) {
+                const int c = (j * T + i0) * 8;
+                if (c >= a.d || far) continue;
+                float x[8], g[8];
+                decode8<BF16>(h[j], x);
+                decode8<BF16>(gamma[j], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * g[e];
-            if constexpr (MODE == kRms16)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.Y) + r * a.d + c) = encode8<BF16>(x);
-            else
-                store_e4m3(static_cast<uint8_t*>(a.Y) + r * a.d + c, x, inv);
+                for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * g[e];
+                if constexpr (MODE == kRms16)
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.Y) + r * a.d + c) = encode8<BF16>(x);
+                else
+                    store_e4m3(static_cast<uint8_t*>(a.Y) + r * a.d + c, x, inv);
+            }
+            if (far) far_row<T>(a, MODE, r, factor, part[0], upart[0]);
+            break;
         }
     }
     if constexpr (MODE == kRmsTensor) {
-        const uint32_t m = row_max<rms_block<T>()>(top, upart, 0);
+        if (BF16 && any_far) top = max(top, far_rows<T>(a, part[0], upart[0]));
+        const uint32_t m = row_max<rms_block<T>()>(top, upart[0]);
         if (threadIdx.x == 0) a.ws_max[blockIdx.x] = m;
     }
 }
@@ -250,7 +362,7 @@ __global__ void __launch_bounds__(rms_block<T>()) rmsnorm_quantise_kernel(const 
     load_row<T, V>(a.gamma, 0, a.d, gamma);
     uint32_t m = 0;
     for (int i = threadIdx.x; i < parts; i += rms_block<T>()) m = max(m, a.ws_max[i]);
-    m = row_max<rms_block<T>()>(m, upart, 0);
+    m = row_max<rms_block<T>()>(m, upart[0]);
     float scale, inv;
     scale_of(__uint_as_float(m), scale, inv);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.scale[0] = scale;
@@ -346,7 +458,7 @@ __global__ void __launch_bounds__(rms_block<T>()) rmsnorm_backward_kernel(const 
                 dg[j][e] = fmaf(y[e], xh, dg[j][e]);
             }
         }
-        const float mean = row_sum<T>(s, part, parity) * inv_d;
+        const float mean = row_sum<T>(s, part[parity]) * inv_d;
         uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dX) + r * a.d);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -397,13 +509,14 @@ __global__ void __launch_bounds__(rms_block<T>()) rmsnorm_backward_kernel(const 
 // ---- rows longer than that, read again from L1 and L2 for each pass -----------------------
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreadsPerRow) rmsnorm_long_kernel(const RmsnormArgs a)
+__global__ void __launch_bounds__(kThreadsPerRow, 8) rmsnorm_long_kernel(const RmsnormArgs a)
 {
     __shared__ float part[32];
     __shared__ uint32_t upart[32];
     grid_dependency_wait();
     grid_launch_dependents();
     uint32_t cta_max = 0;
+    float far = 0.0f;  // the factor of a far row, the last of them
     for (long long r = blockIdx.x; r < a.t; r += gridDim.x) {
         const uint16_t* x = static_cast<const uint16_t*>(a.X) + r * a.d;
         const uint16_t* res = static_cast<const uint16_t*>(a.residual) + r * a.d;
@@ -424,10 +537,16 @@ __global__ void __launch_bounds__(kThreadsPerRow) rmsnorm_long_kernel(const Rmsn
 #pragma unroll
             for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
         }
-        const float rstd = 1.0f / sqrtf(block_sum(s, part) / static_cast<float>(a.d) + a.eps);
+        s = block_sum(s, part);
+        const float rstd = 1.0f / sqrtf(s / static_cast<float>(a.d) + a.eps);
+        const float factor = BF16 ? far_factor(s, a.eps) : 0.0f;  // (the same in all threads)
         if (threadIdx.x == 0) {
             if (a.rstd) a.rstd[r] = rstd;
-            if (a.mode == kRmsTensor) a.ws_rstd[r] = rstd;
+            if (a.mode == kRmsTensor) a.ws_rstd[r] = factor != 0.0f ? -factor : rstd;
+        }
+        if (factor != 0.0f) {
+            far = factor;
+            continue;
         }
         const uint16_t* h = a.residual ? hout : x;  // (each thread reads back what it wrote)
         const uint16_t* gamma = static_cast<const uint16_t*>(a.gamma);
@@ -465,6 +584,12 @@ __global__ void __launch_bounds__(kThreadsPerRow) rmsnorm_long_kernel(const Rmsn
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.Y) + r * a.d + c) = q;
             }
         }
+    }
+    if (BF16 && far != 0.0f) {
+        if (a.mode == kRmsTensor)
+            cta_max = max(cta_max, block_max(far_rows<kThreadsPerRow>(a, part, upart), upart));
+        else  // (its only row)
+            far_row<kThreadsPerRow>(a, a.mode, blockIdx.x, far, part, upart);
     }
     if (a.mode == kRmsTensor && threadIdx.x == 0) a.ws_max[blockIdx.x] = cta_max;
 }
@@ -639,7 +764,7 @@ cudaError_t rmsnorm_launch_type(const RmsnormArgs& a, cudaStream_t stream)
     if (a.d <= 4096) return rmsnorm_launch_width<BF16, 128, 4>(a, stream);
     if (a.d <= 8192) return rmsnorm_launch_width<BF16, 256, 4>(a, stream);
     if (a.d <= kRmsMaxWidth) return rmsnorm_launch_width<BF16, 512, 4>(a, stream);
-    const int grid = even_grid(a.t, 1, kRmsMaxParts);
+    const int grid = a.mode == kRmsTensor ? even_grid(a.t, 1, kRmsMaxParts) : a.t;
     const cudaError_t e = launch_dependent(rmsnorm_long_kernel<BF16>, grid, kThreadsPerRow, 0, stream, 1, a);
     if (e != cudaSuccess || a.mode != kRmsTensor) return e;
     return launch_dependent(rmsnorm_quantise_long_kernel<BF16>, grid, kThreadsPerRow, 0, stream, 1, a, grid);

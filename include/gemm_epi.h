@@ -352,12 +352,15 @@ gemm_epi_status gemm_epi_layernorm_fold(int64_t d, int64_t f, gemm_epi_dtype dty
  *     H = X + residual, rounded to the 16-bit type (without a residual the norm is of X),
  *     rstd_i = 1 / sqrt(mean_j H_ij^2 + eps),      Y_ij = H_ij rstd_i gamma_j.
  * The norm is of the rounded H, the values that the next sub-layer and the backward pass
- * read; sums and rstd are fp32, Y is rounded once.  X, residual, H, Y: t x d; gamma: d
+ * read; sums and rstd are fp32, Y is rounded once.  A row whose squares leave fp32 (bf16 has fp32's
+ * exponents) is summed times a power of two, so that every finite row has its norm; rstd is infinite
+ * where the root of mean square + eps is below 2^-128.  X, residual, H, Y: t x d; gamma: d
  * elements; all of `dtype` (F16 or BF16), d a multiple of 8, 8 to 2^30, 16-byte aligned.  H is
  * given exactly when the residual is.  H and Y may each be X or the residual itself, but not
- * the same buffer; any other overlap of an output is ERR_INVALID_ARG, here and in the calls below.  rstd: t fp32, 4-byte aligned, or NULL (the backward
- * pass reads it).  eps >= 0.  A NaN or an infinity in a row of H makes that row of Y NaN (or,
- * finite / infinite, 0) as the formula does.  t == 0 launches nothing.  Asynchronous on
+ * the same buffer; any other overlap of an output is ERR_INVALID_ARG, here and in the calls
+ * below.  rstd: t fp32, 4-byte aligned, or NULL (the backward pass reads it).  eps >= 0.  A NaN or
+ * an infinity in a row of H makes that row of Y NaN (or, finite / infinite, 0) as the formula
+ * does.  t == 0 launches nothing.  Asynchronous on
  * `stream`, launched as programmatic dependents of its previous work (which they wait for
  * before they touch memory); the caller owns every buffer, the calls keep nothing, and calls
  * on different streams are independent as long as their buffers are. */

@@ -188,6 +188,70 @@ def test_rmsnorm_given_scale_saturates():
     assert (q[1][big].abs() == 448).all() and (torch.sign(q[1]) == torch.sign(X[1].float())).all()
 
 
+# rows of a bf16 norm whose squares leave fp32: large, largest, one large value among ordinary ones,
+# small, and the smallest normal numbers; ordinary rows between them
+def _far_rows(d, eps):
+    g = torch.Generator().manual_seed(d)
+    X = torch.randn(8, d, generator=g, dtype=torch.float64)
+    X[0] *= 2.0 ** 70
+    X[1] = torch.where(X[1] < 0, -1.0, 1.0) * torch.finfo(torch.bfloat16).max
+    X[2, d // 2] = 2.0 ** 120
+    X[4] *= 2.0 ** -50
+    X[5] *= 2.0 ** -100
+    X[6] = torch.where(X[6] < 0, -1.0, 1.0) * 2.0 ** -126
+    gamma = (1 + 0.3 * torch.randn(d, generator=g)).to(torch.bfloat16)
+    return X.to(torch.bfloat16), gamma
+
+
+@pytest.mark.parametrize("d", [72, 264, 1000, 2048, 4096, 8192, 16384, 20000])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("mode", [None, "ROW"])
+def test_rmsnorm_of_rows_far_from_one(d, eps, mode):
+    X, gamma = _far_rows(d, eps)
+    _, Y, scale, rstd = _forward(X, None, gamma, eps, "bf16", mode)
+    want, wr = ref.rmsnorm(X, gamma, eps)
+    # (a subnormal rstd, of rows around 2^127, is off by up to 2^-150)
+    rel = ref.sum_error(d) / 2 + 6 * ref.F32 + 2.0 ** -150 / wr
+    assert ((rstd.double() - wr).abs() <= rel * wr).all()
+    rel = rel[:, None] + 4 * ref.F32
+    if mode is None:
+        ref.check_16(Y, want, "bf16", rel * want.abs() + 2.0 ** -149, "Y")
+        return
+    top = want.abs().amax(1)
+    assert ((scale.double() - top / 448).abs() <= (rel[:, 0] + 8 * ref.F32) * top / 448 + 2.0 ** -149)[top > 2.0 ** -90].all()
+    for i in range(8):
+        if top[i] < 2.0 ** -100:    # (eps is larger than such a row's squares: zeros, as documented)
+            assert scale[i] == 0 and (Y[i].float() == 0).all()
+        else:
+            ref.check_e4m3(Y[i], want[i] / scale[i].double(), float(rel[i]) + 12 * ref.F32, f"codes of row {i}")
+
+
+def test_rmsnorm_of_far_rows_many_in_a_block():
+    # the blocks of the tensor-scale pass walk the rows: far and ordinary ones in turn, in one block
+    d, eps = 2048, 0.0
+    X, gamma = _far_rows(d, eps)
+    X = X.repeat(700, 1)
+    _, Q, scale, rstd = _forward(X, None, gamma, eps, "bf16", "TENSOR")
+    want, wr = ref.rmsnorm(X[:8], gamma, eps)
+    rel = ref.sum_error(d) / 2 + 6 * ref.F32 + 2.0 ** -150 / wr
+    assert ((rstd[:8].double() - wr).abs() <= rel * wr).all()
+    assert torch.equal(rstd, rstd[:8].repeat(700))
+    assert torch.equal(Q.view(torch.uint8), Q[:8].repeat(700, 1).view(torch.uint8))
+    top = want.abs().max()
+    assert abs(float(scale) - top / 448) <= (rel.max() + 8 * ref.F32) * top / 448
+    ref.check_e4m3(Q[:8], want / scale.double(), float(rel.max()) + 16 * ref.F32, "codes")
+
+
+def test_rmsnorm_backward_of_far_rows():
+    X, gamma = _far_rows(1000, 0.0)
+    _, _, _, rstd = _forward(X, None, gamma, 0.0, "bf16")
+    keep = rstd < 2.0 ** 100        # (the gradient of the smallest rows leaves bf16)
+    X, rstd = X[keep].contiguous(), rstd[keep].contiguous()
+    dy, _, _, _, dh = _bwd_inputs(X.shape[0], 1000, "bf16", 5)
+    dX, dgamma = _backward(dy, X, gamma, rstd, dh, "bf16")
+    _check_bwd(dX, dgamma, dy, X, gamma, rstd, dh, "bf16")
+
+
 # ---- backward -------------------------------------------------------------------------------
 
 def _backward(dy, h, gamma, rstd, dh, dtype, dx=None):
