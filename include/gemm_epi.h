@@ -374,9 +374,10 @@ typedef enum {
     GEMM_EPI_SCALE_GIVEN = 2   /* scale[0] is read: a calibrated scale, 2^-126 or more */
 } gemm_epi_scale_mode;
 
-/* The same norm with Y in E4M3 for an E4M3 plan: Q_ij = Y_ij / scale rounded once from fp32 to
- * the nearest E4M3 value, ties to even, saturated at +-448 (Q: t x d bytes, 16-byte aligned,
- * overlapping nothing else).  The scale is what the plan takes as scale_a: one value (TENSOR,
+/* The same norm with Y in E4M3 for an E4M3 plan: Q_ij = Y_ij * (1 / scale), Y (not rounded to 16
+ * bits) and the reciprocal in fp32, the product rounded to the nearest E4M3 value, ties to even,
+ * saturated at +-448 (next to a halfway point the quotient itself may round to the neighbouring
+ * code).  Q: t x d bytes, 16-byte aligned, overlapping nothing else.  The scale is what the plan takes as scale_a: one value (TENSOR,
  * GIVEN), or one per row (ROW, with GEMM_EPI_OPT_SCALE_A_ROWS); fp32, 4-byte aligned.  A row
  * (tensor) whose largest |Y| is below 2^-100 gets scale 0 and zeros; a NaN gives the row (the
  * tensor) a NaN scale and NaN codes; under GIVEN a NaN stays NaN and an infinity saturates.

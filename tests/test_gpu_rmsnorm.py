@@ -252,6 +252,20 @@ def test_rmsnorm_backward_of_far_rows():
     _check_bwd(dX, dgamma, dy, X, gamma, rstd, dh, "bf16")
 
 
+@pytest.mark.parametrize("t,d", [(37, 264), (300, 1024), (7, 4104), (3, 20000)])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_rmsnorm_codes_are_products_with_the_reciprocal(t, d, mode, dtype):
+    """The codes bit for bit, from the call's own H, rstd and scale: fp32 products in the header's order,
+    times the rounded reciprocal of the scale, rounded once to E4M3."""
+    X, R, gamma = _inputs(t, d, dtype, t * d)
+    H, Q, scale, rstd = _forward(X, R, gamma, 1e-6, dtype, mode, 0.007)
+    y = H.float() * rstd[:, None] * gamma.float()
+    inv = 1.0 / scale.float().view(-1, 1)
+    want = (y * inv).clamp(-448, 448).to(torch.float8_e4m3fn)
+    assert torch.equal(Q.view(torch.uint8), want.view(torch.uint8))
+
+
 # ---- backward -------------------------------------------------------------------------------
 
 def _backward(dy, h, gamma, rstd, dh, dtype, dx=None):
