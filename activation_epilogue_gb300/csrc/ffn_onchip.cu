@@ -269,7 +269,7 @@ __device__ __forceinline__ void oc_epilogue(const OnchipFfnParams& p, uint8_t* s
                 uint4* yp = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.Y) + base);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint4 rr = __ldg(rp + i);
+                    const uint4 rr = rp[i];
                     const uint32_t rw[4] = {rr.x, rr.y, rr.z, rr.w};
                     float y[8];
 #pragma unroll

@@ -842,8 +842,7 @@ __device__ __forceinline__ void backward_factor_row(const GemmParams& p, int epi
     if (epilog == EPI_DRELU_BGRAD) {
         uint32_t mw = 0;
         if (valid > 0)
-            mw = __ldg(static_cast<const uint32_t*>(p.aux_in) + static_cast<long long>(row) * p.aux_ld +
-                       col0 / 32);
+            mw = static_cast<const uint32_t*>(p.aux_in)[static_cast<long long>(row) * p.aux_ld + col0 / 32];
         if (valid < 32) mw &= (1u << valid) - 1u;  // valid == 0 clears every bit
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = ((mw >> j) & 1u) ? v[j] : 0.0f;
@@ -853,7 +852,7 @@ __device__ __forceinline__ void backward_factor_row(const GemmParams& p, int epi
     if (valid == 32) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + q);
+            const uint4 w = reinterpret_cast<const uint4*>(src)[q];
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
@@ -1276,7 +1275,7 @@ __device__ __forceinline__ void run_epilogue(const GemmParams& p, uint8_t* smem,
     grid_dependency_wait();
     // E4M3 inputs: the dequantisation scale, one for the tensor or (scale_a_rows) one per row
     // of A, which is one per lane of the accumulator and is read with each tile's row below
-    const float fp8_tensor_scale = F8 && !p.scale_a_rows ? __ldg(p.scale_a) * __ldg(p.scale_b) : 1.0f;
+    const float fp8_tensor_scale = F8 && !p.scale_a_rows ? *p.scale_a * *p.scale_b : 1.0f;
 
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -1322,7 +1321,7 @@ __device__ __forceinline__ void run_epilogue(const GemmParams& p, uint8_t* smem,
         const int lane_idx = m64 && lane >= 16 ? lane_limit : lane_base + lane;
         float fp8_scale = fp8_tensor_scale;
         if (F8 && p.scale_a_rows)
-            fp8_scale = lane_idx < lane_limit ? __ldg(p.scale_a + lane_idx) * __ldg(p.scale_b) : 0.0f;
+            fp8_scale = lane_idx < lane_limit ? p.scale_a[lane_idx] * *p.scale_b : 0.0f;
         if (*abort_flag) break;
         if (EW == 8 && col_bias) {
             __syncwarp();  // every lane is done reading the previous tile's values
@@ -1330,7 +1329,7 @@ __device__ __forceinline__ void run_epilogue(const GemmParams& p, uint8_t* smem,
             if (col_base + BN <= col_limit && (reinterpret_cast<uintptr_t>(bsrc) & 15) == 0) {
                 // whole tile in range and 16-byte aligned: one 8-element load per lane
                 for (int i8 = lane; i8 < BN / 8; i8 += 32) {
-                    const uint4 w8 = __ldg(reinterpret_cast<const uint4*>(bsrc) + i8);
+                    const uint4 w8 = reinterpret_cast<const uint4*>(bsrc)[i8];
                     const uint32_t ww[4] = {w8.x, w8.y, w8.z, w8.w};
                     float f[8];
 #pragma unroll
@@ -1510,7 +1509,7 @@ __device__ __forceinline__ void run_epilogue(const GemmParams& p, uint8_t* smem,
                         const uint4* rp = reinterpret_cast<const uint4*>(
                             R + static_cast<long long>(lane_idx) * ncols + col0);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) rres[q] = __ldg(rp + q);
+                        for (int q = 0; q < 4; ++q) rres[q] = rp[q];
                     }
                 }
             }
@@ -1677,8 +1676,7 @@ __device__ __forceinline__ void run_epilogue(const GemmParams& p, uint8_t* smem,
                     // lane j < CH fetches the mask word of row t0 + j; bit `lane` of it
                     uint32_t mrow = 0;
                     if (lane < CH && t0 + lane < p.m && word_idx < p.aux_ld)
-                        mrow = __ldg(static_cast<const uint32_t*>(p.aux_in) +
-                                     static_cast<long long>(t0 + lane) * p.aux_ld + word_idx);
+                        mrow = static_cast<const uint32_t*>(p.aux_in)[static_cast<long long>(t0 + lane) * p.aux_ld + word_idx];
 #pragma unroll
                     for (int j = 0; j < CH; ++j) {
                         const uint32_t mw = __shfl_sync(0xFFFFFFFFu, mrow, j);

@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kThreadsPerRow, 8) rmsnorm_long_kernel(const R
         const uint16_t* h = a.residual ? hout : x;  // (each thread reads back what it wrote)
         const uint16_t* gamma = static_cast<const uint16_t*>(a.gamma);
         float inv = 1.0f;
-        if (a.mode == kRmsGiven) inv = 1.0f / __ldg(a.scale);
+        if (a.mode == kRmsGiven) inv = 1.0f / a.scale[0];
         if (a.mode == kRmsRow || a.mode == kRmsTensor) {
             uint32_t m = 0;
             for (int c = threadIdx.x * 8; c < a.d; c += kThreadsPerRow * 8) {

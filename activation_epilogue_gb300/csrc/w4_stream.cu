@@ -71,7 +71,7 @@ template <int G>
 __device__ __forceinline__ void load_words(const uint8_t* src, int t, int left, uint32_t (&w)[4])
 {
     if constexpr (G == 128) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + t * 16));
+        const uint4 v = *reinterpret_cast<const uint4*>(src + t * 16);
         w[0] = v.x;
         w[1] = v.y;
         w[2] = v.z;
@@ -80,7 +80,7 @@ __device__ __forceinline__ void load_words(const uint8_t* src, int t, int left, 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint2 v = make_uint2(0, 0);
-            if (64 * h < left) v = __ldg(reinterpret_cast<const uint2*>(src + 32 * h + t * 8));
+            if (64 * h < left) v = *reinterpret_cast<const uint2*>(src + 32 * h + t * 8);
             w[2 * h] = v.x;
             w[2 * h + 1] = v.y;
         }
@@ -166,8 +166,8 @@ __device__ __forceinline__ void stream_columns(const W4Args& a, uint8_t* smem, i
                 if (row < a.m) {
                     to[j] = row * pitch + (G == 128 ? c ^ (c >> 3 & 1) : c) * 16;
                     if (kseg + c * 8 < a.k)
-                        v[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.A) +
-                                                                    static_cast<long long>(row) * a.k + kseg + c * 8));
+                        v[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.A) +
+                                                               static_cast<long long>(row) * a.k + kseg + c * 8);
                 }
                 c += kThreads;
                 while (c >= chunks) {
