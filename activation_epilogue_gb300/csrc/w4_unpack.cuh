@@ -5,6 +5,7 @@
 #include "kernel_params.h"
 #include "ptx.cuh"
 #include "vec16.cuh"
+#include "wait_time.h"
 
 namespace gemm_epi {
 
@@ -139,7 +140,7 @@ struct W4UnpackInOrder {
 };
 
 // Waits of these kernels are for copies and arithmetic of the block itself, so they end; should
-// one not, `failed` is set after two seconds and the block writes NaN.
+// one not, `failed` is set after two seconds of the kernel's own time and the block writes NaN.
 constexpr unsigned long long kW4WaitNs = 2000ull * 1000 * 1000;
 
 // One try suspends the thread for up to kW4TryNs: a waiting warp takes no issue slots from the
@@ -162,10 +163,10 @@ __device__ __forceinline__ bool w4_try_wait(uint32_t bar, uint32_t parity)
 __device__ __forceinline__ bool w4_wait(uint32_t bar, uint32_t parity, volatile int* failed)
 {
     if (w4_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    WaitTime waited(globaltimer_ns());
     for (unsigned long long poll = 1; poll < kW4WaitNs / 8; ++poll) {
         if (w4_try_wait(bar, parity)) return true;
-        if (*failed || globaltimer_ns() - t0 > kW4WaitNs) break;
+        if (*failed || waited.at(globaltimer_ns()) > kW4WaitNs) break;
     }
     *failed = 1;
     return false;

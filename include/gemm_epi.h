@@ -377,10 +377,11 @@ typedef enum {
 /* The same norm with Y in E4M3 for an E4M3 plan: Q_ij = Y_ij * (1 / scale), Y (not rounded to 16
  * bits) and the reciprocal in fp32, the product rounded to the nearest E4M3 value, ties to even,
  * saturated at +-448 (next to a halfway point the quotient itself may round to the neighbouring
- * code).  Q: t x d bytes, 16-byte aligned, overlapping nothing else.  The scale is what the plan takes as scale_a: one value (TENSOR,
- * GIVEN), or one per row (ROW, with GEMM_EPI_OPT_SCALE_A_ROWS); fp32, 4-byte aligned.  A row
- * (tensor) whose largest |Y| is below 2^-100 gets scale 0 and zeros; a NaN gives the row (the
- * tensor) a NaN scale and NaN codes; under GIVEN a NaN stays NaN and an infinity saturates.
+ * code).  Q: t x d bytes, 16-byte aligned, overlapping nothing else.  The scale is what the plan
+ * takes as scale_a: one value (TENSOR, GIVEN), or one per row (ROW, with
+ * GEMM_EPI_OPT_SCALE_A_ROWS); fp32, 4-byte aligned.  A row (tensor) whose largest |Y| is below
+ * 2^-100 gets scale 0 and zeros; a NaN gives the row (the tensor) a NaN scale and NaN codes; under
+ * GIVEN a NaN stays NaN and an infinity saturates.
  * workspace: for TENSOR, gemm_epi_rmsnorm_workspace(t, d) bytes of device memory, 16-byte
  * aligned, that no other call uses until this one has run; ignored otherwise. */
 gemm_epi_status gemm_epi_rmsnorm_e4m3(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* X,
@@ -410,17 +411,18 @@ int64_t gemm_epi_rmsnorm_workspace(int64_t t, int64_t d);
  * contiguous along k, two values per byte, the lower half first; q in 0..15), scales is
  * k/group rows of n values of `dtype`, and zeros k/group rows of n bytes (0..15), or NULL for
  * z = 8 everywhere; s and z are those of row i / group and column j.  group is 32, 64 or 128;
- * k a multiple of group, n a multiple of 8, both at most 2^30.  For decoding: m is 1 to 64 rows of A (0 launches
- * nothing); for more, gemm_epi_w4_dequantize and a plan.  A: m x k, bias: n elements (the
- * (1,n) layout), residual and D: m x n, of `dtype` (F16 or BF16); epilogs BIAS, RELU_BIAS,
- * GELU_BIAS, TANH_BIAS, BIAS_RESIDUAL and NONE as for plans; bias is NULL exactly for NONE,
- * the residual given exactly for BIAS_RESIDUAL, and D may be the residual itself (and overlaps
- * nothing else: ERR_INVALID_ARG).  The differences q - z are exact in 16 bits and their products with A are summed in fp32, group
- * by group, with the scales applied in fp32.  A, W, scales, residual and D 16-byte aligned,
- * zeros 8-byte, bias 2-byte.  No workspace, no plan; asynchronous on `stream` as above (ahead of the
- * wait L2 may be asked for a part of W, which is read after it).  (The
- * kernel for more than a few rows waits for its own copies and products with a limit of two
- * seconds; should one run out, it ends and writes NaN.) */
+ * k a multiple of group, n a multiple of 8, both at most 2^30.  For decoding: m is 1 to 64 rows
+ * of A (0 launches nothing); for more, gemm_epi_w4_dequantize and a plan.  A: m x k, bias: n
+ * elements (the (1,n) layout), residual and D: m x n, of `dtype` (F16 or BF16); epilogs BIAS,
+ * RELU_BIAS, GELU_BIAS, TANH_BIAS, BIAS_RESIDUAL and NONE as for plans (GELU to the output's
+ * rounding); bias is NULL exactly for NONE, the residual given exactly for BIAS_RESIDUAL, and D may
+ * be the residual itself (and overlaps nothing else: ERR_INVALID_ARG).  The differences q - z are
+ * exact in 16 bits and their products with A are summed in fp32, group by group, with the scales
+ * applied in fp32.  A, W, scales, residual and D 16-byte aligned, zeros 8-byte, bias 2-byte.  No
+ * workspace, no plan; asynchronous on `stream` as above (ahead of the wait L2 may be asked for a
+ * part of W, which is read after it).  (The kernel for more than a few rows waits for its own
+ * copies and products, with a limit of two seconds of its own running time.  There is no plan whose
+ * status could tell of a wait that ran out: the block then ends and writes NaN.) */
 gemm_epi_status gemm_epi_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group,
                                    gemm_epi_dtype dtype, gemm_epi_epilog epilog, const void* A,
                                    const void* W, const void* scales, const uint8_t* zeros,
