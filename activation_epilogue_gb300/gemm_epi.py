@@ -199,13 +199,17 @@ def _dev(t, kind: str = "bytes", count: int = 0):
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous (row-major)")
     if count > 0:
-        name, size = _KIND[kind]
-        if kind != "bytes" and (t.element_size() != size or t.is_complex() or
-                                (t.is_floating_point() and str(t.dtype) != f"torch.{name}")):
-            raise ValueError("a tensor's type is not the one the call reads or writes there")
-        if t.numel() * t.element_size() < count * size:
-            raise ValueError("a tensor has fewer elements than the call's shape")
+        _check_holds(t, kind, count)
     return t.data_ptr()
+
+
+def _check_holds(t, kind: str, count: int):
+    name, size = _KIND[kind]
+    if kind != "bytes" and (t.element_size() != size or t.is_complex() or
+                            (t.is_floating_point() and str(t.dtype) != f"torch.{name}")):
+        raise ValueError("a tensor's type is not the one the call reads or writes there")
+    if t.numel() * t.element_size() < count * size:
+        raise ValueError("a tensor has fewer elements than the call's shape")
 
 
 def _kind16(dtype: int) -> str:
@@ -293,7 +297,8 @@ def _operands(A, B, bias, residual, D, aux, aux_in, dbias, ln=None, scales=None)
 def gemm_epi_execute_operands(plan, A, B, D, bias=None, residual=None, aux=None, aux_in=None,
                               dbias=None, stream=None, ln=None, scales=None):
     """ln: (stats, colsum, bias_folded) for the LN_GELU_BIAS epilog; scales: (scale_a,
-    scale_b) device fp32 scalars for E4M3 plans (B is then given transposed, n x k)."""
+    scale_b) device fp32 scalars for E4M3 plans (B is then given transposed, n x k); with the
+    option SCALE_A_ROWS scale_a holds m values."""
     ops = _operands(A, B, bias, residual, D, aux, aux_in, dbias, ln, scales)
     _check(load_library().gemm_epi_execute_operands(plan, ctypes.byref(ops), _stream(stream)),
            "gemm_epi_execute_operands")
@@ -635,12 +640,22 @@ class Plan:
     def __init__(self, m, n, k, dtype="bf16", epilog="BIAS", bias_layout="1N", **options):
         self.m, self.n, self.k = m, n, k
         self.dtype, self.epilog, self.bias_layout = dtype, epilog, bias_layout
+        self._scales_a = 1  # values in scale_a
         self.handle = gemm_epi_plan(m, n, k, dtype, epilog, bias_layout)
         for key, value in options.items():
-            gemm_epi_plan_set_option(self.handle, key.upper(), value)
+            self.set_option(key, value)
 
     def set_option(self, option: str, value: int):
         gemm_epi_plan_set_option(self.handle, option.upper(), value)
+        if option.upper() == "SCALE_A_ROWS":
+            self._scales_a = self.m if value else 1
+
+    def _checked(self, scales):
+        """scales, whose tensors hold fp32 and as many values as the plan reads."""
+        for t, count in zip(scales or (), (self._scales_a, 1)):
+            if t is not None and not isinstance(t, int) and self.m > 0 and self.n > 0:
+                _check_holds(t, "f32", count)
+        return scales
 
     def describe(self) -> str:
         return gemm_epi_plan_describe(self.handle)
@@ -649,7 +664,7 @@ class Plan:
                 dbias=None, ln=None, scales=None):
         gemm_epi_execute_operands(self.handle, A, B, D, bias=bias, residual=residual, aux=aux,
                                   aux_in=aux_in, dbias=dbias, stream=stream, ln=ln,
-                                  scales=scales)
+                                  scales=self._checked(scales))
 
     def execute_host(self, A, B, bias, D, aux=None, residual=None, stream=None):
         gemm_epi_execute_host(self.handle, A, B, D, bias=bias, residual=residual, aux=aux,
@@ -659,7 +674,7 @@ class Plan:
                         aux_in=None, dbias=None, ln=None, scales=None):
         gemm_epi_execute_operands_unfused(self.handle, A, B, D, pre, bias=bias, residual=residual,
                                           aux=aux, aux_in=aux_in, dbias=dbias, stream=stream,
-                                          ln=ln, scales=scales)
+                                          ln=ln, scales=self._checked(scales))
 
     def sync_status(self, stream=None) -> int:
         return gemm_epi_sync_status(self.handle, stream)

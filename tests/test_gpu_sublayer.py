@@ -67,6 +67,22 @@ def test_row_scale_option_is_for_e4m3_plans():
     gemm_epi.Plan(64, 64, 64, "bf16", "BIAS", "1N", SCALE_A_ROWS=0).free()
 
 
+def test_row_scaled_plan_refuses_short_scales():
+    A, Bt = (torch.zeros(64, 64, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    D = torch.zeros(64, 64, dtype=torch.bfloat16, device="cuda")
+    one, rows = torch.ones(1, device="cuda"), torch.ones(64, device="cuda")
+    with gemm_epi.Plan(64, 64, 64, "e4m3", "NONE", SCALE_A_ROWS=1) as plan:
+        plan.execute(A, Bt, None, D, scales=(rows, one))
+        for scales in ((one, one), (rows[:63], one), (rows.double(), one), (rows, one[:0])):
+            with pytest.raises(ValueError, match="type|fewer"):
+                plan.execute(A, Bt, None, D, scales=scales)
+            with pytest.raises(ValueError, match="type|fewer"):
+                plan.execute_unfused(A, Bt, None, D, D, scales=scales)
+        plan.set_option("SCALE_A_ROWS", 0)
+        plan.execute(A, Bt, None, D, scales=(one, one))
+        assert plan.sync_status() == 0
+
+
 @pytest.mark.parametrize("mode", ["ROW", "TENSOR"])
 def test_norm_into_e4m3_product(mode):
     """H = X + R, Q = E4M3(RMS norm), D = GELU(dequantised Q . W + b) in one stream."""
