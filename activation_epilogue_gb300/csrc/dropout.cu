@@ -41,7 +41,6 @@ constexpr int kThreads = 256;
 constexpr int kPerThread = 2;  // generator blocks (of 8 elements) per thread
 
 // A thread's 8 elements of generator block b, loaded; beyond the end zeros.
-template <bool BF16>
 __device__ __forceinline__ uint4 load_block(const uint16_t* p, long long b, long long count)
 {
     if (b * 8 + 8 <= count) return *reinterpret_cast<const uint4*>(p + b * 8);
@@ -65,8 +64,8 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs a)
     uint4 x4[kPerThread], r4[kPerThread];
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-        x4[i] = load_block<BF16>(X, first + i * kThreads, a.count);
-        if (RES) r4[i] = load_block<BF16>(R, first + i * kThreads, a.count);
+        x4[i] = load_block(X, first + i * kThreads, a.count);
+        if (RES) r4[i] = load_block(R, first + i * kThreads, a.count);
     }
     // a word's upper 16 bits are >= drop when the word is >= drop << 16, its lower 16 bits when
     // the word shifted up is; drop = 65536 (keep nothing) is a threshold that zero words miss
