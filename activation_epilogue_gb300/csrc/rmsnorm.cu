@@ -9,10 +9,12 @@
 // sums of dgamma are fp32; H, Y and dX are rounded once each, E4M3 codes once from fp32 (they are
 // y times the rounded reciprocal of the scale, as the header says).
 // Measured (bf16, 6.79 TB/s copy): 16384 x 8192 with the residual to 16 bits 152 us and to E4M3
-// with a scale per row 133 us (104 % of the copy rate), backward 163 us (97 %); 2039 x 4096 to
-// E4M3 11 us (78 %: a start and an end of short blocks), one row of 4096 1.5 us.  One scale for the tensor
-// has to read H a second time: 177 us for 16384 x 8192, at the copy rate for the 9 bytes an
-// element that it moves.
+// with a scale per row 131 us (105 % of the copy rate), backward 163 us (97 %); 2039 x 4096 to
+// E4M3 10.4 us (83 %: a start and an end of short blocks), one row of 4096 1.6 us.  One scale for
+// the tensor has to read H a second time: 177 us for 16384 x 8192, at the copy rate for the 9 bytes
+// an element that it moves.  Rows wider than 16384 columns are passed over again for each sum: 4096 x
+// 20480 to 16 bits 119 us (83 %), row scales 115 (75 %), tensor scale 138, given 108, backward 170 (58 %);
+// 2048 x 65536 206, 227, 231, 189 and 268 us.
 #include <cuda_fp8.h>
 
 #include "kernel_params.h"
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(rms_block<T>(), rms_blocks<BF16, T, V, MODE>()
 
 // Second pass of the per-tensor scale: the largest of the first pass's maxima, then the codes.
 // It walks the rows from the last to the first, so that it begins with the rows of H that the
-// first pass left in L2.
+// first pass left in L2 (2 % of a call at most, as the loads and stores past L2).
 template <bool BF16, int T, int V>
 __global__ void __launch_bounds__(rms_block<T>()) rmsnorm_quantise_kernel(const RmsnormArgs a, int parts)
 {
@@ -738,7 +740,7 @@ template <bool BF16, int T, int V>
 cudaError_t rmsnorm_launch_width(const RmsnormArgs& a, cudaStream_t stream)
 {
     constexpr int kBlock = rms_block<T>(), kRows = kBlock / T;
-    // A block per row (four for T = 32): 16384x8192 with E4M3 rows 133 us, against 145-163 with
+    // A block per row (four for T = 32): 16384x8192 with E4M3 rows 131 us, against 145-163 with
     // 304 to 1024 blocks that walk the rows.  The first pass of the tensor scale walks, since
     // its blocks' maxima are read by every block of the second.
     const int grid = even_grid(a.t, kRows, a.mode == kRmsTensor ? 912 : (1ll << 31) - 1);

@@ -3,7 +3,8 @@
 //
 // The product, D^T = W A^T, streams the weight once: W's rows (columns of D) are the 16 MMA
 // rows of mma.m16n8k16, rows of A its 8 columns, so even one row of A uses the tensor cores
-// and every weight is unpacked once for up to 64 rows.  For a few rows that is 4 bits of
+// and every weight is unpacked once for the up to 16 rows that this kernel takes (more, and the
+// larger weights, go to w4_stream.cu and w4_tensor.cu).  For a few rows that is 4 bits of
 // traffic per 2 m flops, bound by the weight's bytes.
 //
 //   * A block takes 16 MT CW columns of D and all of k (or a cluster's share of it), in stages of
@@ -19,12 +20,13 @@
 //   * A group's sum is complete in the accumulator (groups are whole MMAs, all of whose lanes
 //     are in one group), so the scale multiplies an fp32 sum, and no weight is ever rounded.
 //   * The KW warps' sums meet in shared memory, in order; then the epilogue.
-// Measured (bf16, groups of 128): 4096 x 4096 with one row 4.4 us, 4096 x 1024 2.3; 8 rows of
-// 8192 x 8192 14.2 us, with groups of 64 of 16384 x 8192 26.9 (37 % of the copy rate for the
-// weight's bytes; with one row of 8192 columns, k 16384, the loads alone took 13.4 us, the
-// arithmetic alone 17.6, both 22.7: the larger weights of up to 4 rows have a kernel of their own,
-// w4_stream.cu).  Tried and left: bulk copies of rows by one warp (33 us: 75 cycles for each copy of
-// 512 bytes), 16 warps a block (26.6), 256 values of k per warp and stage (22.8).
+// Measured (bf16, groups of 128, weights from DRAM): 4096 x 4096 with one row 5.0 us, 4096 x 1024
+// 2.8; 8 rows of 8192 x 8192 14.0 us, with groups of 64 of 16384 x 8192 26.3 (40 % of the copy rate
+// for the weight's bytes); groups of 32 with one row 5.3 us, 2.9, and 8192 x 8192 13.2.  With one row of
+// 8192 columns, k 16384, the loads alone took 13.4 us, the arithmetic alone 17.6, both 22.7: the larger
+// weights of up to 4 rows have a kernel of their own.  Tried and left: bulk copies of rows by one warp
+// (33 us: 75 cycles for each copy of 512 bytes), 16 warps a block (26.6), 256 values of k per warp and
+// stage (22.8).
 #include "kernel_params.h"
 #include "launch.h"
 #include "ptx.cuh"
@@ -298,8 +300,9 @@ cudaError_t w4_launch_one(const W4Args& a, int sms, cudaStream_t stream)
     int smem = STAGES * S::bytes(a.m);
     const int red = S::kKW * NT * 8 * (S::kCols + 1) * 4;
     if (smem < red) smem = red;
-    // k split over a cluster while that leaves an SM for every block (1024x4096, one row:
-    // 3.4 us whole, 3.2 in 4, 4.3 in 8; 4096x4096, 48 rows: 36.8 whole, 13.7 in 4, 26.4 in 8)
+    // k split over a cluster while that leaves an SM for every block (1024 columns, k 4096, one row:
+    // 4.5 us whole, 3.9 in 2, 3.75 in 4, 4.2 in 8; 12 rows 12.7, 8.4, 5.4 and 4.85; 4096x4096, one row,
+    // where 128 blocks have 128 SMs: 5.0 whole, 5.4 in 2, 8.3 in 4; 8 rows 5.5, 5.7 and 9.0)
     int cluster = 1;
     while (cluster < 8 && tiles * cluster * 2 <= sms && steps >= 2 * cluster) cluster *= 2;
     return launch_dependent(kernel, tiles * cluster, kThreadsW4, smem, stream, cluster, a, cluster);

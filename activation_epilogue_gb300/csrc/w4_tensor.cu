@@ -28,9 +28,9 @@
 //     store D.
 // A chain's waits are for its own earlier blocks alone, in order, so that no wait can take an
 // older phase of a barrier for the one it needs.
-// Measured (16384x8192, bf16, 48 rows): 25.1 us with groups of 128, 30.5 with 64, 39.2 with 32
+// Measured (16384x8192, bf16, 48 rows): 24.5 us with groups of 128, 30.5 with 64, 39.0 with 32
 // (a group's hand-over from the issuer to the summing warps costs more than its MMAs); about
-// 6 us of each is start and end (4096x1024: 6.4 us), the rest 580 cycles a block of 128 x 128
+// 6 us of each is start and end (4096x1024: 6.8 us), the rest 580 cycles a block of 128 x 128
 // against some 370 for the unpacking instructions alone and for the weight's bytes.  A block takes
 // 2000 warp instructions with groups of 128, 2600 with 64 (1080 of them unpacking), on 66 to 70 %
 // of the issue slots.  Tried and left: all columns of a group loaded at once (64: 32.2 us, 32:
@@ -547,6 +547,8 @@ cudaError_t launch_one(const W4Args& a, const CUtensorMap& map, int sms, cudaStr
     const cudaError_t e = allow_smem(kernel, Layout<NP, G>::kBytes, prepared);
     if (e != cudaSuccess) return e;
     const int tiles = (a.n + kCols - 1) / kCols, blocks = (a.k + kBlockK - 1) / kBlockK;
+    // (48 rows, k 8192, groups of 128: 8192 columns in clusters of two 16.4 us, 9856 to 16384 with a block
+    // each 24.4 to 24.6, 20480 with a second wave 48.9)
     int cluster = sms / tiles;
     if (cluster > 8) cluster = 8;
     if (cluster > blocks / 4) cluster = blocks / 4;
