@@ -226,6 +226,25 @@ def test_rmsnorm_of_rows_far_from_one(d, eps, mode):
             ref.check_e4m3(Y[i], want[i] / scale[i].double(), float(rel[i]) + 12 * ref.F32, f"codes of row {i}")
 
 
+@pytest.mark.parametrize("d", [72, 1000, 4096, 16384, 20000])
+@pytest.mark.parametrize("which", ["H=X,Y=R", "H=R,Y=X", "H=R", "Y=X"])
+def test_rmsnorm_of_far_rows_in_place(d, which):
+    X, gamma = _far_rows(d, 0.0)
+    R = X.flip(1).contiguous() if "H" in which else None
+    H0, Y0, _, r0 = _forward(X, R, gamma, 0.0, "bf16")
+    want, wr = ref.rmsnorm(X if R is None else H0, gamma, 0.0)
+    near = (wr > 0) & (wr < 2.0 ** 126)     # (not the row that X + R overflows, nor subnormal ones)
+    rel = ref.sum_error(d) / 2 + 10 * ref.F32 + 2.0 ** -150 / wr
+    ref.check_16(Y0[near], want[near], "bf16", rel[near, None] * want[near].abs() + 2.0 ** -149, "Y")
+    bufs = dict(X=X.cuda(), R=None if R is None else R.cuda())
+    out = dict(H=None if R is None else torch.empty_like(bufs["X"]), Y=torch.empty_like(bufs["X"]))
+    out.update({part[0]: bufs[part[2]] for part in which.split(",")})
+    rstd = torch.empty(8, device="cuda")
+    gemm_epi.gemm_epi_rmsnorm(8, d, "bf16", bufs["X"], bufs["R"], gamma.cuda(), 0.0, out["H"], out["Y"], rstd)
+    same = torch.equal(out["Y"].cpu().view(torch.int16), Y0.view(torch.int16)) and torch.equal(rstd.cpu(), r0)
+    assert same and (R is None or torch.equal(out["H"].cpu(), H0))
+
+
 def test_rmsnorm_of_far_rows_many_in_a_block():
     # the blocks of the tensor-scale pass walk the rows: far and ordinary ones in turn, in one block
     d, eps = 2048, 0.0
