@@ -26,8 +26,8 @@ decltype(&gemm_epi_dropout) p_dropout;
 decltype(&gemm_epi_rmsnorm_workspace) p_rmsnorm_workspace;
 
 // What a buffer holds: the call's 16-bit type (by its number in the ABI), fp32, E4M3 codes, 64-bit
-// counters, or bytes of any tensor.
-enum class Kind { kF16 = 0, kBf16 = 1, kF32, kE4m3, kInt64, kBytes };
+// counters, bytes of packed whole numbers, or bytes of any tensor.
+enum class Kind { kF16 = 0, kBf16 = 1, kF32, kE4m3, kInt64, kPacked, kBytes };
 
 Kind kind16(int64_t dtype) { return dtype == 0 ? Kind::kF16 : dtype == 1 ? Kind::kBf16 : Kind::kBytes; }
 
@@ -57,8 +57,9 @@ at::ScalarType type_of(Kind kind)
 // A tensor of whole numbers stands for the bits it holds; floating-point types have to be the kind's.
 bool stands_for(const at::Tensor& t, Kind kind)
 {
-    return kind == Kind::kBytes || (static_cast<int64_t>(t.element_size()) == bytes_per(kind) &&
-                                    c10::isIntegralType(t.scalar_type(), true));
+    if (kind == Kind::kBytes) return true;
+    return c10::isIntegralType(t.scalar_type(), true) &&
+           (kind == Kind::kPacked || static_cast<int64_t>(t.element_size()) == bytes_per(kind));
 }
 
 // a * b, 0 where either is negative (such a shape is the library's to refuse), at most 2^62.
@@ -226,8 +227,8 @@ PyObject* w4_matmul(PyObject*, PyObject* const* args, Py_ssize_t n)
         const Kind k16 = kind16(dtype);
         const bool any = m > 0;
         const int64_t mn = times(m, cols), scaled = any && group > 0 ? times(k / group, cols) : 0;
-        void *A = a.pointer(6, k16, times(m, k)), *W = a.pointer(7, Kind::kBytes, any ? times(k / 2, cols) : 0);
-        void *scales = a.pointer(8, k16, scaled), *zeros = a.pointer(9, Kind::kBytes, scaled);
+        void *A = a.pointer(6, k16, times(m, k)), *W = a.pointer(7, Kind::kPacked, any ? times(k / 2, cols) : 0);
+        void *scales = a.pointer(8, k16, scaled), *zeros = a.pointer(9, Kind::kPacked, scaled);
         void *bias = a.pointer(10, k16, any ? cols : 0), *residual = a.pointer(11, k16, mn), *D = a.pointer(12, k16, mn);
         const cudaStream_t stream = a.stream(13);
         return unlocked(a, p_w4_matmul, m, cols, k, group, dtype_of(dtype),
@@ -242,8 +243,8 @@ PyObject* w4_dequantize(PyObject*, PyObject* const* args, Py_ssize_t n)
         const int64_t cols = a.integer(0), k = a.integer(1), group = a.integer(2), dtype = a.integer(3);
         const Kind k16 = kind16(dtype);
         const int64_t scaled = group > 0 ? times(k / group, cols) : 0;
-        void *W = a.pointer(4, Kind::kBytes, times(k / 2, cols)), *scales = a.pointer(5, k16, scaled);
-        void *zeros = a.pointer(6, Kind::kBytes, scaled), *B = a.pointer(7, k16, times(k, cols));
+        void *W = a.pointer(4, Kind::kPacked, times(k / 2, cols)), *scales = a.pointer(5, k16, scaled);
+        void *zeros = a.pointer(6, Kind::kPacked, scaled), *B = a.pointer(7, k16, times(k, cols));
         const cudaStream_t stream = a.stream(8);
         return unlocked(a, p_w4_dequantize, cols, k, group, dtype_of(dtype), W, scales,
                         static_cast<const uint8_t*>(zeros), B, stream);

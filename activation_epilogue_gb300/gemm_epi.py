@@ -181,9 +181,10 @@ def _ptr(t):
 
 
 # What a buffer of the plan-less calls holds: elements of a 16-bit type, fp32, E4M3 codes, 64-bit
-# counters, or bytes of any tensor; the floating-point type's name in torch and the bytes of one.
+# counters, bytes of packed whole numbers, or bytes of any tensor; the floating-point type's name in
+# torch and the bytes of one.
 _KIND = {"f16": ("float16", 2), "bf16": ("bfloat16", 2), "f32": ("float32", 4),
-         "e4m3": ("float8_e4m3fn", 1), "int64": (None, 8), "bytes": (None, 1)}
+         "e4m3": ("float8_e4m3fn", 1), "int64": (None, 8), "packed": (None, 1), "bytes": (None, 1)}
 
 
 def _dev(t, kind: str = "bytes", count: int = 0):
@@ -205,7 +206,7 @@ def _dev(t, kind: str = "bytes", count: int = 0):
 
 def _check_holds(t, kind: str, count: int):
     name, size = _KIND[kind]
-    if kind != "bytes" and (t.element_size() != size or t.is_complex() or
+    if kind != "bytes" and ((t.element_size() != size and kind != "packed") or t.is_complex() or
                             (t.is_floating_point() and str(t.dtype) != f"torch.{name}")):
         raise ValueError("a tensor's type is not the one the call reads or writes there")
     if t.numel() * t.element_size() < count * size:
@@ -399,8 +400,8 @@ class _CtypesCalls:
         scaled = any_ * _times(k // group, n) if group > 0 else 0
         return self._lib.gemm_epi_w4_matmul(m, n, k, group, dtype, epilog,
                                             _dev(A, kind, _times(m, k)),
-                                            _dev(W, "bytes", any_ * _times(k // 2, n)),
-                                            _dev(scales, kind, scaled), _dev(zeros, "bytes", scaled),
+                                            _dev(W, "packed", any_ * _times(k // 2, n)),
+                                            _dev(scales, kind, scaled), _dev(zeros, "packed", scaled),
                                             _dev(bias, kind, any_ * n), _dev(residual, kind, mn),
                                             _dev(D, kind, mn), _stream(stream))
 
@@ -408,9 +409,9 @@ class _CtypesCalls:
         kind = _kind16(dtype)
         scaled = _times(k // group, n) if group > 0 else 0
         return self._lib.gemm_epi_w4_dequantize(n, k, group, dtype,
-                                                _dev(W, "bytes", _times(k // 2, n)),
+                                                _dev(W, "packed", _times(k // 2, n)),
                                                 _dev(scales, kind, scaled),
-                                                _dev(zeros, "bytes", scaled),
+                                                _dev(zeros, "packed", scaled),
                                                 _dev(B, kind, _times(k, n)), _stream(stream))
 
     def dropout(self, count, dtype, X, residual, p, seed, offset, offset_device, Y, stream):

@@ -253,17 +253,18 @@ TYPED_CALLS = [
      {3: ("bfloat16", 256), 4: ("bfloat16", 256), 5: ("bfloat16", 64), 6: ("float32", 4), 7: ("bfloat16", 256),
       8: ("bfloat16", 256), 9: ("float32", 64), 10: (None, 4112)}),
     ("w4_matmul", (2, 128, 64, 32, 0, 4, None, None, None, None, None, None, None, 0),
-     {6: ("float16", 128), 7: (None, 4096), 8: ("float16", 256), 9: (None, 256), 10: ("float16", 128),
+     {6: ("float16", 128), 7: ("uint8", 4096), 8: ("float16", 256), 9: ("uint8", 256), 10: ("float16", 128),
       11: ("float16", 256), 12: ("float16", 256)}),
     ("w4_dequantize", (128, 64, 32, 1, None, None, None, None, 0),
-     {4: (None, 4096), 5: ("bfloat16", 256), 6: (None, 256), 7: ("bfloat16", 8192)}),
+     {4: ("uint8", 4096), 5: ("bfloat16", 256), 6: ("uint8", 256), 7: ("bfloat16", 8192)}),
     ("dropout", (100, 1, None, None, 0.5, 1, 2, None, None, 0),
      {2: ("bfloat16", 100), 3: ("bfloat16", 100), 7: ("int64", 1), 8: ("bfloat16", 100)}),
 ]
 
 
 def typed_refusals(calls, tensor):
-    """Calls that are right but for one tensor, of another type or one element short; `tensor` makes one."""
+    """Calls that are right but for one tensor, of another type or one element short; `tensor` makes one.
+    (None: a workspace, bytes of any tensor.)"""
     for name, args, tensors in TYPED_CALLS:
         full = list(args)
         for i, (dtype, count) in tensors.items():
