@@ -304,6 +304,72 @@ gemm_epi_status ensure_split_ws(gemm_epi_plan_s* p)
     return GEMM_EPI_OK;
 }
 
+// E4M3 with scales for blocks of 128 of k: CTA pairs on 256 x 256 tiles, or, for few rows of A, tiles of
+// 128 columns by up to 128 rows with K split over a cluster.
+gemm_epi_status configure_blocks(gemm_epi_plan_s* p)
+{
+    const bool square = p->scale_blocks == GEMM_EPI_SCALE_BLOCKS_SQUARE;
+    p->k_blocks = static_cast<int>((p->k + 127) / 128);
+    const int64_t column_tiles = (p->n + 127) / 128;
+    int v = p->opt_variant;
+    if (v == 0) v = p->m <= 128 || column_tiles * ((p->m + 127) / 128) <= p->sm_count ? 2 : 3;
+    if (v != 2 && v != 3) return GEMM_EPI_ERR_INVALID_ARG;
+    if (v == 3) {
+        if (p->opt_bn != 0 && p->opt_bn != 256) return GEMM_EPI_ERR_INVALID_ARG;
+        const GemmParams none = {};
+        const cudaError_t e = square ? block_pair_square(p->epilog, none, 0, nullptr, false, true)
+                                     : block_pair_rows(p->epilog, none, 0, nullptr, false, true);
+        const cudaError_t e2 = square ? block_pair_square(GEMM_EPI_NONE, none, 0, nullptr, false, true)
+                                      : block_pair_rows(GEMM_EPI_NONE, none, 0, nullptr, false, true);
+        if (e != cudaSuccess || e2 != cudaSuccess || rowpair_prepare(256) != cudaSuccess) return GEMM_EPI_ERR_LAUNCH;
+        long long pairs = rowpair_max_clusters(256);  // (the same shared memory)
+        if (pairs > p->sm_count / 2) pairs = p->sm_count / 2;
+        if (p->opt_grid > 0 && p->opt_grid / 2 < pairs) pairs = p->opt_grid / 2;
+        if (pairs < 1) return GEMM_EPI_ERR_LAUNCH;
+        p->variant = kRowPair;
+        p->bn = 256;
+        p->tiles_m = static_cast<int>((p->m + 255) / 256);
+        p->tiles_n = static_cast<int>((p->n + 255) / 256);
+        p->stages = rowpair_stages(256);
+        p->smem = rowpair_smem_bytes(256);
+        const long long tiles = static_cast<long long>(p->tiles_m) * p->tiles_n;
+        if (tiles > (1ll << 30)) return GEMM_EPI_ERR_UNSUPPORTED_SHAPE;
+        if (pairs > tiles) pairs = tiles;
+        p->kb_per_split = p->k_blocks;
+        p->grid = static_cast<int>(2 * pairs);
+        int gm = p->opt_group_m ? p->opt_group_m : 8;
+        if (gm > p->tiles_m) gm = p->tiles_m;
+        p->group_m = gm < 1 ? 1 : gm;
+        return GEMM_EPI_OK;
+    }
+    int np = p->opt_bn;
+    if (np == 0) {
+        np = 16;
+        while (np < 128 && np < p->m) np *= 2;
+    }
+    if (np != 16 && np != 32 && np != 64 && np != 128) return GEMM_EPI_ERR_INVALID_ARG;
+    const int64_t row_tiles = (p->m + np - 1) / np;
+    int split = p->opt_split_k;
+    if (split == 0) {
+        const int64_t fit = p->sm_count / (column_tiles * row_tiles);
+        split = static_cast<int>(fit < 1 ? 1 : fit > 8 ? 8 : fit);
+        if (split > p->k_blocks / 4) split = p->k_blocks / 4 > 1 ? p->k_blocks / 4 : 1;
+    }
+    if (split > p->k_blocks) split = p->k_blocks;
+    if (column_tiles * row_tiles * split > (1ll << 30)) return GEMM_EPI_ERR_UNSUPPORTED_SHAPE;
+    if (block_swapped(np, square, GemmParams{}, 0, nullptr, false, true) != cudaSuccess) return GEMM_EPI_ERR_LAUNCH;
+    p->variant = kBlockSwapped;
+    p->bn = np;
+    p->tiles_m = static_cast<int>(column_tiles);
+    p->tiles_n = static_cast<int>(row_tiles);
+    p->split = split;
+    p->kb_per_split = (p->k_blocks + split - 1) / split;
+    p->stages = block_swapped_stages(np);
+    p->smem = block_swapped_smem(np);
+    p->grid = static_cast<int>(column_tiles * row_tiles * split);
+    return GEMM_EPI_OK;
+}
+
 gemm_epi_status configure(gemm_epi_plan_s* p)
 {
     p->maps_valid = false;
@@ -320,6 +386,9 @@ gemm_epi_status configure(gemm_epi_plan_s* p)
         p->variant = kEmpty;
     } else if (p->k == 0) {
         p->variant = kBiasOnly;
+    } else if (p->scale_blocks) {
+        const gemm_epi_status st = configure_blocks(p);
+        if (st != GEMM_EPI_OK) return st;
     } else if (p->dtype == GEMM_EPI_E4M3) {
         // E4M3: the CTA-pair kernel with 256 x 256 or 256 x 224 tiles (the width with fewer
         // waves, as for 16-bit inputs) and 128-deep K blocks, any shape
@@ -532,7 +601,7 @@ gemm_epi_status configure(gemm_epi_plan_s* p)
         p->dyn_order = want && p->d_sched != nullptr;
     }
     static const char* vname[] = {"empty", "row-tile", "swapped", "bias-only", "row-pair",
-                                  "small-m"};
+                                  "small-m", "block-swapped"};
     static const char* ename[] = {"BIAS",          "RELU_BIAS",     "GELU_BIAS",
                                   "RELU_AUX_BIAS", "BIAS_RESIDUAL", "NONE",
                                   "TANH_BIAS",     "GELU_AUX_BIAS", "DRELU_BGRAD",
@@ -594,9 +663,12 @@ gemm_epi_status ensure_maps(gemm_epi_plan_s* p, const void* A, const void* B, vo
     if (p->dtype == GEMM_EPI_E4M3) {
         // A [m][k] and B transposed [n][k], bytes, K-major boxes {128 k, 128 rows} (A) and
         // {128 k, bn / 2 rows} (B: each CTA's half of a tile's columns); D bf16
+        // (few rows of A: boxes of bn rows of A, 128 of B, and D is stored without a map)
         const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-        const uint32_t b_rows = static_cast<uint32_t>(p->bn / 2);
-        if (!encode_2d(&p->tm_A, A, u8, p->k, p->m, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B, 1) ||
+        const bool swapped = p->variant == kBlockSwapped;
+        const uint32_t a_rows = swapped ? static_cast<uint32_t>(p->bn) : 128u;
+        const uint32_t b_rows = swapped ? 128u : static_cast<uint32_t>(p->bn / 2);
+        if (!encode_2d(&p->tm_A, A, u8, p->k, p->m, 128, a_rows, CU_TENSOR_MAP_SWIZZLE_128B, 1) ||
             !encode_2d(&p->tm_B, B, u8, p->k, p->n, 128, b_rows, CU_TENSOR_MAP_SWIZZLE_128B, 1) ||
             !encode_2d(&p->tm_D, D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p->n, p->m, 32, 32,
                        CU_TENSOR_MAP_SWIZZLE_64B))
@@ -727,7 +799,13 @@ gemm_epi_status launch_gemm(gemm_epi_plan_s* p, const gemm_epi_operands& ops, in
         prm.b_ld = p->ldb ? p->ldb : p->n;
     }
     cudaError_t e;
-    if (p->variant == kRowPair && p->dtype == GEMM_EPI_E4M3)
+    if (p->variant == kBlockSwapped)
+        e = block_swapped(p->bn, p->scale_blocks == GEMM_EPI_SCALE_BLOCKS_SQUARE, prm, p->grid, stream, pdl, false);
+    else if (p->variant == kRowPair && p->scale_blocks == GEMM_EPI_SCALE_BLOCKS_SQUARE)
+        e = block_pair_square(epilog, prm, p->grid, stream, pdl, false);
+    else if (p->variant == kRowPair && p->scale_blocks == GEMM_EPI_SCALE_BLOCKS_ROWS)
+        e = block_pair_rows(epilog, prm, p->grid, stream, pdl, false);
+    else if (p->variant == kRowPair && p->dtype == GEMM_EPI_E4M3)
         e = fp8_pair_launch(p->bn, prm, p->grid, stream, pdl);
     else if (p->variant == kRowPair)
         e = rowpair_launch(p->bn, prm, p->grid, stream, pdl);
@@ -807,7 +885,8 @@ gemm_epi_status check_operands(const gemm_epi_plan_s* p, const gemm_epi_operands
     if (p->variant == kEmpty) return GEMM_EPI_OK;
     const bool f8 = p->dtype == GEMM_EPI_E4M3;
     if ((o.scale_a != nullptr) != f8 || (o.scale_b != nullptr) != f8) return GEMM_EPI_ERR_INVALID_ARG;
-    if (f8 && (!aligned(o.scale_a, 4) || !aligned(o.scale_b, 4))) return GEMM_EPI_ERR_MISALIGNED;
+    if (f8 && (!aligned(o.scale_a, 4) || !aligned(o.scale_b, p->scale_blocks == GEMM_EPI_SCALE_BLOCKS_ROWS ? 16 : 4)))
+        return GEMM_EPI_ERR_MISALIGNED;
     const bool ln = e == GEMM_EPI_LN_GELU_BIAS;
     if (((o.ln_stats != nullptr) != ln) || ((o.ln_colsum != nullptr) != ln) ||
         ((o.ln_bias != nullptr) != ln))
@@ -972,9 +1051,15 @@ gemm_epi_status gemm_epi_plan_set_option(gemm_epi_plan_t p, gemm_epi_option opt,
         p->b_ready = static_cast<int>(value);
         return GEMM_EPI_OK;
     case GEMM_EPI_OPT_SCALE_A_ROWS:
-        if (value != 0 && (value != 1 || p->dtype != GEMM_EPI_E4M3)) return GEMM_EPI_ERR_INVALID_ARG;
+        if (value != 0 && (value != 1 || p->dtype != GEMM_EPI_E4M3 || p->scale_blocks)) return GEMM_EPI_ERR_INVALID_ARG;
         p->scale_a_rows = static_cast<int>(value);
         return GEMM_EPI_OK;
+    case GEMM_EPI_OPT_SCALE_BLOCKS:
+        if (value < 0 || value > GEMM_EPI_SCALE_BLOCKS_ROWS ||
+            (value != 0 && (p->dtype != GEMM_EPI_E4M3 || p->scale_a_rows)))
+            return GEMM_EPI_ERR_INVALID_ARG;
+        p->scale_blocks = static_cast<int>(value);
+        break;
     case GEMM_EPI_OPT_DEBUG_STALL:
         if (value != 0 && value != 1) return GEMM_EPI_ERR_INVALID_ARG;
         p->debug_stall = static_cast<int>(value);

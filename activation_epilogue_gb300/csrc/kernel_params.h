@@ -68,6 +68,7 @@ struct GemmParams {
     // (n x k, K-major boxes {128 k, 128 n}); K blocks are 128 deep; the accumulator is
     // multiplied by *scale_a * *scale_b before the bias, or by scale_a[row] * *scale_b where
     // scale_a_rows is set.
+    // (Scales for blocks of 128 of k: the kernels of gemm_block_*.cu, laid out as told there.)
     const float* scale_a;
     const float* scale_b;
     int scale_a_rows;
@@ -209,6 +210,18 @@ int rowpair_max_clusters(int bn);
 // GELU_BIAS, RELU_AUX_BIAS, BIAS_RESIDUAL, NONE.
 cudaError_t fp8_pair_prepare();
 cudaError_t fp8_pair_launch(int bn, const GemmParams& p, int grid, cudaStream_t stream, bool pdl);
+
+// E4M3 products with a scale for each block of 128 of k (gemm_block_*.cu): GemmParams::scale_a holds
+// k_blocks rows of m fp32, scale_b k_blocks rows of ceil(n / 128) (square: a scale for each 128 x 128
+// block of B) or of n (one for each row of it).  CTA pairs on 256 x 256 tiles, epilogs as
+// fp8_pair_launch; prepare: set the kernel's shared memory instead of launching it.
+cudaError_t block_pair_square(int epilog, const GemmParams& p, int grid, cudaStream_t stream, bool pdl, bool prepare);
+cudaError_t block_pair_rows(int epilog, const GemmParams& p, int grid, cudaStream_t stream, bool pdl, bool prepare);
+// Few rows of A: tiles of 128 columns (tiles_m of them) by np rows (tiles_n; 16, 32, 64 or 128), K over a
+// cluster of `split` blocks; grid = tiles_m * tiles_n * split.
+cudaError_t block_swapped(int np, bool square, const GemmParams& p, int grid, cudaStream_t stream, bool pdl, bool prepare);
+int block_swapped_smem(int np);
+int block_swapped_stages(int np);
 
 // The FFN block in one CTA-pair launch (256 x 256 tiles); never a programmatic dependent.
 cudaError_t ffn_pair_prepare();

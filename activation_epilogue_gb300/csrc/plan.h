@@ -13,7 +13,7 @@
 
 namespace gemm_epi_impl {
 
-enum Variant { kEmpty = 0, kRowTile = 1, kSwapped = 2, kBiasOnly = 3, kRowPair = 4, kSmallM = 5 };
+enum Variant { kEmpty = 0, kRowTile = 1, kSwapped = 2, kBiasOnly = 3, kRowPair = 4, kSmallM = 5, kBlockSwapped = 6 };
 
 constexpr int kSwappedMaxM = 256;
 // A plan's own device words: the status word (byte 0) and the tile counter (bytes 8-15).
@@ -53,6 +53,7 @@ struct gemm_epi_plan_s {
     int no_pdl;    // 1: launch without programmatic dependent launch (GEMM_EPI_OPT_PDL = 0)
     int b_ready;   // 1: no earlier work on the stream writes B (GEMM_EPI_OPT_B_READY)
     int scale_a_rows;  // E4M3: scale_a holds one scale per row of A (GEMM_EPI_OPT_SCALE_A_ROWS)
+    int scale_blocks;  // E4M3: scales for blocks of 128 of k (GEMM_EPI_OPT_SCALE_BLOCKS)
     unsigned long long wait_limit_ns;
     int debug_stall;
     int* d_status;

@@ -23,7 +23,8 @@ BACKWARD = ("DRELU_BGRAD", "DGELU_BGRAD")
 BIAS_LAYOUT = {"M1": 0, "1N": 1}
 OPTION = {"VARIANT": 0, "TILE_N": 1, "SPLIT_K": 2, "GRID": 3, "GROUP_M": 4,
           "WAIT_LIMIT_US": 5, "DEBUG_STALL": 6, "PREFETCH": 7, "PDL": 8, "SPLIT_MODE": 9,
-          "TILE_M": 10, "TILE_ORDER": 11, "B_READY": 12, "SCALE_A_ROWS": 13}
+          "TILE_M": 10, "TILE_ORDER": 11, "B_READY": 12, "SCALE_A_ROWS": 13,
+          "SCALE_BLOCKS": 14}
 STATUS = {0: "OK", 1: "ERR_INVALID_ARG", 2: "ERR_UNSUPPORTED_SHAPE", 3: "ERR_MISALIGNED",
           4: "ERR_NO_DEVICE", 5: "ERR_ARCH", 6: "ERR_ALLOC", 7: "ERR_LAUNCH",
           8: "ERR_DEVICE_TIMEOUT", 9: "ERR_SCRATCH_LIMIT"}
@@ -299,7 +300,8 @@ def gemm_epi_execute_operands(plan, A, B, D, bias=None, residual=None, aux=None,
                               dbias=None, stream=None, ln=None, scales=None):
     """ln: (stats, colsum, bias_folded) for the LN_GELU_BIAS epilog; scales: (scale_a,
     scale_b) device fp32 scalars for E4M3 plans (B is then given transposed, n x k); with the
-    option SCALE_A_ROWS scale_a holds m values."""
+    option SCALE_A_ROWS scale_a holds m values, with SCALE_BLOCKS = 1 (2) ceil(k / 128) rows of m, and
+    scale_b as many rows of ceil(n / 128) (of n)."""
     ops = _operands(A, B, bias, residual, D, aux, aux_in, dbias, ln, scales)
     _check(load_library().gemm_epi_execute_operands(plan, ctypes.byref(ops), _stream(stream)),
            "gemm_epi_execute_operands")
@@ -641,19 +643,24 @@ class Plan:
     def __init__(self, m, n, k, dtype="bf16", epilog="BIAS", bias_layout="1N", **options):
         self.m, self.n, self.k = m, n, k
         self.dtype, self.epilog, self.bias_layout = dtype, epilog, bias_layout
-        self._scales_a = 1  # values in scale_a
+        self._scales = {"SCALE_A_ROWS": 0, "SCALE_BLOCKS": 0}
         self.handle = gemm_epi_plan(m, n, k, dtype, epilog, bias_layout)
         for key, value in options.items():
             self.set_option(key, value)
 
     def set_option(self, option: str, value: int):
         gemm_epi_plan_set_option(self.handle, option.upper(), value)
-        if option.upper() == "SCALE_A_ROWS":
-            self._scales_a = self.m if value else 1
+        if option.upper() in self._scales:
+            self._scales[option.upper()] = int(value)
 
     def _checked(self, scales):
         """scales, whose tensors hold fp32 and as many values as the plan reads."""
-        for t, count in zip(scales or (), (self._scales_a, 1)):
+        counts = (self.m if self._scales["SCALE_A_ROWS"] else 1, 1)
+        if self._scales["SCALE_BLOCKS"]:
+            blocks = -(-self.k // 128)
+            counts = (blocks * self.m,
+                      blocks * (self.n if self._scales["SCALE_BLOCKS"] == 2 else -(-self.n // 128)))
+        for t, count in zip(scales or (), counts):
             if t is not None and not isinstance(t, int) and self.m > 0 and self.n > 0:
                 _check_holds(t, "f32", count)
         return scales

@@ -204,12 +204,33 @@ typedef enum {
                                        read waits; the small-m kernel then only brings its
                                        slab of B into L2 ahead of the wait, which needs no
                                        promise.  The host-buffer call ignores it */
-    GEMM_EPI_OPT_SCALE_A_ROWS = 13  /* E4M3 plans: 1 = scale_a holds m fp32 scales, one for each
+    GEMM_EPI_OPT_SCALE_A_ROWS = 13, /* E4M3 plans: 1 = scale_a holds m fp32 scales, one for each
                                        row of A (gemm_epi_rmsnorm_e4m3 with
                                        GEMM_EPI_SCALE_ROW), D = epi(scale_a[i] * scale_b *
                                        (A.B) + bias); 0 (default) = one scale.  Other plans:
                                        ERR_INVALID_ARG for 1 */
+    GEMM_EPI_OPT_SCALE_BLOCKS = 14  /* E4M3 plans: a scale for each block of 128 of k (a
+                                       gemm_epi_scale_blocks; 0 = none, the default).  It
+                                       comes before the options that its kernels alone take.
+                                       Other plans, and together with SCALE_A_ROWS:
+                                       ERR_INVALID_ARG for 1 and 2 */
 } gemm_epi_option;
+
+/* E4M3 plans with GEMM_EPI_OPT_SCALE_BLOCKS (K = ceil(k / 128) blocks of k, the last one of what is
+ * left; block b holds columns 128 b ... of A and of the transposed B):
+ *     D_ij = epi(sum_b scale_a[b][i] scale_b[b][j'] (sum of A_ik B_kj over k in block b) + bias)
+ * scale_a: K rows of m fp32.  scale_b: K rows of ceil(n / 128) fp32 and j' = j / 128 (SQUARE), or K rows
+ * of n and j' = j (ROWS; 16-byte aligned): what gemm_epi_e4m3_quantize and gemm_epi_layernorm_e4m3
+ * write.  Each block's sum is an fp32 sum of its own; the blocks' sums times their scales are added in
+ * fp32 in the order of k (with SPLIT_K in order within a slice, then the slices'), the same in every
+ * call.  The product of two scales is formed in fp32 and has to be finite in it.  Epilogs as for the
+ * other E4M3 plans, both bias layouts.  VARIANT is 0 (automatic), 3 (CTA pairs, TILE_N 256) or 2 (few
+ * rows of A: TILE_N 16, 32, 64 or 128 rows of D, SPLIT_K slices over a cluster); B_READY and the wait
+ * limit hold for the latter as for the swapped kernel. */
+typedef enum {
+    GEMM_EPI_SCALE_BLOCKS_SQUARE = 1, /* B (n x k, transposed) in blocks of 128 x 128 */
+    GEMM_EPI_SCALE_BLOCKS_ROWS = 2    /* B in blocks of 1 x 128: a scale for each row */
+} gemm_epi_scale_blocks;
 
 /*
  * Make a plan for one problem shape, dtype, epilog and bias layout (the page's
