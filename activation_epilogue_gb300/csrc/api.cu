@@ -908,6 +908,15 @@ gemm_epi_status check_operands(const gemm_epi_plan_s* p, const gemm_epi_operands
         (o.residual && !aligned(o.residual, 16)) || (o.bias && !aligned(o.bias, 2)) ||
         (o.aux && !aligned(o.aux, aux_align)) || (o.aux_in && !aligned(o.aux_in, aux_in_align)))
         return GEMM_EPI_ERR_MISALIGNED;
+    if (p->scale_blocks) {
+        const int64_t blocks = (p->k + 127) / 128;
+        const int64_t per_block = p->scale_blocks == GEMM_EPI_SCALE_BLOCKS_ROWS ? p->n : (p->n + 127) / 128;
+        const Buffer d = {o.D, 2 * p->m * p->n}, aux = {o.aux, 4 * p->m * ((p->n + 31) / 32)};
+        const Buffer r = {o.residual, 2 * p->m * p->n}, a = {o.A, p->m * p->k}, b = {o.B, p->n * p->k};
+        const Buffer bias = {o.bias, 2 * (p->bias_layout == GEMM_EPI_BIAS_M1 ? p->m : p->n)};
+        const Buffer sa = {o.scale_a, 4 * blocks * p->m}, sb = {o.scale_b, 4 * blocks * per_block};
+        if (!apart(d, {a, b, bias, sa, sb, aux}, {r}) || !apart(aux, {a, b, bias, sa, sb})) return GEMM_EPI_ERR_INVALID_ARG;
+    }
     return GEMM_EPI_OK;
 }
 

@@ -1,5 +1,5 @@
-// The binding's argument marshalling in C++ for the calls a model makes for every token (the RMS
-// norm, the 4-bit products, dropout): torch tensors to addresses, then the C ABI call.  It does
+// The binding's argument marshalling in C++ for the calls a model makes for every token (the
+// norms, the 4-bit and block-scaled E4M3 products, dropout): torch tensors to addresses, then the C ABI call.  It does
 // what the ctypes path of gemm_epi.py does, with the same checks (device, layout, and type and size
 // against the call's shape), and stands in for it where the headers of Python and torch were there
 // at build time.  Host time of a six-tensor call (GB300's
@@ -24,6 +24,12 @@ decltype(&gemm_epi_w4_matmul) p_w4_matmul;
 decltype(&gemm_epi_w4_dequantize) p_w4_dequantize;
 decltype(&gemm_epi_dropout) p_dropout;
 decltype(&gemm_epi_rmsnorm_workspace) p_rmsnorm_workspace;
+decltype(&gemm_epi_layernorm_forward) p_layernorm_forward;
+decltype(&gemm_epi_layernorm_e4m3) p_layernorm_e4m3;
+decltype(&gemm_epi_layernorm_backward) p_layernorm_backward;
+decltype(&gemm_epi_layernorm_workspace) p_layernorm_workspace;
+decltype(&gemm_epi_e4m3_quantize) p_e4m3_quantize;
+decltype(&gemm_epi_execute_operands) p_execute_operands;
 
 // What a buffer holds: the call's 16-bit type (by its number in the ABI), fp32, E4M3 codes, 64-bit
 // counters, bytes of packed whole numbers, or bytes of any tensor.
@@ -266,13 +272,105 @@ PyObject* dropout(PyObject*, PyObject* const* args, Py_ssize_t n)
     });
 }
 
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to; }
+
+PyObject* layernorm_forward(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return call(args, n, 12, p_layernorm_forward != nullptr, [](Args& a) {
+        const int64_t t = a.integer(0), d = a.integer(1), dtype = a.integer(2), td = times(t, d), row = t > 0 ? d : 0;
+        const Kind k16 = kind16(dtype);
+        void *X = a.pointer(3, k16, td), *R = a.pointer(4, k16, td), *gamma = a.pointer(5, k16, row);
+        void* beta = a.pointer(6, k16, row);
+        const float eps = a.real(7);
+        void *H = a.pointer(8, k16, td), *Y = a.pointer(9, k16, td), *stats = a.pointer(10, Kind::kF32, times(t, 2));
+        const cudaStream_t stream = a.stream(11);
+        return unlocked(a, p_layernorm_forward, t, d, dtype_of(dtype), X, R, gamma, beta, eps, H, Y,
+                        static_cast<float*>(stats), stream);
+    });
+}
+
+PyObject* layernorm_e4m3(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return call(args, n, 13, p_layernorm_e4m3 != nullptr, [](Args& a) {
+        const int64_t t = a.integer(0), d = a.integer(1), dtype = a.integer(2), td = times(t, d), row = t > 0 ? d : 0;
+        const Kind k16 = kind16(dtype);
+        void *X = a.pointer(3, k16, td), *R = a.pointer(4, k16, td), *gamma = a.pointer(5, k16, row);
+        void* beta = a.pointer(6, k16, row);
+        const float eps = a.real(7);
+        void *H = a.pointer(8, k16, td), *Q = a.pointer(9, Kind::kE4m3, td);
+        void *scale = a.pointer(10, Kind::kF32, d > 0 ? times(t, up(d, 128)) : 0), *stats = a.pointer(11, Kind::kF32, times(t, 2));
+        const cudaStream_t stream = a.stream(12);
+        return unlocked(a, p_layernorm_e4m3, t, d, dtype_of(dtype), X, R, gamma, beta, eps, H, Q,
+                        static_cast<float*>(scale), static_cast<float*>(stats), stream);
+    });
+}
+
+PyObject* layernorm_backward(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return call(args, n, 13, p_layernorm_backward != nullptr, [](Args& a) {
+        const int64_t t = a.integer(0), d = a.integer(1), dtype = a.integer(2), td = times(t, d);
+        const Kind k16 = kind16(dtype);
+        void *dY = a.pointer(3, k16, td), *H = a.pointer(4, k16, td), *gamma = a.pointer(5, k16, t > 0 ? d : 0);
+        void *stats = a.pointer(6, Kind::kF32, times(t, 2)), *dH = a.pointer(7, k16, td), *dX = a.pointer(8, k16, td);
+        void *dgamma = a.pointer(9, Kind::kF32, d), *dbeta = a.pointer(10, Kind::kF32, d);
+        void* workspace = a.pointer(11, Kind::kBytes, t > 0 && !a.bad ? p_layernorm_workspace(t, d) : 0);
+        const cudaStream_t stream = a.stream(12);
+        return unlocked(a, p_layernorm_backward, t, d, dtype_of(dtype), dY, H, gamma,
+                        static_cast<const float*>(stats), dH, dX, static_cast<float*>(dgamma),
+                        static_cast<float*>(dbeta), workspace, stream);
+    });
+}
+
+PyObject* e4m3_quantize(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return call(args, n, 10, p_e4m3_quantize != nullptr, [](Args& a) {
+        const int64_t rows = a.integer(0), cols = a.integer(1), dtype = a.integer(2), block = a.integer(3);
+        const bool any = rows > 0 && cols > 0 && rows < 1ll << 40 && cols < 1ll << 40;
+        const int64_t rb = any ? up(rows, 128) : 0, cb = any ? up(cols, 128) : 0;
+        const bool square = block == GEMM_EPI_BLOCK_128X128;
+        void *X = a.pointer(4, kind16(dtype), times(rows, cols)), *Q = a.pointer(5, Kind::kE4m3, times(rows, cols));
+        void* scale = a.pointer(6, Kind::kF32, times(cb, square ? rb : rows));
+        void* Qt = a.pointer(7, Kind::kE4m3, any ? times(cols, up(rows, 16) * 16) : 0);
+        void* scale_t = a.pointer(8, Kind::kF32, times(rb, square ? cb : cols));
+        const cudaStream_t stream = a.stream(9);
+        return unlocked(a, p_e4m3_quantize, rows, cols, dtype_of(dtype), static_cast<gemm_epi_block>(block), X, Q,
+                        static_cast<float*>(scale), Qt, static_cast<float*>(scale_t), stream);
+    });
+}
+
+// A plan with scales for blocks of 128: (plan, m, n, k, SCALE_BLOCKS, bias values, A, B, bias, residual, D,
+// aux, scale_a, scale_b, stream)
+PyObject* block_product(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return call(args, n, 15, p_execute_operands != nullptr, [](Args& a) {
+        void* plan = reinterpret_cast<void*>(static_cast<uintptr_t>(a.word(0)));
+        const int64_t m = a.integer(1), cols = a.integer(2), k = a.integer(3), blocks = a.integer(4);
+        const int64_t bias_values = a.integer(5), mn = times(m, cols), kb = mn > 0 && k > 0 ? up(k, 128) : 0;
+        const int64_t any = mn > 0;
+        gemm_epi_operands o = {};
+        o.A = a.pointer(6, Kind::kE4m3, any * times(m, k));
+        o.B = a.pointer(7, Kind::kE4m3, any * times(cols, k));
+        o.bias = a.pointer(8, Kind::kBf16, any * bias_values);
+        o.residual = a.pointer(9, Kind::kBf16, mn);
+        o.D = a.pointer(10, Kind::kBf16, mn);
+        o.aux = a.pointer(11, Kind::kBytes, any * times(m, up(cols, 32) * 4));
+        o.scale_a = static_cast<const float*>(a.pointer(12, Kind::kF32, times(kb, m)));
+        o.scale_b = static_cast<const float*>(
+            a.pointer(13, Kind::kF32, times(kb, blocks == GEMM_EPI_SCALE_BLOCKS_ROWS ? cols : up(cols, 128))));
+        const cudaStream_t stream = a.stream(14);
+        return unlocked(a, p_execute_operands, static_cast<gemm_epi_plan_t>(plan),
+                        static_cast<const gemm_epi_operands*>(&o), stream);
+    });
+}
+
 // bind(rmsnorm, rmsnorm_e4m3, rmsnorm_backward, w4_matmul, w4_dequantize, dropout,
-// rmsnorm_workspace): addresses
+// rmsnorm_workspace, layernorm_forward, layernorm_e4m3, layernorm_backward, layernorm_workspace,
+// e4m3_quantize, execute_operands): addresses
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
-    return call(args, n, 7, true, [](Args& a) {
-        void* p[7];
-        for (int i = 0; i < 7; ++i) p[i] = a.pointer(i);
+    return call(args, n, 13, true, [](Args& a) {
+        void* p[13];
+        for (int i = 0; i < 13; ++i) p[i] = a.pointer(i);
         if (a.bad) return 0L;
         p_rmsnorm = reinterpret_cast<decltype(p_rmsnorm)>(p[0]);
         p_rmsnorm_e4m3 = reinterpret_cast<decltype(p_rmsnorm_e4m3)>(p[1]);
@@ -281,6 +379,12 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n)
         p_w4_dequantize = reinterpret_cast<decltype(p_w4_dequantize)>(p[4]);
         p_dropout = reinterpret_cast<decltype(p_dropout)>(p[5]);
         p_rmsnorm_workspace = reinterpret_cast<decltype(p_rmsnorm_workspace)>(p[6]);
+        p_layernorm_forward = reinterpret_cast<decltype(p_layernorm_forward)>(p[7]);
+        p_layernorm_e4m3 = reinterpret_cast<decltype(p_layernorm_e4m3)>(p[8]);
+        p_layernorm_backward = reinterpret_cast<decltype(p_layernorm_backward)>(p[9]);
+        p_layernorm_workspace = reinterpret_cast<decltype(p_layernorm_workspace)>(p[10]);
+        p_e4m3_quantize = reinterpret_cast<decltype(p_e4m3_quantize)>(p[11]);
+        p_execute_operands = reinterpret_cast<decltype(p_execute_operands)>(p[12]);
         return 0L;
     });
 }
@@ -298,6 +402,11 @@ PyMethodDef methods[] = {method("rmsnorm", rmsnorm),
                          method("w4_matmul", w4_matmul),
                          method("w4_dequantize", w4_dequantize),
                          method("dropout", dropout),
+                         method("layernorm_forward", layernorm_forward),
+                         method("layernorm_e4m3", layernorm_e4m3),
+                         method("layernorm_backward", layernorm_backward),
+                         method("e4m3_quantize", e4m3_quantize),
+                         method("block_product", block_product),
                          method("bind", bind),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods,

@@ -160,8 +160,8 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int b = min(kb + i, p.k_blocks - 1);
-                next_a[i] = __ldg(sa + static_cast<long long>(b) * p.m);
-                if (SQUARE) next_b[i] = __ldg(sb + static_cast<long long>(b) * sb_row);
+                next_a[i] = sa[static_cast<long long>(b) * p.m];
+                if (SQUARE) next_b[i] = sb[static_cast<long long>(b) * sb_row];
             }
         };
         auto copy_scales = [&](int kb) {  // (a scale for each row of B; columns past n stay as they are)

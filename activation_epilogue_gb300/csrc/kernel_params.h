@@ -314,6 +314,52 @@ int rmsnorm_backward_parts(long long t, long long d);
 cudaError_t rmsnorm_launch(const RmsnormArgs& a, bool bf16, cudaStream_t stream);
 cudaError_t rmsnorm_backward_launch(const RmsnormBackwardArgs& a, bool bf16, cudaStream_t stream);
 
+// LayerNorm for training (csrc/layernorm_train.cu); d a multiple of 8.  residual and H are both given or
+// both null (then the norm is of X); Y holds 16-bit values, or E4M3 codes with ceil(d / 128) rows of t
+// scales where scale is given.
+struct LayernormArgs {
+    const void* X;
+    const void* residual;
+    const void* gamma;
+    const void* beta;
+    void* H;
+    void* Y;
+    float* scale;
+    float* stats;  // t pairs (mean, rstd), or null
+    float eps;
+    int t, d;
+};
+struct LayernormBackwardArgs {
+    const void* dY;
+    const void* H;
+    const void* gamma;
+    const float* stats;
+    const void* dH;
+    void* dX;
+    float* dgamma;
+    float* dbeta;
+    float* ws_means;  // workspace: t pairs of means (rows too long for registers) ...
+    float* ws_sums;   // ... and layernorm_backward_parts(t, d) rows of 2 d partial sums (dgamma, dbeta)
+    int t, d;
+};
+int layernorm_backward_parts(long long t, long long d);
+cudaError_t layernorm_forward_launch(const LayernormArgs& a, bool bf16, cudaStream_t stream);
+cudaError_t layernorm_backward_launch(const LayernormBackwardArgs& a, bool bf16, cudaStream_t stream);
+
+// E4M3 codes with block scales (csrc/quantize.cu); cols a multiple of 16.  Q and Qt (either may be null):
+// rows x cols, and cols rows of (rows rounded up to 16).
+struct QuantizeArgs {
+    const void* X;
+    uint8_t* Q;
+    float* scale;    // ceil(cols / 128) rows of `rows` (square: of ceil(rows / 128))
+    uint8_t* Qt;
+    float* scale_t;  // ceil(rows / 128) rows of `cols` (square: of ceil(cols / 128))
+    long long rows;
+    int cols;
+    int square;      // 1: blocks of 128 x 128
+};
+cudaError_t quantize_launch(const QuantizeArgs& a, bool bf16, cudaStream_t stream);
+
 // Products with 4-bit weights (csrc/w4.cu): W n rows of k / 2 bytes, scales and zeros k / group
 // rows of n.  w4_dequantize_launch writes B (k x n) to D.
 struct W4Args {

@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cstdint>
+#include <initializer_list>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -23,6 +24,27 @@ constexpr unsigned long long kDefaultWaitNs = 2000ull * 1000 * 1000;  // 2 s
 struct HostPipe;
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+struct Buffer {
+    const void* p;
+    int64_t bytes;
+};
+
+inline bool meet(const Buffer& a, const Buffer& b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x && y && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+
+// An output overlaps none of `others`, and those that it may be (of its own extent) not in part.
+inline bool apart(const Buffer& out, std::initializer_list<Buffer> others, std::initializer_list<Buffer> may_be = {})
+{
+    for (const Buffer& b : others)
+        if (meet(out, b)) return false;
+    for (const Buffer& b : may_be)
+        if (b.p != out.p && meet(out, b)) return false;
+    return true;
+}
 
 }  // namespace gemm_epi_impl
 

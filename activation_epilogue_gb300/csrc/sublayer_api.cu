@@ -1,8 +1,7 @@
-// C ABI calls for what stands around a feed-forward block's GEMMs: the RMS norm, the products
-// with 4-bit weights and dropout.  Argument checks and launches; nothing is kept between calls.
+// C ABI calls for what stands around a feed-forward block's GEMMs: the RMS norm, LayerNorm for
+// training, E4M3 codes with block scales, the products with 4-bit weights and dropout.  Argument checks and launches; nothing is kept between calls.
 #include <atomic>
 #include <cmath>
-#include <initializer_list>
 
 #include "plan.h"
 
@@ -39,27 +38,6 @@ bool norm_shape_ok(int64_t t, int64_t d)
 {
     const int64_t kMax = (1ll << 31) - 1;
     return t >= 0 && d >= 8 && d % 8 == 0 && t <= kMax && d <= kMaxWidth && t * d <= (1ll << 40);
-}
-
-struct Buffer {
-    const void* p;
-    int64_t bytes;
-};
-
-bool meet(const Buffer& a, const Buffer& b)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return x && y && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
-}
-
-// An output overlaps none of `others`, and those that it may be (of its own extent) not in part.
-bool apart(const Buffer& out, std::initializer_list<Buffer> others, std::initializer_list<Buffer> may_be = {})
-{
-    for (const Buffer& b : others)
-        if (meet(out, b)) return false;
-    for (const Buffer& b : may_be)
-        if (b.p != out.p && meet(out, b)) return false;
-    return true;
 }
 
 int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
@@ -112,6 +90,45 @@ gemm_epi_status rmsnorm(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* 
     a.t = static_cast<int>(t);
     a.d = static_cast<int>(d);
     return launched(rmsnorm_launch(a, dtype == GEMM_EPI_BF16, stream));
+}
+
+// Y in 16 bits, or (scale given) in E4M3.
+gemm_epi_status layernorm(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* X, const void* residual,
+                          const void* gamma, const void* beta, float eps, void* H, void* Y, bool e4m3,
+                          float* scale, float* stats, cudaStream_t stream)
+{
+    if (!is_16bit(dtype)) return GEMM_EPI_ERR_INVALID_ARG;
+    if (!norm_shape_ok(t, d)) return GEMM_EPI_ERR_UNSUPPORTED_SHAPE;
+    if (!(eps >= 0.0f) || !(eps < 1e30f)) return GEMM_EPI_ERR_INVALID_ARG;
+    if (t == 0) return GEMM_EPI_OK;
+    if (!X || !gamma || !beta || !Y || (residual != nullptr) != (H != nullptr) || H == Y)
+        return GEMM_EPI_ERR_INVALID_ARG;
+    if (e4m3 && (!scale || Y == X || Y == residual)) return GEMM_EPI_ERR_INVALID_ARG;
+    if (!aligned(X, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(beta, 16) || !aligned(H, 16) ||
+        !aligned(Y, 16) || !aligned(scale, 4) || !aligned(stats, 8))
+        return GEMM_EPI_ERR_MISALIGNED;
+    const Buffer x = {X, 2 * t * d}, r = {residual, 2 * t * d}, g = {gamma, 2 * d}, b = {beta, 2 * d};
+    const Buffer h = {H, 2 * t * d}, y = {Y, (e4m3 ? 1 : 2) * t * d}, st = {stats, 8 * t};
+    const Buffer sc = {scale, 4 * t * ((d + 127) / 128)};
+    bool ok = apart(h, {g, b, y, st, sc}, {x, r}) && apart(st, {x, r, g, b, y, sc});
+    ok = ok && (e4m3 ? apart(y, {x, r, g, b, sc}) && apart(sc, {x, r, g, b}) : apart(y, {g, b}, {x, r}));
+    if (!ok) return GEMM_EPI_ERR_INVALID_ARG;
+    int sms = 0;
+    const gemm_epi_status s = device_sms(&sms);
+    if (s != GEMM_EPI_OK) return s;
+    LayernormArgs a = {};
+    a.X = X;
+    a.residual = residual;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.H = H;
+    a.Y = Y;
+    a.scale = scale;
+    a.stats = stats;
+    a.eps = eps;
+    a.t = static_cast<int>(t);
+    a.d = static_cast<int>(d);
+    return launched(layernorm_forward_launch(a, dtype == GEMM_EPI_BF16, stream));
 }
 
 gemm_epi_status w4_checked(int64_t n, int64_t k, int64_t group, gemm_epi_dtype dtype)
@@ -191,6 +208,110 @@ int64_t gemm_epi_rmsnorm_workspace(int64_t t, int64_t d)
     const int64_t forward = round16(sizeof(uint32_t) * kRmsMaxParts) + round16(sizeof(float) * t);
     const int64_t backward = round16(sizeof(float) * t) + round16(sizeof(float) * rmsnorm_backward_parts(t, d) * d);
     return forward > backward ? forward : backward;
+}
+
+gemm_epi_status gemm_epi_layernorm_forward(int64_t t, int64_t d, gemm_epi_dtype dtype,
+                                           const void* X, const void* residual, const void* gamma,
+                                           const void* beta, float eps, void* H, void* Y,
+                                           float* stats, cudaStream_t stream)
+{
+    return layernorm(t, d, dtype, X, residual, gamma, beta, eps, H, Y, false, nullptr, stats, stream);
+}
+
+gemm_epi_status gemm_epi_layernorm_e4m3(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* X,
+                                        const void* residual, const void* gamma, const void* beta,
+                                        float eps, void* H, void* Q, float* scale, float* stats,
+                                        cudaStream_t stream)
+{
+    return layernorm(t, d, dtype, X, residual, gamma, beta, eps, H, Q, true, scale, stats, stream);
+}
+
+gemm_epi_status gemm_epi_layernorm_backward(int64_t t, int64_t d, gemm_epi_dtype dtype,
+                                            const void* dY, const void* H, const void* gamma,
+                                            const float* stats, const void* dH, void* dX,
+                                            float* dgamma, float* dbeta, void* workspace,
+                                            cudaStream_t stream)
+{
+    if (!is_16bit(dtype)) return GEMM_EPI_ERR_INVALID_ARG;
+    if (!norm_shape_ok(t, d)) return GEMM_EPI_ERR_UNSUPPORTED_SHAPE;
+    if (!dgamma || !dbeta) return GEMM_EPI_ERR_INVALID_ARG;
+    if (!aligned(dgamma, 4) || !aligned(dbeta, 4)) return GEMM_EPI_ERR_MISALIGNED;
+    const Buffer dg = {dgamma, 4 * d}, db = {dbeta, 4 * d};
+    if (!apart(dg, {db})) return GEMM_EPI_ERR_INVALID_ARG;
+    if (t > 0) {
+        if (!dY || !H || !gamma || !stats || !dX || !workspace || dX == H) return GEMM_EPI_ERR_INVALID_ARG;
+        if (!aligned(dY, 16) || !aligned(H, 16) || !aligned(gamma, 16) || !aligned(stats, 8) || !aligned(dH, 16) ||
+            !aligned(dX, 16) || !aligned(workspace, 16))
+            return GEMM_EPI_ERR_MISALIGNED;
+        const Buffer y = {dY, 2 * t * d}, h = {H, 2 * t * d}, g = {gamma, 2 * d}, st = {stats, 8 * t}, z = {dH, 2 * t * d};
+        const Buffer dx = {dX, 2 * t * d}, ws = {workspace, gemm_epi_layernorm_workspace(t, d)};
+        if (!apart(dx, {h, g, st, dg, db, ws}, {y, z}) || !apart(dg, {y, h, g, st, z, ws}) ||
+            !apart(db, {y, h, g, st, z, ws}) || !apart(ws, {y, h, g, st, z}))
+            return GEMM_EPI_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    const gemm_epi_status s = device_sms(&sms);
+    if (s != GEMM_EPI_OK) return s;
+    if (t == 0) {
+        const size_t bytes = sizeof(float) * static_cast<size_t>(d);
+        const cudaError_t e = cudaMemsetAsync(dgamma, 0, bytes, stream);
+        return launched(e != cudaSuccess ? e : cudaMemsetAsync(dbeta, 0, bytes, stream));
+    }
+    LayernormBackwardArgs a = {};
+    a.dY = dY;
+    a.H = H;
+    a.gamma = gamma;
+    a.stats = stats;
+    a.dH = dH;
+    a.dX = dX;
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
+    a.ws_means = static_cast<float*>(workspace);
+    a.ws_sums = a.ws_means + round16(8 * t) / 4;
+    a.t = static_cast<int>(t);
+    a.d = static_cast<int>(d);
+    return launched(layernorm_backward_launch(a, dtype == GEMM_EPI_BF16, stream));
+}
+
+int64_t gemm_epi_layernorm_workspace(int64_t t, int64_t d)
+{
+    if (!norm_shape_ok(t, d)) return 0;
+    return round16(8 * t) + round16(8ll * layernorm_backward_parts(t, d) * d);
+}
+
+gemm_epi_status gemm_epi_e4m3_quantize(int64_t rows, int64_t cols, gemm_epi_dtype dtype,
+                                       gemm_epi_block block, const void* X, void* Q, float* scale,
+                                       void* Qt, float* scale_t, cudaStream_t stream)
+{
+    if (!is_16bit(dtype) || (block != GEMM_EPI_BLOCK_1X128 && block != GEMM_EPI_BLOCK_128X128))
+        return GEMM_EPI_ERR_INVALID_ARG;
+    if (rows < 0 || rows >= (1ll << 31) || cols < 16 || cols % 16 != 0 || cols > kMaxWidth || rows * cols > (1ll << 40))
+        return GEMM_EPI_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0) return GEMM_EPI_OK;
+    if (!X || (!Q && !Qt) || (Q != nullptr) != (scale != nullptr) || (Qt != nullptr) != (scale_t != nullptr))
+        return GEMM_EPI_ERR_INVALID_ARG;
+    if (!aligned(X, 16) || !aligned(Q, 16) || !aligned(Qt, 16) || !aligned(scale, 4) || !aligned(scale_t, 4))
+        return GEMM_EPI_ERR_MISALIGNED;
+    const bool square = block == GEMM_EPI_BLOCK_128X128;
+    const int64_t row_blocks = (rows + 127) / 128, column_blocks = (cols + 127) / 128;
+    const Buffer x = {X, 2 * rows * cols}, q = {Q, rows * cols}, qt = {Qt, cols * round16(rows)};
+    const Buffer s = {scale, 4 * column_blocks * (square ? row_blocks : rows)};
+    const Buffer st = {scale_t, 4 * row_blocks * (square ? column_blocks : cols)};
+    if (!apart(q, {x, s, qt, st}) || !apart(s, {x, qt, st}) || !apart(qt, {x, st}) || !apart(st, {x}))
+        return GEMM_EPI_ERR_INVALID_ARG;
+    int sms = 0;
+    const gemm_epi_status status = device_sms(&sms);
+    if (status != GEMM_EPI_OK) return status;
+    QuantizeArgs a = {};
+    a.X = X;
+    a.Q = static_cast<uint8_t*>(Q);
+    a.scale = scale;
+    a.Qt = static_cast<uint8_t*>(Qt);
+    a.scale_t = scale_t;
+    a.rows = rows;
+    a.cols = static_cast<int>(cols);
+    a.square = square ? 1 : 0;
+    return launched(quantize_launch(a, dtype == GEMM_EPI_BF16, stream));
 }
 
 gemm_epi_status gemm_epi_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group,

@@ -41,10 +41,13 @@ EXPORTS = ["gemm_epi_plan", "gemm_epi_plan_set_option", "gemm_epi_execute",
            "gemm_epi_layernorm_fold", "gemm_epi_ffn_plan_layernorm",
            "gemm_epi_ffn_execute_layernorm", "gemm_epi_execute_host", "gemm_epi_rmsnorm",
            "gemm_epi_rmsnorm_e4m3", "gemm_epi_rmsnorm_backward", "gemm_epi_rmsnorm_workspace",
-           "gemm_epi_w4_matmul", "gemm_epi_w4_dequantize", "gemm_epi_dropout"]
+           "gemm_epi_w4_matmul", "gemm_epi_w4_dequantize", "gemm_epi_dropout",
+           "gemm_epi_layernorm_forward", "gemm_epi_layernorm_e4m3", "gemm_epi_layernorm_backward",
+           "gemm_epi_layernorm_workspace", "gemm_epi_e4m3_quantize"]
 FFN_OPTION = {"LAUNCHES": 0, "SPLIT2": 1, "TILE_ORDER": 2, "B_READY": 3}
 
 SCALE_MODE = {"ROW": 0, "TENSOR": 1, "GIVEN": 2}
+BLOCK = {"1X128": 0, "128X128": 1}
 
 # Most rows of A in one gemm_epi_w4_matmul call.
 W4_MAX_ROWS = 64
@@ -156,6 +159,18 @@ def load_library(path: str | None = None):
         lib.gemm_epi_w4_dequantize.argtypes = [i64, i64, i64, i32, vp, vp, vp, vp, vp]
         lib.gemm_epi_dropout.restype = i32
         lib.gemm_epi_dropout.argtypes = [i64, i32, vp, vp, f32, u64, u64, vp, vp, vp]
+        lib.gemm_epi_layernorm_forward.restype = i32
+        lib.gemm_epi_layernorm_forward.argtypes = [i64, i64, i32, vp, vp, vp, vp, f32, vp, vp, vp, vp]
+        lib.gemm_epi_layernorm_e4m3.restype = i32
+        lib.gemm_epi_layernorm_e4m3.argtypes = [i64, i64, i32, vp, vp, vp, vp, f32, vp, vp, vp, vp,
+                                                vp]
+        lib.gemm_epi_layernorm_backward.restype = i32
+        lib.gemm_epi_layernorm_backward.argtypes = [i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                    vp, vp]
+        lib.gemm_epi_layernorm_workspace.restype = i64
+        lib.gemm_epi_layernorm_workspace.argtypes = [i64, i64]
+        lib.gemm_epi_e4m3_quantize.restype = i32
+        lib.gemm_epi_e4m3_quantize.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp, vp, vp]
         if path is None:
             _lib = lib
         return lib
@@ -424,6 +439,57 @@ class _CtypesCalls:
                                           _dev(Y, kind, count), _stream(stream))
 
 
+    def layernorm_forward(self, t, d, dtype, X, residual, gamma, beta, eps, H, Y, stats, stream):
+        k, td, row = _kind16(dtype), _times(t, d), d if t > 0 else 0
+        return self._lib.gemm_epi_layernorm_forward(t, d, dtype, _dev(X, k, td),
+                                                    _dev(residual, k, td), _dev(gamma, k, row),
+                                                    _dev(beta, k, row), eps, _dev(H, k, td),
+                                                    _dev(Y, k, td), _dev(stats, "f32", 2 * t),
+                                                    _stream(stream))
+
+    def layernorm_e4m3(self, t, d, dtype, X, residual, gamma, beta, eps, H, Q, scale, stats,
+                       stream):
+        k, td, row = _kind16(dtype), _times(t, d), d if t > 0 else 0
+        return self._lib.gemm_epi_layernorm_e4m3(t, d, dtype, _dev(X, k, td), _dev(residual, k, td),
+                                                 _dev(gamma, k, row), _dev(beta, k, row), eps,
+                                                 _dev(H, k, td), _dev(Q, "e4m3", td),
+                                                 _dev(scale, "f32", _times(t, -(-d // 128))),
+                                                 _dev(stats, "f32", 2 * t), _stream(stream))
+
+    def layernorm_backward(self, t, d, dtype, dY, H, gamma, stats, dH, dX, dgamma, dbeta, workspace,
+                           stream):
+        k, td = _kind16(dtype), _times(t, d)
+        ws = self._lib.gemm_epi_layernorm_workspace(t, d) if t > 0 else 0
+        return self._lib.gemm_epi_layernorm_backward(t, d, dtype, _dev(dY, k, td), _dev(H, k, td),
+                                                     _dev(gamma, k, d if t > 0 else 0),
+                                                     _dev(stats, "f32", 2 * t), _dev(dH, k, td),
+                                                     _dev(dX, k, td), _dev(dgamma, "f32", d),
+                                                     _dev(dbeta, "f32", d),
+                                                     _dev(workspace, "bytes", ws), _stream(stream))
+
+    def e4m3_quantize(self, rows, cols, dtype, block, X, Q, scale, Qt, scale_t, stream):
+        rb, cb = -(-rows // 128), -(-cols // 128)
+        square = block == BLOCK["128X128"]
+        return self._lib.gemm_epi_e4m3_quantize(rows, cols, dtype, block,
+                                                _dev(X, _kind16(dtype), _times(rows, cols)),
+                                                _dev(Q, "e4m3", _times(rows, cols)),
+                                                _dev(scale, "f32", _times(cb, rb if square else rows)),
+                                                _dev(Qt, "e4m3", _times(cols, -(-rows // 16) * 16)),
+                                                _dev(scale_t, "f32", _times(rb, cb if square else cols)),
+                                                _stream(stream))
+
+    def block_product(self, plan, m, n, k, blocks, bias_values, A, B, bias, residual, D, aux,
+                      scale_a, scale_b, stream):
+        any_, mn = int(m > 0 and n > 0), _times(m, n)
+        kb = any_ * -(-k // 128)
+        ops = Operands(_dev(A, "e4m3", any_ * _times(m, k)), _dev(B, "e4m3", any_ * _times(n, k)),
+                       _dev(bias, "bf16", any_ * bias_values), _dev(residual, "bf16", mn),
+                       _dev(D, "bf16", mn), _dev(aux, "bytes", any_ * m * -(-n // 32) * 4), None, None,
+                       None, None, None, _dev(scale_a, "f32", kb * m),
+                       _dev(scale_b, "f32", kb * (n if blocks == 2 else -(-n // 128))))
+        return self._lib.gemm_epi_execute_operands(plan, ctypes.byref(ops), _stream(stream))
+
+
 _calls = None
 
 
@@ -439,7 +505,9 @@ def _bind_calls():
         return _calls
     _fastcall.bind(*(ctypes.cast(getattr(lib, "gemm_epi_" + name), ctypes.c_void_p).value
                      for name in ("rmsnorm", "rmsnorm_e4m3", "rmsnorm_backward", "w4_matmul",
-                                  "w4_dequantize", "dropout", "rmsnorm_workspace")))
+                                  "w4_dequantize", "dropout", "rmsnorm_workspace",
+                                  "layernorm_forward", "layernorm_e4m3", "layernorm_backward",
+                                  "layernorm_workspace", "e4m3_quantize", "execute_operands")))
     _calls = _fastcall
     return _calls
 
@@ -478,6 +546,47 @@ def gemm_epi_rmsnorm_backward(t: int, d: int, dtype: str, dY, H, gamma, rstd, dH
 def gemm_epi_rmsnorm_workspace(t: int, d: int) -> int:
     """Bytes of workspace for the RMS norm calls of a t x d problem (0: a refused shape)."""
     return int(load_library().gemm_epi_rmsnorm_workspace(t, d))
+
+
+def gemm_epi_layernorm_forward(t: int, d: int, dtype: str, X, residual, gamma, beta, eps: float, H,
+                               Y, stats=None, stream=None):
+    """stats: t x 2 fp32, (mean, rstd) of each row of H."""
+    status = (_calls or _bind_calls()).layernorm_forward(t, d, DTYPE[dtype], X, residual, gamma, beta,
+                                                         eps, H, Y, stats, _handle(stream))
+    if status:
+        _check(status, "gemm_epi_layernorm_forward")
+
+
+def gemm_epi_layernorm_e4m3(t: int, d: int, dtype: str, X, residual, gamma, beta, eps: float, H, Q,
+                            scale, stats=None, stream=None):
+    """scale: ceil(d / 128) rows of t, the scale_a of a plan with SCALE_BLOCKS."""
+    status = (_calls or _bind_calls()).layernorm_e4m3(t, d, DTYPE[dtype], X, residual, gamma, beta, eps,
+                                                      H, Q, scale, stats, _handle(stream))
+    if status:
+        _check(status, "gemm_epi_layernorm_e4m3")
+
+
+def gemm_epi_layernorm_backward(t: int, d: int, dtype: str, dY, H, gamma, stats, dH, dX, dgamma,
+                                dbeta, workspace, stream=None):
+    status = (_calls or _bind_calls()).layernorm_backward(t, d, DTYPE[dtype], dY, H, gamma, stats, dH,
+                                                          dX, dgamma, dbeta, workspace,
+                                                          _handle(stream))
+    if status:
+        _check(status, "gemm_epi_layernorm_backward")
+
+
+def gemm_epi_layernorm_workspace(t: int, d: int) -> int:
+    """Bytes of workspace for the backward call of a t x d problem (0: a refused shape)."""
+    return int(load_library().gemm_epi_layernorm_workspace(t, d))
+
+
+def gemm_epi_e4m3_quantize(rows: int, cols: int, dtype: str, block: str, X, Q=None, scale=None,
+                           Qt=None, scale_t=None, stream=None):
+    """block: "1X128" or "128X128".  Qt has cols rows of `rows` rounded up to 16."""
+    status = (_calls or _bind_calls()).e4m3_quantize(rows, cols, DTYPE[dtype], BLOCK[block], X, Q, scale,
+                                                     Qt, scale_t, _handle(stream))
+    if status:
+        _check(status, "gemm_epi_e4m3_quantize")
 
 
 def gemm_epi_w4_matmul(m: int, n: int, k: int, group: int, dtype: str, epilog: str, A, W, scales,
@@ -670,6 +779,15 @@ class Plan:
 
     def execute(self, A, B, bias, D, aux=None, residual=None, stream=None, aux_in=None,
                 dbias=None, ln=None, scales=None):
+        if self._scales["SCALE_BLOCKS"] and aux_in is None and dbias is None and ln is None:
+            scale_a, scale_b = scales if scales is not None else (None, None)
+            status = (_calls or _bind_calls()).block_product(
+                self.handle, self.m, self.n, self.k, self._scales["SCALE_BLOCKS"],
+                self.n if self.bias_layout == "1N" else self.m, A, B, bias, residual, D, aux, scale_a,
+                scale_b, _handle(stream))
+            if status:
+                _check(status, "gemm_epi_execute_operands")
+            return
         gemm_epi_execute_operands(self.handle, A, B, D, bias=bias, residual=residual, aux=aux,
                                   aux_in=aux_in, dbias=dbias, stream=stream, ln=ln,
                                   scales=self._checked(scales))

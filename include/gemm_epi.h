@@ -426,6 +426,88 @@ gemm_epi_status gemm_epi_rmsnorm_backward(int64_t t, int64_t d, gemm_epi_dtype d
 /* Bytes of workspace that the RMS norm calls of this shape need (0 for a shape they refuse). */
 int64_t gemm_epi_rmsnorm_workspace(int64_t t, int64_t d);
 
+/* ---- LayerNorm for training and for block-scaled E4M3 products -----------------------------
+ * The LayerNorm above with the residual's addition in front of it (a pre-norm block: the sum is
+ * the residual stream, the norm the next sub-layer's input), its statistics, and its gradients:
+ *     H = X + residual, rounded to the 16-bit type (without a residual the norm is of X),
+ *     mu_i = mean_j H_ij,  rstd_i = 1 / sqrt(mean_j (H_ij - mu_i)^2 + eps),
+ *     Y_ij = (H_ij - mu_i) rstd_i gamma_j + beta_j.
+ * The norm is of the rounded H; sums and statistics are fp32, the variance is of the deviations from
+ * the mean (a row far from zero loses nothing to its mean's rounding), Y is rounded once.  A row whose
+ * sums leave fp32 (bf16 has fp32's exponents) is taken times a power of two, so that every finite row
+ * has its norm.  X, residual, H, Y: t x d; gamma, beta: d elements; all of `dtype` (F16 or BF16), d a
+ * multiple of 8, 8 to 2^30, 16-byte aligned.  H is given exactly when the residual is.  H and Y may each
+ * be X or the residual itself, but not the same buffer; any other overlap of an output is
+ * ERR_INVALID_ARG, here and in the calls below.  stats: t pairs (mu, rstd) in fp32, 8-byte aligned, or
+ * NULL (what the backward pass reads; the layout of gemm_epi_layernorm_stats).  eps >= 0.  A NaN or an
+ * infinity in a row of H makes that row of Y NaN.  t == 0 launches nothing.  Asynchronous on `stream`,
+ * launched as programmatic dependents of its previous work (which they wait for before they touch
+ * memory); the caller owns every buffer, the calls keep nothing, and calls on different streams are
+ * independent as long as their buffers are. */
+gemm_epi_status gemm_epi_layernorm_forward(int64_t t, int64_t d, gemm_epi_dtype dtype,
+                                           const void* X, const void* residual, const void* gamma,
+                                           const void* beta, float eps, void* H, void* Y,
+                                           float* stats, cudaStream_t stream);
+
+/* The same norm with Y in E4M3, a scale for each 128 columns of a row: the A and scale_a of a plan with
+ * GEMM_EPI_OPT_SCALE_BLOCKS.  scale: ceil(d / 128) rows of t fp32, 4-byte aligned, written:
+ * scale[b][i] = max |Y_ij| / 448 over columns j of block b; Q_ij = Y_ij * (1 / scale), Y (not rounded to
+ * 16 bits) and the reciprocal in fp32, rounded as by gemm_epi_e4m3_quantize.  Q: t x d bytes, 16-byte
+ * aligned, overlapping nothing else. */
+gemm_epi_status gemm_epi_layernorm_e4m3(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* X,
+                                        const void* residual, const void* gamma, const void* beta,
+                                        float eps, void* H, void* Q, float* scale, float* stats,
+                                        cudaStream_t stream);
+
+/* Gradients of Y (and of H, which the residual stream also carries on): from dY, the norm's input H (X
+ * where there was no residual), gamma and the forward call's stats,
+ *     g_ij = dY_ij gamma_j,   xh_ij = (H_ij - mu_i) rstd_i,
+ *     dX_ij = rstd_i (g_ij - mean_j g_ij - xh_ij mean_j(g_ij xh_ij)) + dH_ij,
+ *     dgamma_j = sum_i dY_ij xh_ij,   dbeta_j = sum_i dY_ij.
+ * dX is the gradient of X and of the residual alike.  dH, the gradient that reaches H past the norm, may
+ * be NULL (zero).  dY, H, dH, dX: t x d of `dtype`, dX may be dY or dH itself; dgamma, dbeta: d fp32,
+ * summed in an order that depends on (t, d) alone (the same inputs give the same bits); t == 0 writes
+ * zeros to them.  workspace: gemm_epi_layernorm_workspace(t, d) bytes of device memory, 16-byte aligned,
+ * that no other call uses until this one has run (t > 0). */
+gemm_epi_status gemm_epi_layernorm_backward(int64_t t, int64_t d, gemm_epi_dtype dtype,
+                                            const void* dY, const void* H, const void* gamma,
+                                            const float* stats, const void* dH, void* dX,
+                                            float* dgamma, float* dbeta, void* workspace,
+                                            cudaStream_t stream);
+
+/* Bytes of workspace that the backward call of this shape needs (0 for a shape it refuses). */
+int64_t gemm_epi_layernorm_workspace(int64_t t, int64_t d);
+
+/* ---- E4M3 with block scales ---------------------------------------------------------------
+ * Quantise a 16-bit matrix for plans with GEMM_EPI_OPT_SCALE_BLOCKS:
+ *     scale = max |x| / 448 over each block of X,   code = x * (1 / scale),
+ * the reciprocal and the product in fp32, the product rounded to the nearest E4M3 value, ties to even,
+ * saturated at +-448 (next to a halfway point the quotient itself may round to the neighbouring code).
+ * X: rows x cols of `dtype` (F16 or BF16), cols a multiple of 16, 16 to 2^30.
+ *   Q, scale      (or both NULL) the codes row-major, rows x cols; scale: ceil(cols / 128) rows of
+ *                 `rows` fp32 (BLOCK_1X128: scale[b][i] of columns 128 b ... of row i) or of
+ *                 ceil(rows / 128) (BLOCK_128X128);
+ *   Qt, scale_t   (or both NULL) the codes of the transposed X: cols rows of ldt bytes, ldt = rows
+ *                 rounded up to 16, the rest of each row zeros; scale_t: ceil(rows / 128) rows of `cols`
+ *                 fp32 (BLOCK_1X128: blocks of 128 rows of a column of X) or of ceil(cols / 128)
+ *                 (BLOCK_128X128: the same blocks and codes as Q).
+ * So X is an A of m = rows, k = cols, or a transposed B of n = rows, k = cols, by Q; and by Qt an A of
+ * m = cols (a B of n = cols), k = ldt.  For D = X W (W: d x f of 16 bits): A from X's rows, B from W's Qt
+ * in 128 x 128 blocks; for dX = dD W^T: A from dD's rows, B from W's Q; for dW = X^T dD: A from X's Qt and
+ * B from dD's Qt in 1 x 128 blocks (SCALE_BLOCKS_ROWS).  A block without a value of 2^-100 or more gets
+ * scale 0 and zeros; a NaN gives its block a NaN scale and NaN codes, an infinity an infinite scale, zeros
+ * and NaN for the infinite values.  X, Q, Qt 16-byte aligned, scale and scale_t 4-byte; no output overlaps
+ * another buffer.  rows == 0 launches nothing.  One pass over X, whatever is written; asynchronous on
+ * `stream` as above. */
+typedef enum {
+    GEMM_EPI_BLOCK_1X128 = 0,
+    GEMM_EPI_BLOCK_128X128 = 1
+} gemm_epi_block;
+
+gemm_epi_status gemm_epi_e4m3_quantize(int64_t rows, int64_t cols, gemm_epi_dtype dtype,
+                                       gemm_epi_block block, const void* X, void* Q, float* scale,
+                                       void* Qt, float* scale_t, cudaStream_t stream);
+
 /* ---- products with 4-bit weights --------------------------------------------------------
  *     D[m,n] = epi(A[m,k] . B[k,n] + bias),   B[i][j] = (q[j][i] - z) * s,
  * with the weight held in 4 bits: W is n rows of k/2 bytes (column j of B is row j of W,

@@ -77,3 +77,83 @@ def check(got, want, error, dtype="bf16", what=""):
     assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, worst "
                            f"{float(((got - want).abs() / bound)[bad].nan_to_num(1e30).max()):.3g} of the bound, "
                            f"first at {bad.nonzero()[0].tolist()}")
+
+
+# ---- quantisation ----------------------------------------------------------------------------
+
+def tops(x: torch.Tensor, block: str) -> torch.Tensor:
+    """The largest |x| of every block: [block of columns][row, or block of rows]."""
+    rows, cols = x.shape
+    high = 128 if block == "128X128" else 1
+    x = torch.nn.functional.pad(x.double(), (0, up(cols, 128) - cols, 0, up(rows, high) - rows))
+    return x.reshape(-1, high, up(cols, 128) // 128, 128).abs().amax((1, 3)).t()
+
+
+def check_codes(codes: torch.Tensor, value: torch.Tensor, error: torch.Tensor, what: str):
+    """codes are E4M3 roundings of quotients within `error` (absolute) of `value`: half a step is 2^-4 of
+    the value, 2^-10 in the subnormal range."""
+    v = value.clamp(-E4M3_MAX, E4M3_MAX)
+    bound = (2.0 ** -4 * (v.abs() + error)).clamp(min=2.0 ** -10) + error
+    bad = ~((codes.float().double() - v).abs() <= bound)
+    assert not bad.any(), f"{what}: {int(bad.sum())} codes off, first at {bad.nonzero()[0].tolist()}"
+
+
+def check_quantized(x, block, codes, scale, what=""):
+    """The codes and scales of a finite x: a scale is one fp32 division of a 16-bit value (2^-24), the
+    reciprocal and the product add a rounding each."""
+    top = tops(x, block)
+    want = torch.where(top < NOTHING, 0.0, top / E4M3_MAX)
+    assert torch.all((scale.double() - want).abs() <= F32 * want), what + " scale"
+    rows, cols = x.shape
+    s = spread(scale, block, rows, cols)
+    q = torch.where(s > 0, x.double() / s, 0.0)
+    check_codes(codes, q, 3 * F32 * q.abs(), what)
+
+
+# ---- LayerNorm -------------------------------------------------------------------------------
+
+def sum_error(n: int) -> float:
+    """Relative error of an fp32 sum of n terms of one sign: no summation tree that splits n over at
+    least a warp has a longer chain than n / 32 + 32 roundings."""
+    return (n / 32 + 32) * F32
+
+
+def layernorm(h, gamma, beta, eps):
+    """(y, mean, rstd, a bound of the error of y before its rounding) in 64 bits of the rows of h.
+
+    The kernels take the deviations u from a first mean m0, which is off by at most S mean|h| (S:
+    sum_error), and what their mean says m0 lacks, itself off by S of the mean of |u|.  So u - more is
+    three roundings of u and S mean|u| off, the variance S of itself, rstd half of that and four
+    roundings."""
+    h, gamma, beta = h.double(), gamma.double(), beta.double()
+    mean = h.mean(1, keepdim=True)
+    dev = h - mean
+    rstd = 1.0 / torch.sqrt((dev * dev).mean(1, keepdim=True) + eps)
+    xh = dev * rstd
+    y = xh * gamma + beta
+    S = sum_error(h.shape[1])
+    lacks = S * h.abs().mean(1, keepdim=True)  # how far m0 may be off
+    spread_ = dev.abs().mean(1, keepdim=True) + lacks
+    e_dev = 4 * F32 * (dev.abs() + lacks) + S * spread_
+    e_var = 2 * S * ((dev * dev).mean(1, keepdim=True) + lacks * lacks)
+    rel = e_var * rstd * rstd + 8 * F32
+    error = gamma.abs() * (rstd * e_dev + xh.abs() * rel) + 3 * F32 * (y.abs() + beta.abs())
+    return y, mean[:, 0], rstd[:, 0], error
+
+
+def layernorm_backward(dy, h, gamma, stats, dh):
+    """(dx, dgamma, dbeta, bounds of their errors) in 64 bits, for the stats that are given."""
+    dy, h, gamma = dy.double(), h.double(), gamma.double()
+    mean, r = stats.double()[:, :1], stats.double()[:, 1:]
+    g, xh = dy * gamma, (h - mean) * r
+    m1, m2 = g.mean(1, keepdim=True), (g * xh).mean(1, keepdim=True)
+    dx = r * (g - m1 - xh * m2)
+    t, d = h.shape
+    S = sum_error(d) + 6 * F32
+    error = r * (6 * F32 * (g.abs() + m1.abs() + (xh * m2).abs()) +
+                 S * (g.abs().mean(1, keepdim=True) + xh.abs() * (g * xh).abs().mean(1, keepdim=True)))
+    if dh is not None:
+        dx = dx + dh.double()
+        error = error + F32 * dx.abs()
+    chain = (t + 64) * F32  # no order of summation has a longer chain of roundings
+    return (dx, (dy * xh).sum(0), dy.sum(0), error, chain * (dy * xh).abs().sum(0), chain * dy.abs().sum(0))
