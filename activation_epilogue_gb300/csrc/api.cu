@@ -330,8 +330,8 @@ gemm_epi_status configure_blocks(gemm_epi_plan_s* p)
         p->bn = 256;
         p->tiles_m = static_cast<int>((p->m + 255) / 256);
         p->tiles_n = static_cast<int>((p->n + 255) / 256);
-        p->stages = rowpair_stages(256);
-        p->smem = rowpair_smem_bytes(256);
+        p->stages = block_pair_stages();
+        p->smem = block_pair_smem();
         const long long tiles = static_cast<long long>(p->tiles_m) * p->tiles_n;
         if (tiles > (1ll << 30)) return GEMM_EPI_ERR_UNSUPPORTED_SHAPE;
         if (pairs > tiles) pairs = tiles;
@@ -663,11 +663,12 @@ gemm_epi_status ensure_maps(gemm_epi_plan_s* p, const void* A, const void* B, vo
     if (p->dtype == GEMM_EPI_E4M3) {
         // A [m][k] and B transposed [n][k], bytes, K-major boxes {128 k, 128 rows} (A) and
         // {128 k, bn / 2 rows} (B: each CTA's half of a tile's columns); D bf16
-        // (few rows of A: boxes of bn rows of A, 128 of B, and D is stored without a map)
+        // (block scales: boxes of 64 rows of B for CTA pairs; for few rows of A boxes of bn rows of A and
+        // 128 of B, and D is stored without a map)
         const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
         const bool swapped = p->variant == kBlockSwapped;
         const uint32_t a_rows = swapped ? static_cast<uint32_t>(p->bn) : 128u;
-        const uint32_t b_rows = swapped ? 128u : static_cast<uint32_t>(p->bn / 2);
+        const uint32_t b_rows = swapped ? 128u : static_cast<uint32_t>(p->scale_blocks ? 64 : p->bn / 2);
         if (!encode_2d(&p->tm_A, A, u8, p->k, p->m, 128, a_rows, CU_TENSOR_MAP_SWIZZLE_128B, 1) ||
             !encode_2d(&p->tm_B, B, u8, p->k, p->n, 128, b_rows, CU_TENSOR_MAP_SWIZZLE_128B, 1) ||
             !encode_2d(&p->tm_D, D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p->n, p->m, 32, 32,

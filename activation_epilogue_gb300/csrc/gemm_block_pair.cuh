@@ -6,15 +6,20 @@
 // the transposed B (SQUARE, n / 128 of them for each block) or per row of it (n of them).
 //
 // The tensor cores cannot apply such scales to a sum that they keep, so the sum of each block of
-// 128 k is a sum of its own: the MMA thread starts every K block with a cleared accumulator and
-// hands it over, alternating between the two that tensor memory holds, and the epilogue warps read
-// it, multiply it by its scales and add it to the tile's sums in fp32 registers: 128 a thread (two
-// warps a lane quarter, 128 columns each, so that with SQUARE a warp's columns share one scale and
-// a thread has one factor a block).  A block's MMAs take 512 cycles (256 x 256 x 128 on the pair);
-// reading 128 x 256 fp32 from tensor memory takes 256 of them and the additions, two columns an
-// instruction, 128 issue slots a scheduler (256 where every column has its scale), so the
-// promotion hides behind the next block's MMAs.  The copies, the tile order and the stores are
-// those of the CTA-pair kernel for one scale.
+// 128 k is a sum of its own: the MMA warp starts every K block with cleared accumulators and hands
+// them over, and the summing warps read them, multiply them by their scales and add them to the
+// tile's sums in fp32 registers.  What bounds it is this hand-over and the additions, not the MMAs
+// (256 x 256 x 128 take 590 cycles on the pair):
+//   * Four accumulators of 128 columns, half a tile each: a half's MMAs run while the three before
+//     it are read, so that no MMA waits for a round trip through barriers.
+//   * Eight summing warps (a lane quarter, half the tile's columns each), 128 sums a thread; sixteen values
+//     are on their way from tensor memory while the sixteen before them are added, in plain fp32 (the
+//     two-column instructions are slower).  Sixteen warps of 64 sums leave too few registers for the
+//     addresses, which are then formed again in every block (1099 us for 16384 x 8192 x 8192, 835 so).
+//   * SQUARE: a warp's columns share one scale, a thread (a row) has one factor a block.  Otherwise
+//     every column has its own, and a thread's values are loaded as four rows of 32 columns, so that 32
+//     scales a block come from shared memory for them and not 128 (whose 1024 cycles a block would bound it).
+//   * One warp brings the scales of all blocks into a ring in shared memory, ahead of the sums.
 #pragma once
 
 #include "gemm_kernel.cuh"
@@ -24,47 +29,173 @@ namespace gemm_epi {
 namespace block_pair {
 
 using C = TileCfg<256, true>;
-constexpr int kCols = 128;                    // columns of D per epilogue warp
-// Four warps of copies and MMAs (two of them idle), then the eight that sum: the registers are
+constexpr int kCols = 128;                    // columns of D per accumulator
+constexpr int kHalfBytes = 64 * 128;          // a CTA's rows of B for half a tile's columns, in a stage
+constexpr int kStages = 6;
+constexpr int kStageBytes = C::kStageBytes;
+// Four warps of copies, MMAs and scales (and an idle one), then those that sum: the registers are
 // given out by warpgroup, and the sums need more than an even share of the block's 384 x 168.
-constexpr int kBlockThreads = 384;
-constexpr int kIssueRegs = 56, kSumRegs = 224;
-static_assert(128 * kIssueRegs + 256 * kSumRegs <= 384 * 168, "a split of the registers that the block starts with");
-constexpr int kScaleDepth = 3;                // a scale for each row of B: blocks of scales in flight
-static_assert(kCols * (1 + kScaleDepth) * 4 <= 2048, "a warp's staging area");
+constexpr int kSumWarps = 8;
+constexpr int kBlockThreads = 128 + 32 * kSumWarps;
+constexpr int kIssueRegs = 72, kSumRegs = 216;
+static_assert(128 * kIssueRegs + 32 * kSumWarps * kSumRegs <= kBlockThreads * 168,
+              "a split of the registers that the block starts with");
+// Blocks of scales on their way: 128 rows of A and, SQUARE, the factors of the tile's two halves (a row's scale times the
+// block's of B), otherwise the rows' scales and those of 256 columns.
+constexpr int kGroup = 4;                     // K blocks of scales that are handed over together
+constexpr int kScaleGroups = 2;
+constexpr int kScaleFloats = 3 * 128;
+// Shared memory: the stages, a 2 KB box and the bias of its columns for each summing warp, the scales.
+constexpr int kOffBox = kStages * kStageBytes;
+constexpr int kOffBias = kOffBox + kSumWarps * 2048;
+constexpr int kOffScale = kOffBias + kSumWarps * kCols * 4;
+constexpr int kOffBar = kOffScale + kScaleGroups * kGroup * kScaleFloats * 4;
+constexpr int kSmemBytes = 1024 + kOffBar + C::kBarBytes;  // (1024: alignment)
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+constexpr int kBarAccFull = kBarTmemFull;     // [4], in place of the one-scale kernel's four
+constexpr int kBarAccEmpty = 44;              // [4], behind the tile indices
+constexpr int kBarScaleFull = 48;             // [2]
+constexpr int kBarScaleEmpty = kBarScaleFull + kScaleGroups;
+static_assert(kBarAccFull + 4 == kBarStall && kOffSchedSlot + 4 * kSchedSlots <= kBarAccEmpty * 8 && (kBarScaleEmpty + kScaleGroups) * 8 <= C::kBarBytes,
+              "barrier area");
 
-// (x, y) += (a, b) * s
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float s)
+// Start loading values of this warp's accumulator lanes, valid after tmem_wait on them: 16 columns of each thread's
+// lane ...
+__device__ __forceinline__ void load_lane16(uint32_t taddr, uint32_t (&r)[16])
 {
-    unsigned long long acc, v, ss;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(x), "f"(y));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(ss));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(acc));
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
-// (a, b) * (u, v)
-__device__ __forceinline__ float2 mul2(float a, float b, float u, float v)
+// ... or, of 16 lanes and 32 columns, thread t's pairs of columns 8 i + 2 (t % 4), + 1 in lanes t / 4 (r[4 i],
+// r[4 i + 1]) and t / 4 + 8 (r[4 i + 2], r[4 i + 3]).
+__device__ __forceinline__ void load_square16(uint32_t taddr, uint32_t (&r)[16])
 {
-    unsigned long long x, y;
-    float2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(u), "f"(v));
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
+// Wait for this thread's loads; r (their destination) is marked as written here, so that nothing reads it earlier.
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+// A whole warp's wait (it gives up as one: what follows is for all of its lanes): one try in line, the loop out of
+// the way (a loop of tries in its place took 1040 us for 16384 x 8192 x 8192 instead of 885).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag,
+                                          unsigned long long limit_ns)
+{
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, limit_ns));
+}
+
+// One thread of each CTA: the K blocks of every tile into the ring of stages, the even CTA's barriers
+// counting both CTAs' bytes.  A CTA's 128 rows of B are 64 of each half of the tile's columns, so that the
+// pair's MMA of a half (64 rows from either CTA) makes 128 columns next to each other.  The even CTA also
+// tells the tiles to everyone else, a tile ahead (see the one-scale kernel's producer).
+__device__ __forceinline__ void copy_operands(const GemmParams& p, uint32_t sbase, uint32_t bar0, volatile int* abort_flag)
+{
+    const WorkRange w = work_range<true>(p);
+    const uint32_t rank = static_cast<uint32_t>(w.pair_rank);
+    const bool even = rank == 0, dyn = even && p.sched != nullptr;
+    const uint32_t full0 = map_shared_rank(bar0 + 8u * kBarFull, cluster_ctarank() & ~1u);
+    int stage = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool ok = true;
+    int tile = w.first, next = w.end;
+    grid_dependency_wait();
+    for (int j = 0; ok; ++j) {
+        if (j > 0) {
+            if (even)
+                tile = next;
+            else if (!sched_take(bar0, j, tile, abort_flag, p.wait_limit_ns))
+                ok = false;
+        }
+        if (!ok || tile >= w.end) break;
+        const unsigned ticket = dyn ? atomicAdd(p.sched, 1u) : 0u;  // (needed a few K blocks later)
+        const int publish_at = min(2, p.k_blocks - 1);
+        int tm, tn;
+        tile_coords(tile, p, tm, tn);
+        const int arow = tm * 2 * kBM + static_cast<int>(rank) * kBM, brow = tn * 256 + static_cast<int>(rank) * 64;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+            ok = wait_bounded(bar0 + 8u * (kBarEmpty + stage), phase ^ 1u, abort_flag, p.wait_limit_ns);
+            if (!ok) break;
+            const uint32_t sa = sbase + stage * kStageBytes, full = full0 + 8u * stage;
+            if (even) mbar_arrive_expect_tx(bar0 + 8u * (kBarFull + stage), 2 * kStageBytes);
+            tma_load_2d_pair(sa, &p.tm_A, full, kb * 128, arow);
+            tma_load_2d_pair(sa + C::kABytes, &p.tm_B, full, kb * 128, brow);
+            tma_load_2d_pair(sa + C::kABytes + kHalfBytes, &p.tm_B, full, kb * 128, brow + 128);
+            ++issued;
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            if (even && kb == publish_at) {
+                const long long at = dyn ? static_cast<long long>(w.stride) + ticket : static_cast<long long>(tile) + w.stride;
+                next = at < w.end ? static_cast<int>(at) : w.end;
+                ok = sched_publish(bar0, j + 1, next, abort_flag, p.wait_limit_ns);
+                if (!ok) break;
+            }
+        }
+    }
+    if (ok) return;
+    if (!*abort_flag) record_failure(p.status, abort_flag, kRoleProducer);
+    if (!even) return;
+    // the copies on their way land before the CTA can leave (the even CTA's barriers count both CTAs' copies)
+    for (long long f = issued > kStages ? issued - kStages : 0; f < issued; ++f)
+        wait_bounded(bar0 + 8u * (kBarFull + static_cast<int>(f % kStages)), static_cast<uint32_t>(f / kStages & 1),
+                     abort_flag, kDrainLimitNs, false);
+}
+
+// Arrive on an mbarrier of the even CTA (a shared::cluster address).  What it orders are this warp's reads
+// of tensor memory, which the tcgen05 fences around the barrier order; a release at cluster scope would
+// wait for the warp's loads and stores of memory as well, a microsecond in every K block (16384 x 8192 x
+// 8192: 1980 us with it, 1012 so).
+__device__ __forceinline__ void arrive_pair(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The whole warp runs the loop, so that what the instructions take is uniform over it (in one thread's
+// branch each operand is moved to uniform registers first); one elected lane issues.
 __device__ __forceinline__ void issue_blocks(const GemmParams& p, uint32_t sbase, uint32_t bar0, uint32_t tmem_base,
                                         volatile int* abort_flag)
 {
-    constexpr uint32_t idesc = make_idesc_e4m3(2 * kBM, 256);
+    constexpr uint32_t idesc = make_idesc_e4m3(2 * kBM, kCols);
     const WorkRange w = work_range<true>(p);
     if (w.pair_rank != 0) return;
     const uint32_t self = cluster_ctarank();
     const uint16_t mask_self = static_cast<uint16_t>(1u << self);
     const uint16_t mask_pair = static_cast<uint16_t>(3u << self);
+    const bool elected = elect_one();
+    const uint64_t desc0 = make_sdesc_sw128(sbase, 0, 1024);
     int stage = 0;
     uint32_t phase = 0;
     uint32_t block = 0;  // K blocks so far, over all tiles
@@ -72,32 +203,37 @@ __device__ __forceinline__ void issue_blocks(const GemmParams& p, uint32_t sbase
     bool ok = true;
     int tile = w.first;
     for (int j = 0; ok; ++j) {
-        if (j > 0 && !sched_take(bar0, j, tile, abort_flag, p.wait_limit_ns)) {
+        if (j > 0 && !sched_take_warp(bar0, j, tile, abort_flag, p.wait_limit_ns)) {
             if (!*abort_flag) record_failure(p.status, abort_flag, kRoleMma);
             ok = false;
             break;
         }
         if (tile >= w.end) break;
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++block) {
-            const uint32_t acc = block & 1u;
-            if (!wait_bounded<true>(bar0 + 8u * (kBarTmemEmpty + acc), ((block >> 1) & 1u) ^ 1u, abort_flag,
-                                    p.wait_limit_ns) ||
-                !wait_bounded(bar0 + 8u * (kBarFull + stage), phase, abort_flag, p.wait_limit_ns)) {
-                if (!*abort_flag) record_failure(p.status, abort_flag, kRoleMma);
-                ok = false;
-                break;
-            }
-            tcgen05_fence_after_sync();
-            const uint32_t sa = sbase + stage * C::kStageBytes;
-            const uint32_t sb = sa + C::kABytes;
+        for (int kb = 0; kb < p.k_blocks && ok; ++kb, ++block) {
+            const uint64_t desc = desc0 + static_cast<uint32_t>(stage * (kStageBytes >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_f8_ss_pair(tmem_base + acc * 256u, make_sdesc_sw128(sa + kk * 32, 0, 1024),
-                               make_sdesc_sw128(sb + kk * 32, 0, 1024), idesc, kk > 0 ? 1u : 0u);
-            issued_any = true;
-            mma_commit_pair(bar0 + 8u * (kBarEmpty + stage), mask_pair);
-            mma_commit_pair(bar0 + 8u * (kBarTmemFull + acc), mask_pair);
-            if (++stage == C::kStages) {
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t acc = 2 * (block & 1u) + h;
+                if (h == 0) ok = warp_wait(bar0 + 8u * (kBarFull + stage), phase, abort_flag, p.wait_limit_ns);
+                ok = ok && warp_wait(bar0 + 8u * (kBarAccEmpty + acc), ((block >> 1) & 1u) ^ 1u, abort_flag, p.wait_limit_ns);
+                if (!ok) {
+                    if (!*abort_flag) record_failure(p.status, abort_flag, kRoleMma);
+                    break;
+                }
+                tcgen05_fence_after_sync();
+                if (elected) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8_ss_pair(tmem_base + acc * kCols, desc + kk * 2,
+                                       desc + ((C::kABytes + h * kHalfBytes) >> 4) + kk * 2, idesc, kk > 0 ? 1u : 0u);
+                    mma_commit_pair(bar0 + 8u * (kBarAccFull + acc), mask_pair);
+                    if (h == 1) mma_commit_pair(bar0 + 8u * (kBarEmpty + stage), mask_pair);
+                }
+                __syncwarp();
+                issued_any = true;
+            }
+            if (!ok) break;
+            if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -105,32 +241,224 @@ __device__ __forceinline__ void issue_blocks(const GemmParams& p, uint32_t sbase
     }
     if (!ok && issued_any) {
         // every MMA issued completes before tensor memory is released
-        mma_commit_pair(bar0 + 8u * kBarDrain, mask_self);
+        if (elected) mma_commit_pair(bar0 + 8u * kBarDrain, mask_self);
+        __syncwarp();
         wait_bounded(bar0 + 8u * kBarDrain, 0, abort_flag, kDrainLimitNs, false);
+    }
+}
+
+// One warp: the scales of every K block of every tile into the ring.
+template <bool SQUARE>
+__device__ __forceinline__ void stage_scales(const GemmParams& p, uint8_t* smem, uint32_t bar0, volatile int* abort_flag)
+{
+    const int lane = threadIdx.x & 31;
+    const WorkRange w = work_range<true>(p);
+    const long long sb_row = SQUARE ? (p.n + 127) / 128 : p.n;
+    constexpr int kB = SQUARE ? 2 : 8;        // scales of B of a lane and block
+    constexpr int kAtOnce = SQUARE ? 4 : 2;   // blocks whose loads are on their way together
+    float* ring = reinterpret_cast<float*>(smem + kOffScale);
+    grid_dependency_wait();
+    uint32_t group = 0;
+    int tile = w.first;
+    for (int j = 0;; ++j) {
+        if (j > 0 && !sched_take_warp(bar0, j, tile, abort_flag, p.wait_limit_ns)) {
+            if (!*abort_flag) record_failure(p.status, abort_flag, kRoleProducer);
+            return;
+        }
+        if (tile >= w.end) return;
+        int tm, tn;
+        tile_coords(tile, p, tm, tn);
+        const int row0 = tm * 2 * kBM + w.pair_rank * kBM;
+        int ia[4], ib[kB];  // (those past the matrix are the last ones again: their sums are not stored)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ia[i] = min(row0 + lane + 32 * i, p.m - 1);
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+            ib[i] = SQUARE ? min(tn * 2 + i, static_cast<int>(sb_row) - 1) : min(tn * 256 + lane + 32 * i, p.n - 1);
+        for (int kb0 = 0; kb0 < p.k_blocks; kb0 += kGroup, ++group) {
+            const uint32_t slot = group % kScaleGroups;
+#pragma unroll
+            for (int q0 = 0; q0 < kGroup; q0 += kAtOnce) {
+                float a[kAtOnce][4], b[kAtOnce][kB];
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) {
+                    const long long kb = min(kb0 + q0 + q, p.k_blocks - 1);
+                    const float* sa = p.scale_a + kb * p.m;
+                    const float* sb = p.scale_b + kb * sb_row;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[q][i] = sa[ia[i]];
+#pragma unroll
+                    for (int i = 0; i < kB; ++i) b[q][i] = sb[ib[i]];
+                }
+                if (q0 == 0 && !warp_wait(bar0 + 8u * (kBarScaleEmpty + slot), (group / kScaleGroups & 1u) ^ 1u, abort_flag,
+                                               p.wait_limit_ns)) {
+                    if (!*abort_flag) record_failure(p.status, abort_flag, kRoleProducer);
+                    return;
+                }
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) {
+                    float* to = ring + (slot * kGroup + q0 + q) * kScaleFloats + lane;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        to[32 * i] = SQUARE ? a[q][i] * b[q][0] : a[q][i];
+                        if (SQUARE) to[128 + 32 * i] = a[q][i] * b[q][1];
+                    }
+                    if constexpr (!SQUARE) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) to[128 + 32 * i] = b[q][i];
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar0 + 8u * (kBarScaleFull + slot));
+        }
+    }
+}
+
+// The place of a thread's sums: with SQUARE sum[e] is column e of its lane's row; otherwise sum
+// 32 b + 16 a + 4 i + 2 u + v is row lane / 4 + 16 a + 8 u, column 32 b + 8 i + 2 (lane % 4) + v.
+
+// The epilogue of 32 of the warp's columns, `at` on, and their store through the warp's box.
+template <bool SQUARE, int EPI>
+__device__ __forceinline__ void store_chunk(const GemmParams& p, const float* sum, const float* bias, int row0, int at,
+                                            uint8_t* box, uint32_t box_u32)
+{
+    const int lane = threadIdx.x & 31;
+    constexpr bool kBias = EPI != EPI_NONE;
+    const bool along_cols = p.bias_layout == 1;
+    // (a thread's rows: one, or four)
+    auto row_of = [&](int q) { return SQUARE ? row0 + lane : row0 + lane / 4 + 8 * q; };
+    if (lane == 0) bulk_wait_group_read<0>();  // this warp's last box is read
+    __syncwarp();
+    if constexpr (SQUARE) {
+        const int row = row_of(0);
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = sum[e];
+        if constexpr (kBias) add_bias<32>(v, bias, along_cols, !along_cols && row < p.m ? load_16bit(p.bias, row, 1) : 0.0f);
+        if constexpr (EPI == EPI_RELU_AUX_BIAS) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) word |= (v[e] > 0.0f && at + e < p.n) ? (1u << e) : 0u;
+            if (row < p.m) static_cast<uint32_t*>(p.aux)[static_cast<long long>(row) * p.aux_ld + at / 32] = word;
+        }
+        activate(v, EPI);
+        const uint16_t* R = static_cast<const uint16_t*>(p.residual) + static_cast<long long>(row) * p.n + at;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (EPI == EPI_BIAS_RESIDUAL && row < p.m && at + 8 * q < p.n) {  // (n is a multiple of 8)
+                const uint4 w = *reinterpret_cast<const uint4*>(R + 8 * q);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    v[8 * q + 2 * h] += __uint_as_float(ww[h] << 16);
+                    v[8 * q + 2 * h + 1] += __uint_as_float(ww[h] & 0xFFFF0000u);
+                }
+            }
+            *reinterpret_cast<uint4*>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pack2(v[8 * q], v[8 * q + 1], 1), pack2(v[8 * q + 2], v[8 * q + 3], 1),
+                           pack2(v[8 * q + 4], v[8 * q + 5], 1), pack2(v[8 * q + 6], v[8 * q + 7], 1));
+        }
+    } else {
+        const int c2 = 2 * (lane & 3);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // rows lane / 4 + 8 q
+            const int row = row_of(q);
+            const float lb = kBias && !along_cols && row < p.m ? load_16bit(p.bias, row, 1) : 0.0f;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 b = kBias && along_cols ? *reinterpret_cast<const float2*>(bias + 8 * i + c2) : make_float2(lb, lb);
+                v[2 * i] = sum[16 * (q >> 1) + 4 * i + 2 * (q & 1)] + b.x;
+                v[2 * i + 1] = sum[16 * (q >> 1) + 4 * i + 2 * (q & 1) + 1] + b.y;
+            }
+            if constexpr (EPI == EPI_RELU_AUX_BIAS) {
+                uint32_t word = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (at + 8 * i < p.n)
+                        word |= ((v[2 * i] > 0.0f ? 1u : 0u) | (v[2 * i + 1] > 0.0f ? 2u : 0u)) << (8 * i + c2);
+                word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
+                word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
+                if (c2 == 0 && row < p.m) static_cast<uint32_t*>(p.aux)[static_cast<long long>(row) * p.aux_ld + at / 32] = word;
+            }
+            activate(v, EPI);
+            const uint16_t* R = static_cast<const uint16_t*>(p.residual) + static_cast<long long>(row) * p.n + at + c2;
+            const int r32 = lane / 4 + 8 * q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (EPI == EPI_BIAS_RESIDUAL && row < p.m && at + 8 * i < p.n) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(R + 8 * i);
+                    v[2 * i] += __uint_as_float(w << 16);
+                    v[2 * i + 1] += __uint_as_float(w & 0xFFFF0000u);
+                }
+                *reinterpret_cast<uint32_t*>(box + r32 * 64 + ((i ^ ((r32 >> 1) & 3)) << 4) + 2 * c2) =
+                    pack2(v[2 * i], v[2 * i + 1], 1);
+            }
+        }
+    }
+    // 32 rows x 32 columns, 64-byte rows with the 64-byte swizzle
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(&p.tm_D, box_u32, at, row0);
+        bulk_commit_group();
     }
 }
 
 template <bool SQUARE, int EPI>
 __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, uint32_t sbase, uint32_t bar0,
-                                             uint32_t tmem_base, volatile int* abort_flag)
+                                           uint32_t tmem_base, volatile int* abort_flag)
 {
-    const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int ew = warp - 4;
-    const int quarter = warp & 3, half = ew >> 2;
+    const int sw = static_cast<int>(threadIdx.x >> 5) - 4;
+    const int quarter = sw & 3, half = sw >> 2;
     const WorkRange w = work_range<true>(p);
-    float* sbias = reinterpret_cast<float*>(smem + C::kOffBias) + ew * 512;  // this warp's own, as all of its areas
-    float* sscale = sbias + kCols;
-    const uint32_t sscale_u32 = sbase + C::kOffBias + ew * 2048 + kCols * 4;
-    uint8_t* box = smem + C::kOffEpi + ew * 2048;
-    const uint32_t box_u32 = sbase + C::kOffEpi + ew * 2048;
-    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * kCols;
-    const uint32_t empty0 = map_shared_rank(bar0 + 8u * kBarTmemEmpty, cluster_ctarank() & ~1u);
-    const long long sb_row = SQUARE ? (p.n + 127) / 128 : p.n;
+    float* sbias = reinterpret_cast<float*>(smem + kOffBias) + sw * kCols;  // this warp's own, as the box
+    uint8_t* box = smem + kOffBox + sw * 2048;
+    const uint32_t box_u32 = sbase + kOffBox + sw * 2048;
+    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t empty0 = map_shared_rank(bar0 + 8u * kBarAccEmpty, cluster_ctarank() & ~1u);
+    const float* scales = reinterpret_cast<const float*>(smem + kOffScale);
+    // this thread's row's factor, or its four rows' scales and its columns'
+    const float* rows = scales + quarter * 32 + (SQUARE ? half * 128 + lane : lane / 4);
+    const float* columns = scales + 128 + half * 128 + 2 * (lane & 3);
     constexpr bool kBias = EPI != EPI_NONE;
     grid_dependency_wait();
 
-    uint32_t block = 0;
+    uint32_t block = 0, group = 0;  // K blocks and groups of scales so far, over all tiles
+    auto failed = [&]() {
+        if (!*abort_flag) record_failure(p.status, abort_flag, kRoleEpilogue);
+        return false;
+    };
+    // block `b`'s MMAs are done
+    auto ready = [&](uint32_t b) {
+        const bool ok = warp_wait(bar0 + 8u * (kBarAccFull + 2 * (b & 1u) + half), (b >> 1) & 1u, abort_flag, p.wait_limit_ns);
+        tcgen05_fence_after_sync();
+        return ok || failed();
+    };
+    // the scales of block kb of the tile are there
+    auto scales_ready = [&](int kb) {
+        if (kb % kGroup != 0) return true;
+        return warp_wait(bar0 + 8u * (kBarScaleFull + group % kScaleGroups), group / kScaleGroups & 1u, abort_flag,
+                              p.wait_limit_ns) || failed();
+    };
+    // this warp has read its part of block `b`'s accumulator
+    auto release = [&](uint32_t b) {
+        tcgen05_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_pair(empty0 + 8u * (2 * (b & 1u) + half));
+    };
+    // ... and the scales of block kb
+    auto release_scales = [&](int kb) {
+        if (kb % kGroup != kGroup - 1 && kb != p.k_blocks - 1) return;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar0 + 8u * (kBarScaleEmpty + group % kScaleGroups));
+        ++group;
+    };
+    auto scales_at = [&](int kb) { return (group % kScaleGroups * kGroup + kb % kGroup) * kScaleFloats; };
+    auto accumulator = [&](uint32_t b) { return t_lane + (2 * (b & 1u) + half) * kCols; };
+
     int tile = w.first;
     for (int j = 0;; ++j) {
         if (j > 0 && !sched_take_warp(bar0, j, tile, abort_flag, p.wait_limit_ns)) {
@@ -141,161 +469,77 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
         int tm, tn;
         tile_coords(tile, p, tm, tn);
         const int row0 = tm * 2 * kBM + w.pair_rank * kBM + quarter * 32;
-        const int row = row0 + lane;
         const int col0 = tn * 256 + half * kCols;
-        const bool live = row0 < p.m && col0 < p.n;  // this warp has something to store
-        float lb = 0.0f;
+        bool ok = true;
+        if (row0 >= p.m || col0 >= p.n) {  // nothing of the tile for this warp to store
+            for (int kb = 0; kb < p.k_blocks && ok; ++kb, ++block) {
+                ok = scales_ready(kb) && ready(block);
+                if (!ok) break;
+                release(block);
+                release_scales(kb);
+            }
+            if (!ok) break;
+            continue;
+        }
         if (kBias && p.bias_layout == 1) {
             __syncwarp();
             for (int i = lane; i < kCols; i += 32)
                 sbias[i] = col0 + i < p.n ? load_16bit(p.bias, col0 + i, 1) : 0.0f;
-        } else if (kBias && row < p.m) {
-            lb = load_16bit(p.bias, row, 1);
-        }
-        const float* sa = p.scale_a + min(row, p.m - 1);
-        const float* sb = p.scale_b + (SQUARE ? min(col0 / kCols, static_cast<int>(sb_row) - 1) : 0);
-        // the scales of four blocks of k at a time, loaded while those before are worked on
-        float next_a[4], next_b[4];
-        auto load_scales = [&](int kb) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int b = min(kb + i, p.k_blocks - 1);
-                next_a[i] = sa[static_cast<long long>(b) * p.m];
-                if (SQUARE) next_b[i] = sb[static_cast<long long>(b) * sb_row];
-            }
-        };
-        auto copy_scales = [&](int kb) {  // (a scale for each row of B; columns past n stay as they are)
-            if (kb < p.k_blocks && col0 + 4 * lane < p.n)
-                cp_async_16(sscale_u32 + (kb % kScaleDepth) * (kCols * 4) + lane * 16,
-                            p.scale_b + static_cast<long long>(kb) * sb_row + col0 + 4 * lane);
-            cp_async_commit();
-        };
-        load_scales(0);
-        if constexpr (!SQUARE) {
-            __syncwarp();
-            copy_scales(0);
-            copy_scales(1);
         }
         float sum[kCols];
 #pragma unroll
         for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
-        bool ok = true;
-        for (int kb0 = 0; kb0 < p.k_blocks && ok; kb0 += 4) {
-            float f[4];
+        // sixteen values are on their way while those before them are added
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++block) {
+            ok = scales_ready(kb);
+            if (!ok) break;
+            float f[SQUARE ? 1 : 4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = SQUARE ? next_a[i] * next_b[i] : next_a[i];
-            if (kb0 + 4 < p.k_blocks) load_scales(kb0 + 4);
+            for (int i = 0; i < (SQUARE ? 1 : 4); ++i) f[i] = rows[scales_at(kb) + 8 * i];
+            const float* fc = columns + scales_at(kb);
+            ok = ready(block);
+            if (!ok) break;
+            const uint32_t from = accumulator(block);
+            uint32_t r[2][16];
+            float2 g[4];
+            auto load = [&](int c) {  // SQUARE: columns 16 c on; otherwise columns 32 (c / 2) on, lanes 16 (c % 2) on
+                if constexpr (SQUARE)
+                    load_lane16(from + c * 16, r[c & 1]);
+                else
+                    load_square16(from + ((c & 1) << 20) + (c >> 1) * 32, r[c & 1]);
+            };
+            load(0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int kb = kb0 + i;
-                if (kb >= p.k_blocks) break;
-                const float* cs = nullptr;
-                if constexpr (!SQUARE) {
-                    copy_scales(kb + 2);
-                    cp_async_wait_group<2>();
-                    __syncwarp();
-                    cs = sscale + (kb % kScaleDepth) * kCols;
+            for (int c = 0; c < 8; ++c) {
+                if (!SQUARE && c % 2 == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) g[i] = *reinterpret_cast<const float2*>(fc + 16 * c + 8 * i);
                 }
-                const uint32_t acc = block & 1u;
-                // (the warp gives up as one: what follows is for all of its lanes)
-                if (!__all_sync(0xFFFFFFFFu, wait_bounded(bar0 + 8u * (kBarTmemFull + acc), (block >> 1) & 1u,
-                                                          abort_flag, p.wait_limit_ns))) {
-                    if (!*abort_flag) record_failure(p.status, abort_flag, kRoleEpilogue);
-                    ok = false;
-                    break;
-                }
-                ++block;
-                tcgen05_fence_after_sync();
+                tmem_wait(r[c & 1]);
+                if (c < 7)
+                    load(c + 1);
+                else
+                    release(block);
+                float* s = sum + c * 16;
+                if constexpr (SQUARE) {
 #pragma unroll
-                for (int c = 0; c < kCols / 32; ++c) {
-                    uint32_t r[32];
-                    __syncwarp();
-                    if (live) tmem_load_32cols(t_lane + acc * 256u + c * 32, r);
-                    if (c == kCols / 32 - 1) {
-                        tcgen05_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(empty0 + 8u * acc);
-                    }
-                    if (!live) continue;
+                    for (int e = 0; e < 16; ++e) s[e] = fmaf(__uint_as_float(r[c & 1][e]), f[0], s[e]);
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        float* s = sum + c * 32 + e;
-                        const float x[4] = {__uint_as_float(r[e]), __uint_as_float(r[e + 1]),
-                                            __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])};
-                        if constexpr (SQUARE) {
-                            fma2(s[0], s[1], x[0], x[1], f[i]);
-                            fma2(s[2], s[3], x[2], x[3], f[i]);
-                        } else {
-                            const float4 v = *reinterpret_cast<const float4*>(cs + c * 32 + e);
-                            const float2 y = mul2(x[0], x[1], v.x, v.y), z = mul2(x[2], x[3], v.z, v.w);
-                            fma2(s[0], s[1], y.x, y.y, f[i]);
-                            fma2(s[2], s[3], z.x, z.y, f[i]);
-                        }
-                    }
+                    for (int e = 0; e < 16; ++e)
+                        s[e] = fmaf(__uint_as_float(r[c & 1][e]) * (e & 1 ? g[e / 4].y : g[e / 4].x), f[2 * (c & 1) + (e >> 1 & 1)], s[e]);
                 }
             }
+            release_scales(kb);
         }
         if (!ok) break;
-        if (!live) continue;
-        // ---- the tile's sums: bias, activation, residual, one rounding ----
-        if (kBias) __syncwarp();  // (sbias)
+        __syncwarp();  // (sbias)
 #pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) {
-            const int at = col0 + c * 32;
-            if (at >= p.n) break;
-            float v[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = sum[c * 32 + e];
-            uint4 res[4];
-            const bool whole = row < p.m && at + 32 <= p.n;
-            const uint16_t* R = static_cast<const uint16_t*>(p.residual) + static_cast<long long>(row) * p.n + at;
-            if (EPI == EPI_BIAS_RESIDUAL && whole) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) res[q] = reinterpret_cast<const uint4*>(R)[q];
-            }
-            if constexpr (kBias) add_bias<32>(v, sbias + c * 32, p.bias_layout == 1, lb);
-            if constexpr (EPI == EPI_RELU_AUX_BIAS) {
-                uint32_t word = 0;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) word |= (v[e] > 0.0f && at + e < p.n) ? (1u << e) : 0u;
-                if (row < p.m)
-                    static_cast<uint32_t*>(p.aux)[static_cast<long long>(row) * p.aux_ld + at / 32] = word;
-            }
-            activate(v, EPI);
-            if constexpr (EPI == EPI_BIAS_RESIDUAL) {
-                if (whole) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t ww[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            v[q * 8 + 2 * h] += __uint_as_float(ww[h] << 16);
-                            v[q * 8 + 2 * h + 1] += __uint_as_float(ww[h] & 0xFFFF0000u);
-                        }
-                    }
-                } else if (row < p.m) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (at + e < p.n) v[e] += load_16bit(R, e, 1);
-                }
-            }
-            // 32 rows x 32 columns, 64-byte rows with the 64-byte swizzle
-            if (lane == 0) bulk_wait_group_read<0>();  // this warp's last box is read
-            __syncwarp();
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<uint4*>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-                    make_uint4(pack2(v[8 * q], v[8 * q + 1], 1), pack2(v[8 * q + 2], v[8 * q + 3], 1),
-                               pack2(v[8 * q + 4], v[8 * q + 5], 1), pack2(v[8 * q + 6], v[8 * q + 7], 1));
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                tma_store_2d(&p.tm_D, box_u32, at, row0);
-                bulk_commit_group();
-            }
-        }
+        for (int c = 0; c < 4; ++c)
+            if (col0 + c * 32 < p.n)
+                store_chunk<SQUARE, EPI>(p, sum + c * 32, sbias + c * 32, row0,
+                                         col0 + c * 32, box, box_u32);
     }
-    if constexpr (!SQUARE) cp_async_wait_all();
     if (lane == 0) bulk_wait_group_read<0>();
     __syncwarp();
 }
@@ -307,26 +551,30 @@ __global__ void __launch_bounds__(kBlockThreads, 1) block_pair_kernel(const __gr
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t bar0 = sbase + C::kOffBar;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffBar + kOffHolder);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + kOffAbort);
+    const uint32_t bar0 = sbase + kOffBar;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffBar + kOffHolder);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + kOffAbort);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         prefetch_tensormap(&p.tm_A);
         prefetch_tensormap(&p.tm_B);
         prefetch_tensormap(&p.tm_D);
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(bar0 + 8u * (kBarFull + s), 1);
             mbar_init(bar0 + 8u * (kBarEmpty + s), 1);
         }
         for (int s = 0; s < kSchedSlots; ++s) {
             mbar_init(bar0 + 8u * (kBarSchedFull + s), 1);
-            mbar_init(bar0 + 8u * (kBarSchedEmpty + s), sched_consumers<kEpiWarps>());
+            mbar_init(bar0 + 8u * (kBarSchedEmpty + s), sched_consumers<kSumWarps>() + 2);  // (and the scales' warps)
         }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(bar0 + 8u * (kBarTmemFull + a), 1);
-            mbar_init(bar0 + 8u * (kBarTmemEmpty + a), 2 * kEpiWarps);  // a lane of every epilogue warp of the pair
+        for (int s = 0; s < kScaleGroups; ++s) {
+            mbar_init(bar0 + 8u * (kBarScaleFull + s), 1);
+            mbar_init(bar0 + 8u * (kBarScaleEmpty + s), kSumWarps);
+        }
+        for (int a = 0; a < 4; ++a) {
+            mbar_init(bar0 + 8u * (kBarAccFull + a), 1);
+            mbar_init(bar0 + 8u * (kBarAccEmpty + a), kSumWarps);  // a lane of each warp of this half, of both CTAs
         }
         mbar_init(bar0 + 8u * kBarStall, 1);
         mbar_init(bar0 + 8u * kBarDrain, 1);
@@ -352,9 +600,11 @@ __global__ void __launch_bounds__(kBlockThreads, 1) block_pair_kernel(const __gr
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 0 && !*abort_flag) {
-            if (lane == 0) run_producer<256, false, true, false, true>(p, sbase, bar0, abort_flag, 0);
+            if (lane == 0) copy_operands(p, sbase, bar0, abort_flag);
         } else if (warp == 1 && !*abort_flag) {
-            if (lane == 0) issue_blocks(p, sbase, bar0, tmem_base, abort_flag);
+            issue_blocks(p, sbase, bar0, tmem_base, abort_flag);
+        } else if (warp == 2 && !*abort_flag) {
+            stage_scales<SQUARE>(p, smem, bar0, abort_flag);
         }
         __syncwarp();
     } else {
@@ -376,11 +626,11 @@ cudaError_t launch_one(const GemmParams& p, int grid, cudaStream_t stream, bool 
 {
     if (prepare)
         return cudaFuncSetAttribute(block_pair_kernel<SQUARE, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    C::kSmemBytes);
+                                    kSmemBytes);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(kBlockThreads, 1, 1);
-    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -8,4 +8,7 @@ cudaError_t block_pair_square(int epilog, const GemmParams& p, int grid, cudaStr
     return block_pair::launch_epilog<true>(epilog, p, grid, stream, pdl, prepare);
 }
 
+int block_pair_smem() { return block_pair::kSmemBytes; }
+int block_pair_stages() { return block_pair::kStages; }
+
 }  // namespace gemm_epi

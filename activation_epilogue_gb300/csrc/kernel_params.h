@@ -217,6 +217,8 @@ cudaError_t fp8_pair_launch(int bn, const GemmParams& p, int grid, cudaStream_t 
 // fp8_pair_launch; prepare: set the kernel's shared memory instead of launching it.
 cudaError_t block_pair_square(int epilog, const GemmParams& p, int grid, cudaStream_t stream, bool pdl, bool prepare);
 cudaError_t block_pair_rows(int epilog, const GemmParams& p, int grid, cudaStream_t stream, bool pdl, bool prepare);
+int block_pair_smem();
+int block_pair_stages();
 // Few rows of A: tiles of 128 columns (tiles_m of them) by np rows (tiles_n; 16, 32, 64 or 128), K over a
 // cluster of `split` blocks; grid = tiles_m * tiles_n * split.
 cudaError_t block_swapped(int np, bool square, const GemmParams& p, int grid, cudaStream_t stream, bool pdl, bool prepare);
