@@ -13,8 +13,7 @@
 //   * Four accumulators of 128 columns, half a tile each: a half's MMAs run while the three before
 //     it are read, so that no MMA waits for a round trip through barriers.
 //   * Eight summing warps (a lane quarter, half the tile's columns each), 128 sums a thread; sixteen values
-//     are on their way from tensor memory while the sixteen before them are added, in plain fp32 (the
-//     two-column instructions are slower).  Sixteen warps of 64 sums leave too few registers for the
+//     are on their way from tensor memory while the sixteen before them are added, two an instruction.  Sixteen warps of 64 sums leave too few registers for the
 //     addresses, which are then formed again in every block (1099 us for 16384 x 8192 x 8192, 835 so).
 //   * SQUARE: a warp's columns share one scale, a thread (a row) has one factor a block.  Otherwise
 //     every column has its own, and a thread's values are loaded as four rows of 32 columns, so that 32
@@ -92,6 +91,40 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[N])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Pairs of fp32 in 64-bit registers: two additions an instruction.
+using Pair = unsigned long long;
+
+__device__ __forceinline__ Pair pair_of(uint32_t a, uint32_t b)
+{
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(a), "r"(b));
+    return p;
+}
+
+// (x, y) += a b
+__device__ __forceinline__ void fma2(float& x, float& y, Pair a, Pair b)
+{
+    Pair acc;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(x), "f"(y));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(acc));
+}
+
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
+
+// Shared memory by its own address (through generic ones the loads' latency is much longer).
+__device__ __forceinline__ Pair ld_shared_pair(uint32_t addr)
+{
+    Pair v;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // True in one lane of a converged warp.
@@ -419,10 +452,9 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
     const uint32_t box_u32 = sbase + kOffBox + sw * 2048;
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t empty0 = map_shared_rank(bar0 + 8u * kBarAccEmpty, cluster_ctarank() & ~1u);
-    const float* scales = reinterpret_cast<const float*>(smem + kOffScale);
     // this thread's row's factor, or its four rows' scales and its columns'
-    const float* rows = scales + quarter * 32 + (SQUARE ? half * 128 + lane : lane / 4);
-    const float* columns = scales + 128 + half * 128 + 2 * (lane & 3);
+    const uint32_t rows = sbase + kOffScale + 4 * (quarter * 32 + (SQUARE ? half * 128 + lane : lane / 4));
+    const uint32_t columns = sbase + kOffScale + 4 * (128 + half * 128 + 2 * (lane & 3));
     constexpr bool kBias = EPI != EPI_NONE;
     grid_dependency_wait();
 
@@ -456,7 +488,7 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
         if (lane == 0) mbar_arrive(bar0 + 8u * (kBarScaleEmpty + group % kScaleGroups));
         ++group;
     };
-    auto scales_at = [&](int kb) { return (group % kScaleGroups * kGroup + kb % kGroup) * kScaleFloats; };
+    auto scales_at = [&](int kb) { return (group % kScaleGroups * kGroup + kb % kGroup) * (kScaleFloats * 4); };
     auto accumulator = [&](uint32_t b) { return t_lane + (2 * (b & 1u) + half) * kCols; };
 
     int tile = w.first;
@@ -489,45 +521,47 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
         float sum[kCols];
 #pragma unroll
         for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
-        // sixteen values are on their way while those before them are added
+        // Sixteen values are on their way while those before them are added.  (The next block's first ones ahead of
+        // this one's end, and sums held as pairs, cost copies of registers: 941 and 860 us for 16384 x 8192 x 8192, 827 so.)
+        uint32_t r[2][16];
+        auto load = [&](uint32_t b, int c) {  // SQUARE: columns 16 c on; otherwise columns 32 (c / 2) on, lanes 16 (c % 2) on
+            if constexpr (SQUARE)
+                load_lane16(accumulator(b) + c * 16, r[c & 1]);
+            else
+                load_square16(accumulator(b) + ((c & 1) << 20) + (c >> 1) * 32, r[c & 1]);
+        };
         for (int kb = 0; kb < p.k_blocks; ++kb, ++block) {
             ok = scales_ready(kb);
             if (!ok) break;
-            float f[SQUARE ? 1 : 4];
+            const uint32_t at = scales_at(kb);
+            Pair f[SQUARE ? 1 : 4], g[4];
 #pragma unroll
-            for (int i = 0; i < (SQUARE ? 1 : 4); ++i) f[i] = rows[scales_at(kb) + 8 * i];
-            const float* fc = columns + scales_at(kb);
+            for (int i = 0; i < (SQUARE ? 1 : 4); ++i) {
+                const uint32_t v = ld_shared_u32(rows + at + 32 * i);
+                f[i] = pair_of(v, v);
+            }
             ok = ready(block);
             if (!ok) break;
-            const uint32_t from = accumulator(block);
-            uint32_t r[2][16];
-            float2 g[4];
-            auto load = [&](int c) {  // SQUARE: columns 16 c on; otherwise columns 32 (c / 2) on, lanes 16 (c % 2) on
-                if constexpr (SQUARE)
-                    load_lane16(from + c * 16, r[c & 1]);
-                else
-                    load_square16(from + ((c & 1) << 20) + (c >> 1) * 32, r[c & 1]);
-            };
-            load(0);
+            load(block, 0);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 if (!SQUARE && c % 2 == 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) g[i] = *reinterpret_cast<const float2*>(fc + 16 * c + 8 * i);
+                    for (int i = 0; i < 4; ++i) g[i] = ld_shared_pair(columns + at + 64 * c + 32 * i);
                 }
                 tmem_wait(r[c & 1]);
                 if (c < 7)
-                    load(c + 1);
+                    load(block, c + 1);
                 else
                     release(block);
-                float* s = sum + c * 16;
-                if constexpr (SQUARE) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) s[e] = fmaf(__uint_as_float(r[c & 1][e]), f[0], s[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        s[e] = fmaf(__uint_as_float(r[c & 1][e]) * (e & 1 ? g[e / 4].y : g[e / 4].x), f[2 * (c & 1) + (e >> 1 & 1)], s[e]);
+                for (int e = 0; e < 16; e += 2) {
+                    float* s = sum + c * 16 + e;
+                    const Pair x = pair_of(r[c & 1][e], r[c & 1][e + 1]);
+                    if constexpr (SQUARE)
+                        fma2(s[0], s[1], x, f[0]);
+                    else
+                        fma2(s[0], s[1], mul2(x, g[e / 4]), f[2 * (c & 1) + (e >> 1 & 1)]);
                 }
             }
             release_scales(kb);
