@@ -23,12 +23,26 @@ __device__ __forceinline__ uint2 e4m3_codes8(const float (&x)[8], float inv)
                       e4m3_codes4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
 }
 
-// A block's scale and its reciprocal from its largest |x|; an infinite or NaN one goes into the scale.
+// A block's scale, top / 448 correctly rounded (the quotient's remainder, exact in one fma, put right: Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), and its reciprocal to
+// 2^-23 from its largest |x|; an infinite or NaN one goes into the scale.
 __device__ __forceinline__ void block_scale(float top, float& scale, float& inv)
 {
-    const bool nothing = top < kBlockFloor;
-    scale = nothing ? 0.0f : top / kE4m3Top;
-    inv = nothing ? 0.0f : 1.0f / scale;
+    constexpr float kInverse = 1.0f / kE4m3Top;
+    const float q = top * kInverse;
+    const float right = fmaf(fmaf(-q, kE4m3Top, top), kInverse, q);
+    scale = top < kBlockFloor ? 0.0f : q < 1.0e36f ? right : q;  // (an infinity has no remainder)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+    inv = top < kBlockFloor ? 0.0f : inv;
+}
+
+// The largest bit pattern of eight |x|.
+__device__ __forceinline__ uint32_t abs_max8(const float (&x)[8])
+{
+    uint32_t m[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[e] = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+    return __vimax3_u32(__vimax3_u32(m[0], m[1], m[2]), __vimax3_u32(m[3], m[4], m[5]), max(m[6], m[7]));
 }
 
 // The largest of the 16 lanes of a half warp, in all of them (bit patterns of |x|: as whole numbers

@@ -108,11 +108,8 @@ __device__ __forceinline__ void store_y(const LayernormArgs& a, long long r, int
     if constexpr (!E4M3) {
         if (in) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.Y) + r * a.d + c) = encode8<BF16>(y);
     } else {
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(y[e]) & 0x7FFFFFFFu);
         float scale, inv;
-        block_scale(__uint_as_float(half_warp_max(in ? m : 0u)), scale, inv);
+        block_scale(__uint_as_float(half_warp_max(in ? abs_max8(y) : 0u)), scale, inv);
         if (!in) return;
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.Y) + r * a.d + c) = e4m3_codes8(y, inv);
         if ((threadIdx.x & 15) == 0) a.scale[static_cast<long long>(c / 128) * a.t + r] = scale;
@@ -185,8 +182,17 @@ __device__ __forceinline__ float row_from_memory(const LayernormArgs& a, long lo
     return 0.0f;
 }
 
+// Blocks an SM (at least): what keeps enough loads on their way.  gamma and beta are read where they are used, from L1
+// and L2: held in registers from the start they left two blocks of 256 threads an SM (16384 x 8192 to E4M3: 200 us;
+// three blocks so 156, four 154, five 141).  2039 x 4096 to 16 bits: 8.1 us with 8, 8.5 with 6, 9.5 with 10.
+template <int T, int V>
+constexpr int ln_blocks()
+{
+    return T == 512 ? 2 : T == 256 ? 5 : V == 4 ? 8 : V == 2 ? 10 : 12;
+}
+
 template <bool BF16, int T, int V, bool E4M3>
-__global__ void __launch_bounds__(ln_block<T>()) layernorm_forward_kernel(const LayernormArgs a)
+__global__ void __launch_bounds__(ln_block<T>(), ln_blocks<T, V>()) layernorm_forward_kernel(const LayernormArgs a)
 {
     constexpr int kRows = ln_block<T>() / T;
     __shared__ float part[16];
@@ -196,13 +202,11 @@ __global__ void __launch_bounds__(ln_block<T>()) layernorm_forward_kernel(const 
     grid_launch_dependents();
     const long long r = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / T;
     if (r >= a.t) return;  // (T = 32: a whole warp, and no barrier below)
-    uint4 h[V], gamma[V], beta[V];
+    uint4 h[V];
     load_row<T, V>(a.X, r, a.d, h);
     if (a.residual) {
         uint4 res[V];
         load_row<T, V>(a.residual, r, a.d, res);
-        load_row<T, V>(a.gamma, 0, a.d, gamma);
-        load_row<T, V>(a.beta, 0, a.d, beta);
         uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.H) + r * a.d);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -214,9 +218,6 @@ __global__ void __launch_bounds__(ln_block<T>()) layernorm_forward_kernel(const 
             h[j] = encode8<BF16>(x);
             if ((j * T + i0) * 8 < a.d) out[j * T + i0] = h[j];
         }
-    } else {
-        load_row<T, V>(a.gamma, 0, a.d, gamma);
-        load_row<T, V>(a.beta, 0, a.d, beta);
     }
     const float inv_d = 1.0f / static_cast<float>(a.d);
     float s = 0.0f;
@@ -253,10 +254,15 @@ __global__ void __launch_bounds__(ln_block<T>()) layernorm_forward_kernel(const 
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int c = (j * T + i0) * 8;
+        uint4 gamma = make_uint4(0, 0, 0, 0), beta = gamma;
+        if (c < a.d) {
+            gamma = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.gamma) + c);
+            beta = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.beta) + c);
+        }
         float x[8], g[8], b[8];
         decode8<BF16>(h[j], x);
-        decode8<BF16>(gamma[j], g);
-        decode8<BF16>(beta[j], b);
+        decode8<BF16>(gamma, g);
+        decode8<BF16>(beta, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = fmaf((x[e] - m0 - more) * rstd, g[e], b[e]);
         store_y<BF16, E4M3>(a, r, c, c < a.d, x);
@@ -292,7 +298,8 @@ __global__ void __launch_bounds__(kLongThreads) layernorm_long_kernel(const Laye
 // ---- backward ------------------------------------------------------------------------------
 // A block walks rows and keeps the sums of dgamma and dbeta of its rows in registers, every column with
 // one thread (T = 32: one per warp, added in order at the end), and writes them to its row of the
-// workspace; layernorm_sums_kernel adds those.  The next row is copied to shared memory while this one
+// workspace; layernorm_sums_kernel adds those.  (Added up over a cluster of two to eight blocks first they
+// cost more than the rows saved: 8192 x 4096 46 us without, 46 to 68 so.)  The next row is copied to shared memory while this one
 // is worked on, every thread copying the vectors that it reads itself, so that the copies need no barrier.
 
 // (h - mu) rstd, where h - mu may leave fp32: both are halved for rows of that size.
@@ -314,8 +321,10 @@ __host__ __device__ constexpr int ln_backward_smem()
     return 2 * 3 * V * ln_block<T>() * 16;
 }
 
+// (As many registers as a block can have, but for the two blocks an SM of 8192 columns: 8192 x 4096 46 us, 59 with the
+// compiler's 80; 16384 x 8192 165 us with two blocks, 174 with one.)
 template <bool BF16, int T, int V>
-__global__ void __launch_bounds__(ln_block<T>()) layernorm_backward_kernel(const LayernormBackwardArgs a)
+__global__ void __launch_bounds__(ln_block<T>(), T == 256 && V == 4 ? 2 : 1) layernorm_backward_kernel(const LayernormBackwardArgs a)
 {
     constexpr int kBlock = ln_block<T>(), kRows = kBlock / T;
     extern __shared__ __align__(16) uint4 buf[];  // [2][dY, H, dH][V][thread]
@@ -402,36 +411,37 @@ __global__ void __launch_bounds__(ln_block<T>()) layernorm_backward_kernel(const
         }
         now = next;
     }
-    const long long width = 2ll * a.d;
+    float4* out = reinterpret_cast<float4*>(a.ws_sums) + blockIdx.x * 2ll * (a.d / 4);  // [dgamma, dbeta][d / 4]
+    auto place = [&](int j, int q) { return (q >> 1) * (a.d / 4) + (j * T + i0) * 2 + (q & 1); };
+    auto value = [&](int j, int q) {  // of dgamma's eight columns, then of dbeta's
+        const float* v = q < 2 ? dg[j] + 4 * q : db[j] + 4 * (q - 2);
+        return make_float4(v[0], v[1], v[2], v[3]);
+    };
     if constexpr (kRows > 1) {
-        __shared__ float sum[2][T * V * 8];
+        float4* sums = reinterpret_cast<float4*>(buf);
+        cp_async_wait_group<0>();
         for (int w = 0; w < kRows; ++w) {
-            if (threadIdx.x / T == w) {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int at = (j * T + i0) * 8 + e;
-                        sum[0][at] = w == 0 ? dg[j][e] : sum[0][at] + dg[j][e];
-                        sum[1][at] = w == 0 ? db[j][e] : sum[1][at] + db[j][e];
-                    }
-            }
             __syncthreads();
+            if (static_cast<int>(threadIdx.x) / T != w) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if ((j * T + i0) * 8 >= a.d) continue;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 v = value(j, q);
+                    float4& at = sums[place(j, q)];
+                    at = w == 0 ? v : make_float4(at.x + v.x, at.y + v.y, at.z + v.z, at.w + v.w);
+                }
+            }
         }
-        for (int c = threadIdx.x; c < a.d; c += kBlock) {
-            a.ws_sums[blockIdx.x * width + c] = sum[0][c];
-            a.ws_sums[blockIdx.x * width + a.d + c] = sum[1][c];
-        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.d / 2; i += kBlock) out[i] = sums[i];
     } else {
-        float4* out = reinterpret_cast<float4*>(a.ws_sums + blockIdx.x * width);
-        float4* out_b = reinterpret_cast<float4*>(a.ws_sums + blockIdx.x * width + a.d);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             if ((j * T + i0) * 8 >= a.d) continue;
-            out[(j * T + i0) * 2] = make_float4(dg[j][0], dg[j][1], dg[j][2], dg[j][3]);
-            out[(j * T + i0) * 2 + 1] = make_float4(dg[j][4], dg[j][5], dg[j][6], dg[j][7]);
-            out_b[(j * T + i0) * 2] = make_float4(db[j][0], db[j][1], db[j][2], db[j][3]);
-            out_b[(j * T + i0) * 2 + 1] = make_float4(db[j][4], db[j][5], db[j][6], db[j][7]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) out[place(j, q)] = value(j, q);
         }
     }
 }
@@ -585,9 +595,11 @@ struct BackwardShape {
 
 BackwardShape backward_shape(long long t, long long d)
 {
+    // (most blocks, measured: 8192 x 1024 18.1 us with 912, 18.9 with 608; 8192 x 2048 27.9 with 760, 29.5 with 608, 33.8
+    // with 456; 8192 x 4096 46 with 304, 51 with 608, 56 with 456: more than are there at once make a second wave)
     if (d <= 512) return t <= 2048 ? BackwardShape{1, 456} : BackwardShape{4, 456};
-    if (d <= 2048) return {1, 608};
-    if (d <= 4096) return {1, 456};
+    if (d <= 1024) return {1, t <= 2048 ? 456 : 912};
+    if (d <= 2048) return {1, 760};
     if (d <= 8192) return {1, 304};
     if (d <= kMaxWidth) return {1, 152};
     return {1, static_cast<int>(kMaxWidth * 64 / d) + 1};  // (times d / 2048 blocks)
