@@ -1,0 +1,87 @@
+// What the block-scaled products' summing warps use: loads from tensor memory that are waited for later, and
+// fp32 arithmetic on pairs.
+#pragma once
+
+#include <cstdint>
+
+namespace gemm_epi {
+
+// Start loading values of this warp's accumulator lanes, valid after tmem_wait on them: 16 columns of each thread's
+// lane ...
+__device__ __forceinline__ void load_lane16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// ... or, of 16 lanes and 32 columns, thread t's pairs of columns 8 i + 2 (t % 4), + 1 in lanes t / 4 (r[4 i],
+// r[4 i + 1]) and t / 4 + 8 (r[4 i + 2], r[4 i + 3]).
+__device__ __forceinline__ void load_square16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// ... and of 16 lanes and 16 columns.
+__device__ __forceinline__ void load_square8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Wait for this thread's loads; r (their destination) is marked as written here, so that nothing reads it earlier.
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Pairs of fp32 in 64-bit registers: two additions an instruction.
+using Pair = unsigned long long;
+
+__device__ __forceinline__ Pair pair_of(uint32_t a, uint32_t b)
+{
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(a), "r"(b));
+    return p;
+}
+
+// (x, y) += a b
+__device__ __forceinline__ void fma2(float& x, float& y, Pair a, Pair b)
+{
+    Pair acc;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(x), "f"(y));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(acc));
+}
+
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
+
+// Shared memory by its own address (through generic ones the loads' latency is much longer).
+__device__ __forceinline__ Pair ld_shared_pair(uint32_t addr)
+{
+    Pair v;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+}  // namespace gemm_epi

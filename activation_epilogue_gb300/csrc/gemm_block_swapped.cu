@@ -3,13 +3,15 @@
 // few rows streams B through every SM without computing rows that are not there.
 //
 // As in the CTA-pair kernel (gemm_block_pair.cuh) each K block's sum is an accumulator of its own,
-// here one of four in turn, which the summing warps read, scale and add up in fp32.  A thread's
-// lane is a column of D and its registers are rows of A, so that the scales of A vary along the
-// registers: the warps stage them eight K blocks at a time in shared memory (times the scale of
-// B's block, which the whole tile shares, with SQUARE; otherwise the lane's own scale of B is
-// applied with the addition).  K may be split over the blocks of a cluster, which add their sums
+// here one of four in turn, which the summing warps read, scale and add up in fp32.  Accumulator
+// lanes are columns of D and its columns rows of A.  The warps stage the scales of A eight K blocks
+// at a time in shared memory (times the scale of B's block, which the whole tile shares, with
+// SQUARE; otherwise with the scales of B's rows), and a thread's values are loaded as four lanes of
+// a quarter of the rows of A, so that it reads a quarter of their scales (all of them, by every lane,
+// took 256 cycles of shared memory a K block of 64 rows, as many as the copies).  K may be split over the blocks of a cluster, which add their sums
 // in rank order through distributed shared memory, each for every cluster-th row, so that the
 // result does not depend on timing.  A block is bound by the copies of its 16 KB of B a K block.
+#include "block_sums.cuh"
 #include "gemm_kernel.cuh"
 #include "launch.h"
 
@@ -21,11 +23,13 @@ constexpr int kRowsB = 128;   // columns of D per block: MMA rows
 constexpr int kAccs = 4;
 constexpr int kGroup = 8;     // K blocks whose scales are staged together
 constexpr int kMaxStages = 12;
+constexpr int kAloneSmem = 200 * 1024;  // with this much a block has an SM to itself
+constexpr int kRedRow = kRowsB + 4;  // (a warp's sums meet different banks)
 
 enum : int { kFull = 0, kEmpty = kMaxStages, kAccFull = 2 * kMaxStages, kAccEmpty = kAccFull + kAccs,
              kStall = kAccEmpty + kAccs, kDrain, kBars };
 
-template <int NP>
+template <int NP, bool SQUARE>
 struct Layout {
     static constexpr int kParts = NP >= 64 ? 2 : 1;       // warps per lane quarter, NP / kParts rows of A each
     static constexpr int kOwn = NP / kParts;
@@ -35,14 +39,19 @@ struct Layout {
     static constexpr int kThreads = kSumThreads + 128;    // (the last two warps help with the epilogue)
     static constexpr int kB = kRowsB * 128, kA = NP * 128;
     static constexpr int kStage = kB + kA;
-    static constexpr int kStagesRaw = (200 * 1024) / kStage;
+    // Two blocks an SM (one of 128 rows, whose sums need the registers): twice the K slices, and a call's last
+    // blocks share the SMs with the next call's first.
+    static constexpr int kPerSm = NP == 128 ? 1 : 2;
+    static constexpr int kStagesRaw = (NP == 128 ? 200 : 96) * 1024 / kStage;
     static constexpr int kStages = kStagesRaw > kMaxStages ? kMaxStages : kStagesRaw;
-    static constexpr int kOffScale = kStages * kStage;    // [2][kGroup][NP]
-    static constexpr int kOffBar = kOffScale + 2 * kGroup * NP * 4;
+    static constexpr int kChunk = kOwn < 32 ? 16 : 32;    // rows of A per load from tensor memory
+    static constexpr int kScaleBytes = kGroup * (NP + (SQUARE ? 0 : kRowsB)) * 4;
+    static constexpr int kOffScale = kStages * kStage;    // [2][kGroup][NP], then [kGroup][columns of D]
+    static constexpr int kOffBar = kOffScale + 2 * kScaleBytes;
     static constexpr int kBytes = 1024 + kOffBar + kBars * 8 + 16;
     static constexpr int kTmem = kAccs * NP;
-    static_assert(kBytes <= 227 * 1024, "shared memory");
-    static_assert(NP * kRowsB * 4 <= kStages * kStage, "the sums fit the ring");
+    static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory");
+    static_assert(NP * kRedRow * 4 <= kStages * kStage, "the sums fit the ring");
     static_assert(kTmem <= 512 && kTmem >= 32, "tensor memory");
     static constexpr int kStaged = kGroup * NP / kSumThreads;  // scales that a thread stages for a group
     static_assert(kGroup * NP % kSumThreads == 0, "staging");
@@ -66,16 +75,10 @@ __device__ __forceinline__ float2 ld_shared_cluster_f32x2(uint32_t addr)
     return v;
 }
 
-// (x, y) += (a, b) * (u, v)
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float u, float v)
-{
-    unsigned long long acc, c, s;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(x), "f"(y));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(a), "f"(b));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(s) : "f"(u), "f"(v));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(c), "l"(s));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(acc));
-}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) { st_shared_u32(addr, __float_as_uint(v)); }
+
+__device__ __forceinline__ void load_values(uint32_t taddr, uint32_t (&r)[16]) { load_square16(taddr, r); }
+__device__ __forceinline__ void load_values(uint32_t taddr, uint32_t (&r)[8]) { load_square8(taddr, r); }
 
 __device__ __forceinline__ float apply(float v, int epilog)
 {
@@ -84,9 +87,9 @@ __device__ __forceinline__ float apply(float v, int epilog)
 }
 
 template <int NP, bool SQUARE>
-__global__ void __launch_bounds__(Layout<NP>::kThreads, 1) block_swapped_kernel(const __grid_constant__ GemmParams p)
+__global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUARE>::kPerSm) block_swapped_kernel(const __grid_constant__ GemmParams p)
 {
-    using L = Layout<NP>;
+    using L = Layout<NP, SQUARE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t sbase = smem_u32(smem);
@@ -150,8 +153,13 @@ __global__ void __launch_bounds__(Layout<NP>::kThreads, 1) block_swapped_kernel(
                 if (a) tma_load_2d(sbase + s * L::kStage + L::kB, &p.tm_A, full, (first + i) * 128, m0);
             };
             const int ahead = min(blocks, L::kStages);
-            if (p.b_ready)
-                for (int i = 0; i < ahead; ++i) copy(i, true, false);
+            // (ahead of the wait: B itself where that is promised, otherwise B into L2, which needs no promise)
+            for (int i = 0; i < ahead; ++i) {
+                if (p.b_ready)
+                    copy(i, true, false);
+                else
+                    tma_prefetch_2d(&p.tm_B, (first + i) * 128, n0);
+            }
             grid_dependency_wait();
             for (int i = 0; i < ahead; ++i) copy(i, !p.b_ready, true);
             issued = ahead;
@@ -200,11 +208,10 @@ __global__ void __launch_bounds__(Layout<NP>::kThreads, 1) block_swapped_kernel(
         __syncwarp();
     } else if (warp < L::kSumWarps && !p.debug_stall) {
         const int quarter = warp & 3, part = warp >> 2;
-        const int col = min(n0 + quarter * 32 + lane, p.n - 1);
         const long long sb_row = SQUARE ? (p.n + 127) / 128 : p.n;
-        float* staged = reinterpret_cast<float*>(smem + L::kOffScale);
+        const uint32_t staged = sbase + L::kOffScale;
         float next[L::kStaged], next_b[SQUARE ? 1 : kGroup];
-        auto load = [&](int g) {  // the scales of group g of this block's K blocks (the last one's again past the end)
+        auto load_scales = [&](int g) {  // of group g of this block's K blocks (the last one's again past the end)
 #pragma unroll
             for (int e = 0; e < L::kStaged; ++e) {
                 const int at = threadIdx.x + e * L::kSumThreads;
@@ -212,62 +219,77 @@ __global__ void __launch_bounds__(Layout<NP>::kThreads, 1) block_swapped_kernel(
                 next[e] = p.scale_a[static_cast<long long>(b) * p.m + min(m0 + at % NP, p.m - 1)];
                 if (SQUARE) next[e] *= p.scale_b[static_cast<long long>(b) * sb_row + n0 / 128];
             }
-            if constexpr (!SQUARE) {
+            if (!SQUARE && threadIdx.x < kRowsB) {
 #pragma unroll
                 for (int e = 0; e < kGroup; ++e)
-                    next_b[e] = p.scale_b[static_cast<long long>(first + min(g * kGroup + e, blocks - 1)) * sb_row + col];
+                    next_b[e] = p.scale_b[static_cast<long long>(first + min(g * kGroup + e, blocks - 1)) * sb_row +
+                                          min(n0 + static_cast<int>(threadIdx.x), p.n - 1)];
             }
         };
         grid_dependency_wait();
-        load(0);
+        load_scales(0);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * L::kOwn;
         bool ok = true;
         for (int g = 0; g * kGroup < blocks; ++g) {
-            float* mine = staged + (g & 1) * (kGroup * NP);
-            float fb[SQUARE ? 1 : kGroup];
+            const uint32_t mine = staged + (g & 1) * L::kScaleBytes;
 #pragma unroll
-            for (int e = 0; e < L::kStaged; ++e) mine[threadIdx.x + e * L::kSumThreads] = next[e];
-            if constexpr (!SQUARE) {
+            for (int e = 0; e < L::kStaged; ++e) st_shared_f32(mine + 4 * (threadIdx.x + e * L::kSumThreads), next[e]);
+            if (!SQUARE && threadIdx.x < kRowsB) {
 #pragma unroll
-                for (int e = 0; e < kGroup; ++e) fb[e] = next_b[e];
+                for (int e = 0; e < kGroup; ++e) st_shared_f32(mine + kGroup * NP * 4 + 4 * (e * kRowsB + threadIdx.x), next_b[e]);
             }
             // (a buffer is written again two groups on: by then every thread has passed the barrier between)
             named_barrier_sync(1, L::kSumThreads);
-            if ((g + 1) * kGroup < blocks) load(g + 1);
-#pragma unroll
+            if ((g + 1) * kGroup < blocks) load_scales(g + 1);
+#pragma unroll 1
             for (int e = 0; e < kGroup; ++e) {
-                const int i = g * kGroup + e, acc = e % kAccs;
+                const int i = g * kGroup + e, acc = i % kAccs;
                 if (i >= blocks || !ok) continue;
                 // (the warp gives up as one: what follows is for all of its lanes)
-                if (!__all_sync(0xFFFFFFFFu, wait_bounded(bar0 + 8 * (kAccFull + acc), i / kAccs & 1, abort_flag,
-                                                          p.wait_limit_ns))) {
+                const uint32_t bar = bar0 + 8 * (kAccFull + acc), parity = i / kAccs & 1;
+                if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)) &&
+                    !__all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, p.wait_limit_ns))) {
                     if (!*abort_flag) record_failure(p.status, abort_flag, kRoleEpilogue);
                     ok = false;
                     continue;
                 }
                 tcgen05_fence_after_sync();
-                const float* fa = mine + e * NP + part * L::kOwn;
+                const uint32_t fa = mine + (e * NP + part * L::kOwn + 2 * (lane & 3)) * 4;
+                Pair fb[4];  // lanes lane / 4 + 8 j
+                if constexpr (!SQUARE) {
 #pragma unroll
-                for (int c = 0; c < L::kOwn; c += 16) {
-                    uint32_t r[32];
-                    __syncwarp();
-                    tmem_load_16cols(t_lane + acc * NP + c, r);
-                    if (c + 16 == L::kOwn) {
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t v = ld_shared_u32(mine + (kGroup * NP + e * kRowsB + quarter * 32 + 8 * j + (lane >> 2)) * 4);
+                        fb[j] = pair_of(v, v);
+                    }
+                }
+                constexpr int kLoads = 2 * L::kOwn / L::kChunk;  // chunk of columns, half of the lanes
+                uint32_t r[2][L::kChunk / 2];
+                auto load = [&](int c) { load_values(t_lane + acc * NP + ((c & 1) << 20) + (c >> 1) * L::kChunk, r[c & 1]); };
+                load(0);
+                Pair f[L::kChunk / 8];
+#pragma unroll
+                for (int c = 0; c < kLoads; ++c) {
+                    if (c % 2 == 0) {
+#pragma unroll
+                        for (int q = 0; q < L::kChunk / 8; ++q) f[q] = ld_shared_pair(fa + ((c >> 1) * L::kChunk + 8 * q) * 4);
+                    }
+                    tmem_wait(r[c & 1]);
+                    if (c + 1 < kLoads) {
+                        load(c + 1);
+                    } else {
                         tcgen05_fence_before_sync();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar0 + 8 * (kAccEmpty + acc));
                     }
 #pragma unroll
-                    for (int q = 0; q < 16; q += 4) {
-                        float4 f = *reinterpret_cast<const float4*>(fa + c + q);
-                        if constexpr (!SQUARE) {
-                            f.x *= fb[e];
-                            f.y *= fb[e];
-                            f.z *= fb[e];
-                            f.w *= fb[e];
-                        }
-                        fma2(sum[c + q], sum[c + q + 1], __uint_as_float(r[q]), __uint_as_float(r[q + 1]), f.x, f.y);
-                        fma2(sum[c + q + 2], sum[c + q + 3], __uint_as_float(r[q + 2]), __uint_as_float(r[q + 3]), f.z, f.w);
+                    for (int q = 0; q < L::kChunk / 2; q += 2) {
+                        float* s = sum + c * (L::kChunk / 2) + q;
+                        const Pair x = pair_of(r[c & 1][q], r[c & 1][q + 1]);
+                        if constexpr (SQUARE)
+                            fma2(s[0], s[1], x, f[q / 4]);
+                        else
+                            fma2(s[0], s[1], mul2(x, f[q / 4]), fb[2 * (c & 1) + (q >> 1 & 1)]);
                     }
                 }
             }
@@ -285,8 +307,11 @@ __global__ void __launch_bounds__(Layout<NP>::kThreads, 1) block_swapped_kernel(
     float* red = reinterpret_cast<float*>(smem);
     if (warp < L::kSumWarps) {
 #pragma unroll
-        for (int i = 0; i < L::kOwn; ++i)
-            red[((warp >> 2) * L::kOwn + i) * kRowsB + (warp & 3) * 32 + lane] = sum[i];
+        for (int i = 0; i < L::kOwn; ++i) {
+            const int c = i / (L::kChunk / 2), e = i % (L::kChunk / 2);  // the load, its value (see load_values)
+            const int row = (warp >> 2) * L::kOwn + (c >> 1) * L::kChunk + (e >> 2) * 8 + 2 * (lane & 3) + (e & 1);
+            red[row * kRedRow + (warp & 3) * 32 + (c & 1) * 16 + (e >> 1 & 1) * 8 + (lane >> 2)] = sum[i];
+        }
     }
     if (split > 1)
         cluster_sync_all();
@@ -303,10 +328,10 @@ __global__ void __launch_bounds__(Layout<NP>::kThreads, 1) block_swapped_kernel(
     for (int r = static_cast<int>(threadIdx.x) / (kRowsB / 2) + rank * kRowsAtOnce; r < rows; r += split * kRowsAtOnce) {
         float2 v = make_float2(0.0f, 0.0f);
         if (split == 1) {
-            v = *reinterpret_cast<const float2*>(red + r * kRowsB + c2);
+            v = *reinterpret_cast<const float2*>(red + r * kRedRow + c2);
         } else {
             for (int q = 0; q < split; ++q) {
-                const float2 w = ld_shared_cluster_f32x2(map_shared_rank(sbase + (r * kRowsB + c2) * 4, q));
+                const float2 w = ld_shared_cluster_f32x2(map_shared_rank(sbase + (r * kRedRow + c2) * 4, q));
                 v.x += w.x;
                 v.y += w.y;
             }
@@ -340,12 +365,16 @@ template <int NP, bool SQUARE>
 cudaError_t launch_one(const GemmParams& p, int grid, cudaStream_t stream, bool pdl, bool prepare)
 {
     auto kernel = block_swapped_kernel<NP, SQUARE>;
-    if (prepare)
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<NP>::kBytes);
+    if (prepare) {
+        constexpr int most = Layout<NP, SQUARE>::kBytes > kAloneSmem ? Layout<NP, SQUARE>::kBytes : kAloneSmem;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        return e != cudaSuccess ? e
+                                : cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(Layout<NP>::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Layout<NP>::kBytes;
+    cfg.blockDim = dim3(Layout<NP, SQUARE>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Layout<NP, SQUARE>::kBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -357,6 +386,28 @@ cudaError_t launch_one(const GemmParams& p, int grid, cudaStream_t stream, bool 
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// Clusters of `split` blocks that the GPU holds at once, kPerSm blocks an SM: what it holds with one an SM (asked for
+// with shared memory that makes it so; the answer for two is one's too), times kPerSm.
+template <int NP>
+int max_clusters(int split)
+{
+    auto kernel = block_swapped_kernel<NP, true>;
+    if (launch_one<NP, true>(GemmParams{}, 0, nullptr, false, true) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(split), 1, 1);
+    cfg.blockDim = dim3(Layout<NP, true>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kAloneSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n * Layout<NP, true>::kPerSm : 0;
 }
 
 template <bool SQUARE>
@@ -373,6 +424,22 @@ cudaError_t launch_np(int np, const GemmParams& p, int grid, cudaStream_t stream
 
 }  // namespace
 
+// (Asked for once a process: its devices are taken to be the same GPU model, as elsewhere in the planner.)
+int block_swapped_max_clusters(int np, int split)
+{
+    static std::atomic<int> known[4][9];  // (0: not asked yet; else the answer + 1)
+    std::atomic<int>& at = known[np == 16 ? 0 : np == 32 ? 1 : np == 64 ? 2 : 3][split];
+    int v = at.load(std::memory_order_relaxed);
+    if (v == 0) {
+        v = 1 + (np == 16   ? max_clusters<16>(split)
+                 : np == 32 ? max_clusters<32>(split)
+                 : np == 64 ? max_clusters<64>(split)
+                            : max_clusters<128>(split));
+        at.store(v, std::memory_order_relaxed);
+    }
+    return v - 1;
+}
+
 cudaError_t block_swapped(int np, bool square, const GemmParams& p, int grid, cudaStream_t stream, bool pdl, bool prepare)
 {
     return square ? launch_np<true>(np, p, grid, stream, pdl, prepare) : launch_np<false>(np, p, grid, stream, pdl, prepare);
@@ -380,12 +447,12 @@ cudaError_t block_swapped(int np, bool square, const GemmParams& p, int grid, cu
 
 int block_swapped_smem(int np)
 {
-    return np == 16 ? Layout<16>::kBytes : np == 32 ? Layout<32>::kBytes : np == 64 ? Layout<64>::kBytes : Layout<128>::kBytes;
+    return np == 16 ? Layout<16, true>::kBytes : np == 32 ? Layout<32, true>::kBytes : np == 64 ? Layout<64, true>::kBytes : Layout<128, true>::kBytes;
 }
 
 int block_swapped_stages(int np)
 {
-    return np == 16 ? Layout<16>::kStages : np == 32 ? Layout<32>::kStages : np == 64 ? Layout<64>::kStages : Layout<128>::kStages;
+    return np == 16 ? Layout<16, true>::kStages : np == 32 ? Layout<32, true>::kStages : np == 64 ? Layout<64, true>::kStages : Layout<128, true>::kStages;
 }
 
 }  // namespace gemm_epi

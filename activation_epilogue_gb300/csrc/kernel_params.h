@@ -224,6 +224,7 @@ int block_pair_stages();
 cudaError_t block_swapped(int np, bool square, const GemmParams& p, int grid, cudaStream_t stream, bool pdl, bool prepare);
 int block_swapped_smem(int np);
 int block_swapped_stages(int np);
+int block_swapped_max_clusters(int np, int split);
 
 // The FFN block in one CTA-pair launch (256 x 256 tiles); never a programmatic dependent.
 cudaError_t ffn_pair_prepare();
