@@ -4,6 +4,8 @@
 
 #include <cstdint>
 
+#include "gelu.cuh"
+
 namespace gemm_epi {
 
 // Start loading values of this warp's accumulator lanes, valid after tmem_wait on them: 16 columns of each thread's
@@ -82,6 +84,51 @@ __device__ __forceinline__ Pair ld_shared_pair(uint32_t addr)
     Pair v;
     asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
     return v;
+}
+
+__device__ __forceinline__ Pair pair_of(float a, float b) { return pair_of(__float_as_uint(a), __float_as_uint(b)); }
+
+__device__ __forceinline__ float2 unpair(Pair p)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+
+// GELU of four values by gelu_erf_fast's formula, x / (1 + 2^(x p(x^2))), with one reciprocal for the four
+// denominators (1 / a0 = a1 a2 a3 / (a0 a1 a2 a3)): the special-function unit, sixteen lanes' work a cycle, is what a
+// tile's GELU takes (two operations a value 2.2 us of 256 x 256, 1.25 so).  The exponents stop at 30, where the
+// product of four denominators still fits fp32 and a NaN does not reach its neighbours; below -8 the result is 0
+// (within 5e-15 of it).
+__device__ __forceinline__ void gelu4(float* v)
+{
+    const Pair k1 = pair_of(-2.3014667034f, -2.3014667034f), k3 = pair_of(-0.10654459149f, -0.10654459149f);
+    const Pair k5 = pair_of(0.00098442099988f, 0.00098442099988f), one = pair_of(1.0f, 1.0f);
+    Pair x[2];
+    float2 a[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x[i] = pair_of(v[2 * i], v[2 * i + 1]);
+        const float2 s = unpair(mul2(x[i], x[i]));
+        const Pair s2 = pair_of(fminf(s.x, 64.0f), fminf(s.y, 64.0f));
+        Pair p, q, d;
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(s2), "l"(k5), "l"(k3));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(s2), "l"(q), "l"(k1));
+        const float2 u = unpair(mul2(x[i], p));
+        const Pair e = pair_of(exp2_approx(fminf(u.x, 30.0f)), exp2_approx(fminf(u.y, 30.0f)));
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(e), "l"(one));
+        a[i] = unpair(d);
+    }
+    const float ab = a[0].x * a[0].y, cd = a[1].x * a[1].y;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ab * cd));
+    const float over[2] = {r * cd, r * ab};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 y = unpair(mul2(x[i], mul2(pair_of(a[i].y, a[i].x), pair_of(over[i], over[i]))));
+        v[2 * i] = v[2 * i] < -8.0f ? 0.0f : y.x;
+        v[2 * i + 1] = v[2 * i + 1] < -8.0f ? 0.0f : y.y;
+    }
 }
 
 }  // namespace gemm_epi

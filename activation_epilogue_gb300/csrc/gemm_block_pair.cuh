@@ -280,6 +280,17 @@ __device__ __forceinline__ void stage_scales(const GemmParams& p, uint8_t* smem,
     }
 }
 
+template <int N, int EPI>
+__device__ __forceinline__ void activate_block(float (&v)[N])
+{
+    if constexpr (EPI == EPI_GELU_BIAS) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) gelu4(v + i);
+    } else {
+        activate(v, EPI);
+    }
+}
+
 // The place of a thread's sums: with SQUARE sum[e] is column e of its lane's row; otherwise sum
 // 32 b + 16 a + 4 i + 2 u + v is row lane / 4 + 16 a + 8 u, column 32 b + 8 i + 2 (lane % 4) + v.
 
@@ -307,7 +318,7 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
             for (int e = 0; e < 32; ++e) word |= (v[e] > 0.0f && at + e < p.n) ? (1u << e) : 0u;
             if (row < p.m) static_cast<uint32_t*>(p.aux)[static_cast<long long>(row) * p.aux_ld + at / 32] = word;
         }
-        activate(v, EPI);
+        activate_block<32, EPI>(v);
         const uint16_t* R = static_cast<const uint16_t*>(p.residual) + static_cast<long long>(row) * p.n + at;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -347,7 +358,7 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
                 word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
                 if (c2 == 0 && row < p.m) static_cast<uint32_t*>(p.aux)[static_cast<long long>(row) * p.aux_ld + at / 32] = word;
             }
-            activate(v, EPI);
+            activate_block<8, EPI>(v);
             const uint16_t* R = static_cast<const uint16_t*>(p.residual) + static_cast<long long>(row) * p.n + at + c2;
             const int r32 = lane / 4 + 8 * q;
 #pragma unroll
