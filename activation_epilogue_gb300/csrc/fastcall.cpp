@@ -1,5 +1,6 @@
 // The binding's argument marshalling in C++ for the calls a model makes for every token (the
-// norms, the 4-bit and block-scaled E4M3 products, dropout): torch tensors to addresses, then the C ABI call.  It does
+// norms, the 4-bit and block-scaled E4M3 products, dropout): torch tensors to addresses, then the C ABI
+// call.  It does
 // what the ctypes path of gemm_epi.py does, with the same checks (device, layout, and type and size
 // against the call's shape), and stands in for it where the headers of Python and torch were there
 // at build time.  Host time of a six-tensor call (GB300's
@@ -272,7 +273,7 @@ PyObject* dropout(PyObject*, PyObject* const* args, Py_ssize_t n)
     });
 }
 
-int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to; }
+int64_t up(int64_t v, int64_t to) { return v / to + (v % to > 0); }
 
 PyObject* layernorm_forward(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
@@ -298,7 +299,8 @@ PyObject* layernorm_e4m3(PyObject*, PyObject* const* args, Py_ssize_t n)
         void* beta = a.pointer(6, k16, row);
         const float eps = a.real(7);
         void *H = a.pointer(8, k16, td), *Q = a.pointer(9, Kind::kE4m3, td);
-        void *scale = a.pointer(10, Kind::kF32, d > 0 ? times(t, up(d, 128)) : 0), *stats = a.pointer(11, Kind::kF32, times(t, 2));
+        void* scale = a.pointer(10, Kind::kF32, d > 0 ? times(t, up(d, 128)) : 0);
+        void* stats = a.pointer(11, Kind::kF32, times(t, 2));
         const cudaStream_t stream = a.stream(12);
         return unlocked(a, p_layernorm_e4m3, t, d, dtype_of(dtype), X, R, gamma, beta, eps, H, Q,
                         static_cast<float*>(scale), static_cast<float*>(stats), stream);

@@ -210,3 +210,13 @@ def test_both_marshalling_paths_agree():
         for calls in (fast, slow):
             with pytest.raises((ValueError, TypeError, AttributeError)):
                 calls.e4m3_quantize(4, 64, 1, 0, bad, q[1], q[2], None, None, 0)
+
+
+def test_widths_next_to_the_largest_integer():
+    q = [i * 16 << 20 for i in range(1, 8)]
+    for calls in (gemm_epi._bind_calls(), gemm_epi._CtypesCalls(gemm_epi.load_library())):
+        for d in (2 ** 63 - 8, 2 ** 63 - 128):
+            assert calls.layernorm_e4m3(4, d, 1, q[0], None, q[1], q[2], 1e-5, None, q[3], q[4], None, 0) == SHAPE
+            assert calls.layernorm_forward(4, d, 1, q[0], None, q[1], q[2], 1e-5, None, q[3], None, 0) == SHAPE
+            assert calls.e4m3_quantize(4, d, 1, 0, q[0], q[1], q[2], q[3], q[4], 0) == SHAPE
+            assert calls.e4m3_quantize(d, 16, 1, 0, q[0], q[1], q[2], q[3], q[4], 0) == SHAPE
