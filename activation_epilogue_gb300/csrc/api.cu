@@ -305,7 +305,12 @@ gemm_epi_status ensure_split_ws(gemm_epi_plan_s* p)
 }
 
 // E4M3 with scales for blocks of 128 of k: CTA pairs on 256 x 256 tiles, or, for few rows of A, tiles of
-// 128 columns by up to 128 rows with K split over a cluster.
+// 128 columns by up to 128 rows with K split over a cluster.  The latter as long as its tiles of 128 x 128
+// are there at once, one an SM (and up to 128 rows, where a pair's tile would be half empty): its one wave
+// is then as quick as the pairs', a second one is not.  Measured (n x k, few rows / pairs, GELU, us):
+// 4096 x 4096 with 128 rows 10.6 / 19.7, 256 15.3 / 19.9, 512 20.4 / 20.1, 768 39.8 / 20.6;
+// 8192 x 8192 with 128 21.6 / 32.8, 256 32.4 / 32.9, 384 63 / 33.6; 4096 x 1024 with 256 10.8 / 10.4;
+// 1024 x 4096 with 1024 15.1 / 19.6, 2039 20.2 / 19.9; 16384 x 4096 with 128 21.5 / 21.3, 192 40 / 21.3.
 gemm_epi_status configure_blocks(gemm_epi_plan_s* p)
 {
     const bool square = p->scale_blocks == GEMM_EPI_SCALE_BLOCKS_SQUARE;

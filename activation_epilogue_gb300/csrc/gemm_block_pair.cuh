@@ -8,17 +8,23 @@
 // The tensor cores cannot apply such scales to a sum that they keep, so the sum of each block of
 // 128 k is a sum of its own: the MMA warp starts every K block with cleared accumulators and hands
 // them over, and the summing warps read them, multiply them by their scales and add them to the
-// tile's sums in fp32 registers.  What bounds it is this hand-over and the additions, not the MMAs
-// (256 x 256 x 128 take 590 cycles on the pair):
+// tile's sums in fp32 registers.  What bounds it is this hand-over and the additions, not the MMAs:
+// 256 x 256 x 128 take 584 cycles on the pair, the sums of a block about 860 (SQUARE) and 1300.
 //   * Four accumulators of 128 columns, half a tile each: a half's MMAs run while the three before
-//     it are read, so that no MMA waits for a round trip through barriers.
-//   * Eight summing warps (a lane quarter, half the tile's columns each), 128 sums a thread; sixteen values
-//     are on their way from tensor memory while the sixteen before them are added, two an instruction.  Sixteen warps of 64 sums leave too few registers for the
-//     addresses, which are then formed again in every block (1099 us for 16384 x 8192 x 8192, 835 so).
+//     it are read, so that no MMA waits for a round trip through barriers (one accumulator for a
+//     whole tile, two in turn: 1977 us for 16384 x 8192 x 8192, 850 so, with what follows).
+//   * Eight summing warps (a lane quarter, half the tile's columns each), 128 sums a thread; sixteen
+//     values are on their way from tensor memory while the sixteen before them are added, two an
+//     instruction.  Sixteen warps of 64 sums, sixteen values at a time, take as long (858 us): their
+//     registers do not hold a second load's values, and waits and barriers are twice as many.
 //   * SQUARE: a warp's columns share one scale, a thread (a row) has one factor a block.  Otherwise
-//     every column has its own, and a thread's values are loaded as four rows of 32 columns, so that 32
-//     scales a block come from shared memory for them and not 128 (whose 1024 cycles a block would bound it).
+//     every column has its own, and a thread's values are loaded as four rows of 32 columns, so that
+//     32 scales a block come from shared memory for them and not 128 (whose 1024 cycles a block
+//     would bound it); the loads of this shape are the slower ones, and each value takes a product
+//     before its addition (1170 us).
 //   * One warp brings the scales of all blocks into a ring in shared memory, ahead of the sums.
+// 16384 x 8192 x 8192: 850 us, 2.59 PFLOP/s (1170, 1.88 with a scale for each row of B); its MMAs
+// alone would take 590.
 #pragma once
 
 #include "block_sums.cuh"
@@ -40,8 +46,8 @@ constexpr int kBlockThreads = 128 + 32 * kSumWarps;
 constexpr int kIssueRegs = 72, kSumRegs = 216;
 static_assert(128 * kIssueRegs + 32 * kSumWarps * kSumRegs <= kBlockThreads * 168,
               "a split of the registers that the block starts with");
-// Blocks of scales on their way: 128 rows of A and, SQUARE, the factors of the tile's two halves (a row's scale times the
-// block's of B), otherwise the rows' scales and those of 256 columns.
+// Blocks of scales on their way: SQUARE, the rows' factors for the tile's two halves (a row's scale times
+// the block's of B); otherwise the rows' scales and those of 256 columns.
 constexpr int kGroup = 4;                     // K blocks of scales that are handed over together
 constexpr int kScaleGroups = 2;
 constexpr int kScaleFloats = 3 * 128;
@@ -56,7 +62,8 @@ constexpr int kBarAccFull = kBarTmemFull;     // [4], in place of the one-scale 
 constexpr int kBarAccEmpty = 44;              // [4], behind the tile indices
 constexpr int kBarScaleFull = 48;             // [2]
 constexpr int kBarScaleEmpty = kBarScaleFull + kScaleGroups;
-static_assert(kBarAccFull + 4 == kBarStall && kOffSchedSlot + 4 * kSchedSlots <= kBarAccEmpty * 8 && (kBarScaleEmpty + kScaleGroups) * 8 <= C::kBarBytes,
+static_assert(kBarAccFull + 4 == kBarStall && kOffSchedSlot + 4 * kSchedSlots <= kBarAccEmpty * 8 &&
+                  (kBarScaleEmpty + kScaleGroups) * 8 <= C::kBarBytes,
               "barrier area");
 
 // True in one lane of a converged warp.
@@ -141,8 +148,8 @@ __device__ __forceinline__ void copy_operands(const GemmParams& p, uint32_t sbas
 
 // Arrive on an mbarrier of the even CTA (a shared::cluster address).  What it orders are this warp's reads
 // of tensor memory, which the tcgen05 fences around the barrier order; a release at cluster scope would
-// wait for the warp's loads and stores of memory as well, a microsecond in every K block (16384 x 8192 x
-// 8192: 1980 us with it, 1012 so).
+// wait for the warp's loads and stores of memory as well, a microsecond in every K block (before the later
+// steps 1980 us for 16384 x 8192 x 8192 with it, 1012 so).
 __device__ __forceinline__ void arrive_pair(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -311,7 +318,8 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = sum[e];
-        if constexpr (kBias) add_bias<32>(v, bias, along_cols, !along_cols && row < p.m ? load_16bit(p.bias, row, 1) : 0.0f);
+        if constexpr (kBias)
+            add_bias<32>(v, bias, along_cols, !along_cols && row < p.m ? load_16bit(p.bias, row, 1) : 0.0f);
         if constexpr (EPI == EPI_RELU_AUX_BIAS) {
             uint32_t word = 0;
 #pragma unroll
@@ -344,7 +352,8 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
             float v[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 b = kBias && along_cols ? *reinterpret_cast<const float2*>(bias + 8 * i + c2) : make_float2(lb, lb);
+                const float2 b =
+                    kBias && along_cols ? *reinterpret_cast<const float2*>(bias + 8 * i + c2) : make_float2(lb, lb);
                 v[2 * i] = sum[16 * (q >> 1) + 4 * i + 2 * (q & 1)] + b.x;
                 v[2 * i + 1] = sum[16 * (q >> 1) + 4 * i + 2 * (q & 1) + 1] + b.y;
             }
@@ -356,7 +365,8 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
                         word |= ((v[2 * i] > 0.0f ? 1u : 0u) | (v[2 * i + 1] > 0.0f ? 2u : 0u)) << (8 * i + c2);
                 word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
                 word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
-                if (c2 == 0 && row < p.m) static_cast<uint32_t*>(p.aux)[static_cast<long long>(row) * p.aux_ld + at / 32] = word;
+                if (c2 == 0 && row < p.m)
+                    static_cast<uint32_t*>(p.aux)[static_cast<long long>(row) * p.aux_ld + at / 32] = word;
             }
             activate_block<8, EPI>(v);
             const uint16_t* R = static_cast<const uint16_t*>(p.residual) + static_cast<long long>(row) * p.n + at + c2;
@@ -408,7 +418,8 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
     };
     // block `b`'s MMAs are done
     auto ready = [&](uint32_t b) {
-        const bool ok = warp_wait(bar0 + 8u * (kBarAccFull + 2 * (b & 1u) + half), (b >> 1) & 1u, abort_flag, p.wait_limit_ns);
+        const bool ok =
+            warp_wait(bar0 + 8u * (kBarAccFull + 2 * (b & 1u) + half), (b >> 1) & 1u, abort_flag, p.wait_limit_ns);
         tcgen05_fence_after_sync();
         return ok || failed();
     };
@@ -464,8 +475,9 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
         float sum[kCols];
 #pragma unroll
         for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
-        // Sixteen values are on their way while those before them are added.  (The next block's first ones ahead of
-        // this one's end, and sums held as pairs, cost copies of registers: 941 and 860 us for 16384 x 8192 x 8192, 827 so.)
+        // Sixteen values are on their way while those before them are added.  (The next block's first ones ahead
+        // of this one's end, and sums held as pairs, cost copies of registers: 941 and 860 us for 16384 x 8192 x
+        // 8192 in runs where this took 827 to 850.)
         uint32_t r[2][16];
         auto load = [&](uint32_t b, int c) {  // SQUARE: columns 16 c on; otherwise columns 32 (c / 2) on, lanes 16 (c % 2) on
             if constexpr (SQUARE)

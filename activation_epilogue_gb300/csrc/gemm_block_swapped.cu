@@ -8,9 +8,13 @@
 // at a time in shared memory (times the scale of B's block, which the whole tile shares, with
 // SQUARE; otherwise with the scales of B's rows), and a thread's values are loaded as four lanes of
 // a quarter of the rows of A, so that it reads a quarter of their scales (all of them, by every lane,
-// took 256 cycles of shared memory a K block of 64 rows, as many as the copies).  K may be split over the blocks of a cluster, which add their sums
-// in rank order through distributed shared memory, each for every cluster-th row, so that the
-// result does not depend on timing.  A block is bound by the copies of its 16 KB of B a K block.
+// took 256 cycles of shared memory a K block of 64 rows, as many as the copies).  K may be split over
+// the blocks of a cluster, which add their sums in rank order through distributed shared memory, each
+// for every cluster-th row, so that the result does not depend on timing.
+//
+// Bound by B's bytes: one row of 16384 x 8192 (n x k) takes 24.2 us, 134 MB at 5.5 TB/s (28.8 with one
+// block an SM), 48 rows of 8192 x 16384 26.9 us (29.6); launch, first copies and the last sums are the
+// four microseconds that a copy of these bytes does not have.
 #include "block_sums.cuh"
 #include "gemm_kernel.cuh"
 #include "launch.h"
@@ -83,11 +87,13 @@ __device__ __forceinline__ void load_values(uint32_t taddr, uint32_t (&r)[8]) { 
 __device__ __forceinline__ float apply(float v, int epilog)
 {
     if (epilog == EPI_RELU_BIAS || epilog == EPI_RELU_AUX_BIAS) return v > 0.0f ? v : 0.0f;
-    return epilog == EPI_GELU_BIAS ? gelu_erf_fast(v) : v;
+    // (0 below -8, as with gelu4: an infinity's too)
+    return epilog == EPI_GELU_BIAS ? (v < -8.0f ? 0.0f : gelu_erf_fast(v)) : v;
 }
 
 template <int NP, bool SQUARE>
-__global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUARE>::kPerSm) block_swapped_kernel(const __grid_constant__ GemmParams p)
+__global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUARE>::kPerSm)
+    block_swapped_kernel(const __grid_constant__ GemmParams p)
 {
     using L = Layout<NP, SQUARE>;
     extern __shared__ uint8_t smem_raw[];
@@ -236,7 +242,8 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
             for (int e = 0; e < L::kStaged; ++e) st_shared_f32(mine + 4 * (threadIdx.x + e * L::kSumThreads), next[e]);
             if (!SQUARE && threadIdx.x < kRowsB) {
 #pragma unroll
-                for (int e = 0; e < kGroup; ++e) st_shared_f32(mine + kGroup * NP * 4 + 4 * (e * kRowsB + threadIdx.x), next_b[e]);
+                for (int e = 0; e < kGroup; ++e)
+                    st_shared_f32(mine + kGroup * NP * 4 + 4 * (e * kRowsB + threadIdx.x), next_b[e]);
             }
             // (a buffer is written again two groups on: by then every thread has passed the barrier between)
             named_barrier_sync(1, L::kSumThreads);
@@ -259,7 +266,8 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
                 if constexpr (!SQUARE) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint32_t v = ld_shared_u32(mine + (kGroup * NP + e * kRowsB + quarter * 32 + 8 * j + (lane >> 2)) * 4);
+                        const int at = kGroup * NP + e * kRowsB + quarter * 32 + 8 * j + (lane >> 2);
+                        const uint32_t v = ld_shared_u32(mine + at * 4);
                         fb[j] = pair_of(v, v);
                     }
                 }
@@ -368,8 +376,9 @@ cudaError_t launch_one(const GemmParams& p, int grid, cudaStream_t stream, bool 
     if (prepare) {
         constexpr int most = Layout<NP, SQUARE>::kBytes > kAloneSmem ? Layout<NP, SQUARE>::kBytes : kAloneSmem;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        return e != cudaSuccess ? e
-                                : cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess) return e;
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxShared);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -447,12 +456,18 @@ cudaError_t block_swapped(int np, bool square, const GemmParams& p, int grid, cu
 
 int block_swapped_smem(int np)
 {
-    return np == 16 ? Layout<16, true>::kBytes : np == 32 ? Layout<32, true>::kBytes : np == 64 ? Layout<64, true>::kBytes : Layout<128, true>::kBytes;
+    return np == 16   ? Layout<16, true>::kBytes
+           : np == 32 ? Layout<32, true>::kBytes
+           : np == 64 ? Layout<64, true>::kBytes
+                      : Layout<128, true>::kBytes;
 }
 
 int block_swapped_stages(int np)
 {
-    return np == 16 ? Layout<16, true>::kStages : np == 32 ? Layout<32, true>::kStages : np == 64 ? Layout<64, true>::kStages : Layout<128, true>::kStages;
+    return np == 16   ? Layout<16, true>::kStages
+           : np == 32 ? Layout<32, true>::kStages
+           : np == 64 ? Layout<64, true>::kStages
+                      : Layout<128, true>::kStages;
 }
 
 }  // namespace gemm_epi

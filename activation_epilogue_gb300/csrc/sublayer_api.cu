@@ -1,5 +1,6 @@
 // C ABI calls for what stands around a feed-forward block's GEMMs: the RMS norm, LayerNorm for
-// training, E4M3 codes with block scales, the products with 4-bit weights and dropout.  Argument checks and launches; nothing is kept between calls.
+// training, E4M3 codes with block scales, the products with 4-bit weights and dropout.  Argument checks
+// and launches; nothing is kept between calls.
 #include <atomic>
 #include <cmath>
 

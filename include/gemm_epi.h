@@ -144,7 +144,7 @@ typedef enum {
                                        (m <= 64, forward epilogs, a K slab per CTA that
                                        fits in shared memory; SPLIT_K sets its slices,
                                        TILE_N its rows of D: 16, 32 or 64); E4M3 plans
-                                       take 0 or 3 */
+                                       take 0 or 3, with SCALE_BLOCKS 2 as well */
     GEMM_EPI_OPT_TILE_N = 1,        /* N tile: 64, 128 or 256 for the row-tile kernel;
                                        224 or 256 for the CTA-pair kernel; 16, 32, 64, 128
                                        or 256 rows of D for the swapped kernel (a width
@@ -222,11 +222,12 @@ typedef enum {
  * scale_a: K rows of m fp32.  scale_b: K rows of ceil(n / 128) fp32 and j' = j / 128 (SQUARE), or K rows
  * of n and j' = j (ROWS; 16-byte aligned): what gemm_epi_e4m3_quantize and gemm_epi_layernorm_e4m3
  * write.  Each block's sum is an fp32 sum of its own; the blocks' sums times their scales are added in
- * fp32 in the order of k (with SPLIT_K in order within a slice, then the slices'), the same in every
+ * fp32 in the order of k (where K is split, in order within a slice, then the slices'), the same in every
  * call.  The product of two scales is formed in fp32 and has to be finite in it.  Epilogs as for the
- * other E4M3 plans, both bias layouts.  VARIANT is 0 (automatic), 3 (CTA pairs, TILE_N 256) or 2 (few
- * rows of A: TILE_N 16, 32, 64 or 128 rows of D, SPLIT_K slices over a cluster); B_READY and the wait
- * limit hold for the latter as for the swapped kernel. */
+ * other E4M3 plans, both bias layouts; D may be the residual itself, any other overlap of D or aux with
+ * an operand is ERR_INVALID_ARG.  VARIANT is 0 (automatic), 3 (CTA pairs, TILE_N 256) or 2 (few rows of
+ * A: TILE_N 16, 32, 64 or 128 rows of D; SPLIT_K slices, 1..8, over a cluster, or 0: as many as fit;
+ * SPLIT_MODE is ignored); B_READY and the wait limit hold for the latter as for the swapped kernel. */
 typedef enum {
     GEMM_EPI_SCALE_BLOCKS_SQUARE = 1, /* B (n x k, transposed) in blocks of 128 x 128 */
     GEMM_EPI_SCALE_BLOCKS_ROWS = 2    /* B in blocks of 1 x 128: a scale for each row */
@@ -451,8 +452,8 @@ gemm_epi_status gemm_epi_layernorm_forward(int64_t t, int64_t d, gemm_epi_dtype 
 
 /* The same norm with Y in E4M3, a scale for each 128 columns of a row: the A and scale_a of a plan with
  * GEMM_EPI_OPT_SCALE_BLOCKS.  scale: ceil(d / 128) rows of t fp32, 4-byte aligned, written:
- * scale[b][i] = max |Y_ij| / 448 over columns j of block b; Q_ij = Y_ij * (1 / scale), Y (not rounded to
- * 16 bits) and the reciprocal in fp32, rounded as by gemm_epi_e4m3_quantize.  Q: t x d bytes, 16-byte
+ * scale[b][i] = max |Y_ij| / 448 over columns j of block b; Q_ij = Y_ij * (1 / scale), Y not rounded to
+ * 16 bits, the reciprocal and the rounding as in gemm_epi_e4m3_quantize.  Q: t x d bytes, 16-byte
  * aligned, overlapping nothing else. */
 gemm_epi_status gemm_epi_layernorm_e4m3(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* X,
                                         const void* residual, const void* gamma, const void* beta,
@@ -481,8 +482,9 @@ int64_t gemm_epi_layernorm_workspace(int64_t t, int64_t d);
 /* ---- E4M3 with block scales ---------------------------------------------------------------
  * Quantise a 16-bit matrix for plans with GEMM_EPI_OPT_SCALE_BLOCKS:
  *     scale = max |x| / 448 over each block of X,   code = x * (1 / scale),
- * the reciprocal and the product in fp32, the product rounded to the nearest E4M3 value, ties to even,
- * saturated at +-448 (next to a halfway point the quotient itself may round to the neighbouring code).
+ * the scale rounded to fp32, the reciprocal within 2^-23 of its value, the product in fp32 and rounded to
+ * the nearest E4M3 value, ties to even, saturated at +-448 (next to a halfway point the quotient itself
+ * may round to the neighbouring code).
  * X: rows x cols of `dtype` (F16 or BF16), cols a multiple of 16, 16 to 2^30.
  *   Q, scale      (or both NULL) the codes row-major, rows x cols; scale: ceil(cols / 128) rows of
  *                 `rows` fp32 (BLOCK_1X128: scale[b][i] of columns 128 b ... of row i) or of
