@@ -52,6 +52,15 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[N])
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// ... and for two of them.
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[2][N])
+{
+    tmem_wait(r[0]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[1][i]));
+}
+
 // Pairs of fp32 in 64-bit registers: two additions an instruction.
 using Pair = unsigned long long;
 

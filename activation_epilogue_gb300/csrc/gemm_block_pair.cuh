@@ -13,10 +13,10 @@
 //   * Four accumulators of 128 columns, half a tile each: a half's MMAs run while the three before
 //     it are read, so that no MMA waits for a round trip through barriers (one accumulator for a
 //     whole tile, two in turn: 1977 us for 16384 x 8192 x 8192, 850 so, with what follows).
-//   * Eight summing warps (a lane quarter, half the tile's columns each), 128 sums a thread; sixteen
-//     values are on their way from tensor memory while the sixteen before them are added, two an
-//     instruction.  Sixteen warps of 64 sums, sixteen values at a time, take as long (858 us): their
-//     registers do not hold a second load's values, and waits and barriers are twice as many.
+//   * Eight summing warps (a lane quarter, half the tile's columns each), 128 sums a thread, two added
+//     an instruction.  A block is one chain of steps for each warp: its accumulators' barrier, four
+//     loads of 32 columns, the arrival that frees them.  What is in that chain counts, not the
+//     instructions: barriers tested ahead of their use, addresses that need no arithmetic.
 //   * SQUARE: a warp's columns share one scale, a thread (a row) has one factor a block.  Otherwise
 //     every column has its own, and a thread's values are loaded as four rows of 32 columns, so that
 //     32 scales a block come from shared memory for them and not 128 (whose 1024 cycles a block
@@ -43,7 +43,7 @@ constexpr int kStageBytes = C::kStageBytes;
 // given out by warpgroup, and the sums need more than an even share of the block's 384 x 168.
 constexpr int kSumWarps = 8;
 constexpr int kBlockThreads = 128 + 32 * kSumWarps;
-constexpr int kIssueRegs = 72, kSumRegs = 216;
+constexpr int kIssueRegs = 88, kSumRegs = 208;
 static_assert(128 * kIssueRegs + 32 * kSumWarps * kSumRegs <= kBlockThreads * 168,
               "a split of the registers that the block starts with");
 // Blocks of scales on their way: SQUARE, the rows' factors for the tile's two halves (a row's scale times
@@ -62,8 +62,9 @@ constexpr int kBarAccFull = kBarTmemFull;     // [4], in place of the one-scale 
 constexpr int kBarAccEmpty = 44;              // [4], behind the tile indices
 constexpr int kBarScaleFull = 48;             // [2]
 constexpr int kBarScaleEmpty = kBarScaleFull + kScaleGroups;
+constexpr int kBarDrain2 = kBarScaleEmpty + kScaleGroups;  // (the second issuing warp's kBarDrain)
 static_assert(kBarAccFull + 4 == kBarStall && kOffSchedSlot + 4 * kSchedSlots <= kBarAccEmpty * 8 &&
-                  (kBarScaleEmpty + kScaleGroups) * 8 <= C::kBarBytes,
+                  (kBarDrain2 + 1) * 8 <= C::kBarBytes,
               "barrier area");
 
 // True in one lane of a converged warp.
@@ -78,6 +79,20 @@ __device__ __forceinline__ bool elect_one()
     return one != 0;
 }
 
+// Whether a barrier's phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // A whole warp's wait (it gives up as one: what follows is for all of its lanes): one try in line, the loop out of
 // the way (a loop of tries in its place took 1040 us for 16384 x 8192 x 8192 instead of 885).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag,
@@ -85,6 +100,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
 {
     if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, limit_ns));
+}
+
+// The pair's tile j (j >= 1), for a whole warp: in the static order everyone knows it (handed over like the other
+// order's, by writes and reads ordered over the cluster, it kept the copies and the sums waiting: 4096 x 8192 x 2064
+// 81.5 us, 70.5 so); otherwise the even CTA's producer says it, as in the one-scale kernel.
+__device__ __forceinline__ bool next_tile(const GemmParams& p, const WorkRange& w, uint32_t bar0, int j, int& tile,
+                                          const volatile int* abort_flag)
+{
+    if (p.sched != nullptr) return sched_take_warp(bar0, j, tile, abort_flag, p.wait_limit_ns);
+    const long long at = static_cast<long long>(tile) + w.stride;
+    tile = at < w.end ? static_cast<int>(at) : w.end;
+    return true;
 }
 
 // One thread of each CTA: the K blocks of every tile into the ring of stages, the even CTA's barriers
@@ -95,7 +122,7 @@ __device__ __forceinline__ void copy_operands(const GemmParams& p, uint32_t sbas
 {
     const WorkRange w = work_range<true>(p);
     const uint32_t rank = static_cast<uint32_t>(w.pair_rank);
-    const bool even = rank == 0, dyn = even && p.sched != nullptr;
+    const bool even = rank == 0, dyn = p.sched != nullptr;
     const uint32_t full0 = map_shared_rank(bar0 + 8u * kBarFull, cluster_ctarank() & ~1u);
     int stage = 0;
     uint32_t phase = 0;
@@ -105,13 +132,14 @@ __device__ __forceinline__ void copy_operands(const GemmParams& p, uint32_t sbas
     grid_dependency_wait();
     for (int j = 0; ok; ++j) {
         if (j > 0) {
-            if (even)
+            if (even || !dyn)
                 tile = next;
             else if (!sched_take(bar0, j, tile, abort_flag, p.wait_limit_ns))
                 ok = false;
         }
         if (!ok || tile >= w.end) break;
-        const unsigned ticket = dyn ? atomicAdd(p.sched, 1u) : 0u;  // (needed a few K blocks later)
+        const unsigned ticket = even && dyn ? atomicAdd(p.sched, 1u) : 0u;  // (needed a few K blocks later)
+        if (!dyn) next = static_cast<int>(min(static_cast<long long>(tile) + w.stride, static_cast<long long>(w.end)));
         const int publish_at = min(2, p.k_blocks - 1);
         int tm, tn;
         tile_coords(tile, p, tm, tn);
@@ -129,8 +157,8 @@ __device__ __forceinline__ void copy_operands(const GemmParams& p, uint32_t sbas
                 stage = 0;
                 phase ^= 1u;
             }
-            if (even && kb == publish_at) {
-                const long long at = dyn ? static_cast<long long>(w.stride) + ticket : static_cast<long long>(tile) + w.stride;
+            if (even && dyn && kb == publish_at) {
+                const long long at = static_cast<long long>(w.stride) + ticket;
                 next = at < w.end ? static_cast<int>(at) : w.end;
                 ok = sched_publish(bar0, j + 1, next, abort_flag, p.wait_limit_ns);
                 if (!ok) break;
@@ -155,10 +183,12 @@ __device__ __forceinline__ void arrive_pair(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The whole warp runs the loop, so that what the instructions take is uniform over it (in one thread's
-// branch each operand is moved to uniform registers first); one elected lane issues.
+// Two warps, one for each half of a tile's columns: a wait for a barrier that is long there takes 90 cycles and
+// four MMAs with their commits 160, so that one warp's round for a block, 790 cycles, was longer than the MMAs'.
+// The whole warp runs the loop, so that what the instructions take is uniform over it (in one thread's branch each
+// operand is moved to uniform registers first); one elected lane issues.
 __device__ __forceinline__ void issue_blocks(const GemmParams& p, uint32_t sbase, uint32_t bar0, uint32_t tmem_base,
-                                        volatile int* abort_flag)
+                                             int h, volatile int* abort_flag)
 {
     constexpr uint32_t idesc = make_idesc_e4m3(2 * kBM, kCols);
     const WorkRange w = work_range<true>(p);
@@ -168,55 +198,52 @@ __device__ __forceinline__ void issue_blocks(const GemmParams& p, uint32_t sbase
     const uint16_t mask_pair = static_cast<uint16_t>(3u << self);
     const bool elected = elect_one();
     const uint64_t desc0 = make_sdesc_sw128(sbase, 0, 1024);
+    const uint32_t b_at = static_cast<uint32_t>((C::kABytes + h * kHalfBytes) >> 4);
     int stage = 0;
     uint32_t phase = 0;
     uint32_t block = 0;  // K blocks so far, over all tiles
-    bool issued_any = false;
     bool ok = true;
     int tile = w.first;
     for (int j = 0; ok; ++j) {
-        if (j > 0 && !sched_take_warp(bar0, j, tile, abort_flag, p.wait_limit_ns)) {
-            if (!*abort_flag) record_failure(p.status, abort_flag, kRoleMma);
+        if (j > 0 && !next_tile(p, w, bar0, j, tile, abort_flag)) {
             ok = false;
             break;
         }
         if (tile >= w.end) break;
-        for (int kb = 0; kb < p.k_blocks && ok; ++kb, ++block) {
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++block) {
             const uint64_t desc = desc0 + static_cast<uint32_t>(stage * (kStageBytes >> 4));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t acc = 2 * (block & 1u) + h;
-                if (h == 0) ok = warp_wait(bar0 + 8u * (kBarFull + stage), phase, abort_flag, p.wait_limit_ns);
-                ok = ok && warp_wait(bar0 + 8u * (kBarAccEmpty + acc), ((block >> 1) & 1u) ^ 1u, abort_flag, p.wait_limit_ns);
-                if (!ok) {
-                    if (!*abort_flag) record_failure(p.status, abort_flag, kRoleMma);
-                    break;
-                }
-                tcgen05_fence_after_sync();
-                if (elected) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f8_ss_pair(tmem_base + acc * kCols, desc + kk * 2,
-                                       desc + ((C::kABytes + h * kHalfBytes) >> 4) + kk * 2, idesc, kk > 0 ? 1u : 0u);
-                    mma_commit_pair(bar0 + 8u * (kBarAccFull + acc), mask_pair);
-                    if (h == 1) mma_commit_pair(bar0 + 8u * (kBarEmpty + stage), mask_pair);
-                }
-                __syncwarp();
-                issued_any = true;
+            const uint32_t acc = 2 * (block & 1u) + h;
+            const uint32_t full = bar0 + 8u * (kBarFull + stage), empty = bar0 + 8u * (kBarAccEmpty + acc);
+            const uint32_t turn = ((block >> 1) & 1u) ^ 1u;
+            // (both at once: either takes 90 cycles)
+            const bool there = mbar_try_wait(full, phase), free = mbar_try_wait(empty, turn);
+            if (!__all_sync(0xFFFFFFFFu, there && free)) {
+                ok = warp_wait(full, phase, abort_flag, p.wait_limit_ns) &&
+                     warp_wait(empty, turn, abort_flag, p.wait_limit_ns);
+                if (!ok) break;
             }
-            if (!ok) break;
+            tcgen05_fence_after_sync();
+            if (elected) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f8_ss_pair(tmem_base + acc * kCols, desc + kk * 2, desc + b_at + kk * 2, idesc, kk > 0 ? 1u : 0u);
+                mma_commit_pair(bar0 + 8u * (kBarAccFull + acc), mask_pair);
+                mma_commit_pair(bar0 + 8u * (kBarEmpty + stage), mask_pair);
+            }
+            __syncwarp();
             if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1u;
             }
         }
     }
-    if (!ok && issued_any) {
-        // every MMA issued completes before tensor memory is released
-        if (elected) mma_commit_pair(bar0 + 8u * kBarDrain, mask_self);
-        __syncwarp();
-        wait_bounded(bar0 + 8u * kBarDrain, 0, abort_flag, kDrainLimitNs, false);
-    }
+    if (ok) return;
+    if (!*abort_flag) record_failure(p.status, abort_flag, kRoleMma);
+    // every MMA issued completes before tensor memory is released
+    const uint32_t drain = bar0 + 8u * (h ? kBarDrain2 : kBarDrain);
+    if (elected) mma_commit_pair(drain, mask_self);
+    __syncwarp();
+    wait_bounded(drain, 0, abort_flag, kDrainLimitNs, false);
 }
 
 // One warp: the scales of every K block of every tile into the ring.
@@ -233,7 +260,7 @@ __device__ __forceinline__ void stage_scales(const GemmParams& p, uint8_t* smem,
     uint32_t group = 0;
     int tile = w.first;
     for (int j = 0;; ++j) {
-        if (j > 0 && !sched_take_warp(bar0, j, tile, abort_flag, p.wait_limit_ns)) {
+        if (j > 0 && !next_tile(p, w, bar0, j, tile, abort_flag)) {
             if (!*abort_flag) record_failure(p.status, abort_flag, kRoleProducer);
             return;
         }
@@ -416,38 +443,33 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
         if (!*abort_flag) record_failure(p.status, abort_flag, kRoleEpilogue);
         return false;
     };
-    // block `b`'s MMAs are done
-    auto ready = [&](uint32_t b) {
-        const bool ok =
-            warp_wait(bar0 + 8u * (kBarAccFull + 2 * (b & 1u) + half), (b >> 1) & 1u, abort_flag, p.wait_limit_ns);
+    // the MMAs into accumulator `a` (0 or 1, of this half) are done
+    auto ready = [&](uint32_t bar, uint32_t parity) {
+        const bool ok = warp_wait(bar, parity, abort_flag, p.wait_limit_ns);
         tcgen05_fence_after_sync();
         return ok || failed();
     };
-    // the scales of block kb of the tile are there
-    auto scales_ready = [&](int kb) {
-        if (kb % kGroup != 0) return true;
+    // the scales of the next group of K blocks are there
+    auto scales_ready = [&]() {
         return warp_wait(bar0 + 8u * (kBarScaleFull + group % kScaleGroups), group / kScaleGroups & 1u, abort_flag,
-                              p.wait_limit_ns) || failed();
+                         p.wait_limit_ns) || failed();
     };
-    // this warp has read its part of block `b`'s accumulator
-    auto release = [&](uint32_t b) {
+    // this warp has read its part of an accumulator
+    auto release = [&](uint32_t bar) {
         tcgen05_fence_before_sync();
         __syncwarp();
-        if (lane == 0) arrive_pair(empty0 + 8u * (2 * (b & 1u) + half));
+        if (lane == 0) arrive_pair(bar);
     };
-    // ... and the scales of block kb
-    auto release_scales = [&](int kb) {
-        if (kb % kGroup != kGroup - 1 && kb != p.k_blocks - 1) return;
+    // ... and a group's scales
+    auto release_scales = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar0 + 8u * (kBarScaleEmpty + group % kScaleGroups));
         ++group;
     };
-    auto scales_at = [&](int kb) { return (group % kScaleGroups * kGroup + kb % kGroup) * (kScaleFloats * 4); };
-    auto accumulator = [&](uint32_t b) { return t_lane + (2 * (b & 1u) + half) * kCols; };
 
     int tile = w.first;
     for (int j = 0;; ++j) {
-        if (j > 0 && !sched_take_warp(bar0, j, tile, abort_flag, p.wait_limit_ns)) {
+        if (j > 0 && !next_tile(p, w, bar0, j, tile, abort_flag)) {
             if (!*abort_flag) record_failure(p.status, abort_flag, kRoleEpilogue);
             break;
         }
@@ -459,10 +481,11 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
         bool ok = true;
         if (row0 >= p.m || col0 >= p.n) {  // nothing of the tile for this warp to store
             for (int kb = 0; kb < p.k_blocks && ok; ++kb, ++block) {
-                ok = scales_ready(kb) && ready(block);
+                const uint32_t at = 2 * (block & 1u) + half;
+                ok = (kb % kGroup != 0 || scales_ready()) && ready(bar0 + 8u * (kBarAccFull + at), block >> 1 & 1u);
                 if (!ok) break;
-                release(block);
-                release_scales(kb);
+                release(empty0 + 8u * at);
+                if (kb % kGroup == kGroup - 1 || kb == p.k_blocks - 1) release_scales();
             }
             if (!ok) break;
             continue;
@@ -475,51 +498,76 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
         float sum[kCols];
 #pragma unroll
         for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
-        // Sixteen values are on their way while those before them are added.  (The next block's first ones ahead
-        // of this one's end, and sums held as pairs, cost copies of registers: 941 and 860 us for 16384 x 8192 x
-        // 8192 in runs where this took 827 to 850.)
+        // Columns 32 c on, as two loads (SQUARE: half of the columns; otherwise half of the lanes each).  The blocks
+        // are walked in groups, as their scales come, so that every address and parity within one is a constant
+        // next to a few registers.  (Sixteen values on their way while sixteen are added were no quicker; the next
+        // block's first ones ahead of this one's end, and sums held as pairs, cost copies of registers.)
         uint32_t r[2][16];
-        auto load = [&](uint32_t b, int c) {  // SQUARE: columns 16 c on; otherwise columns 32 (c / 2) on, lanes 16 (c % 2) on
-            if constexpr (SQUARE)
-                load_lane16(accumulator(b) + c * 16, r[c & 1]);
-            else
-                load_square16(accumulator(b) + ((c & 1) << 20) + (c >> 1) * 32, r[c & 1]);
+        auto load = [&](uint32_t from, int c) {
+            if constexpr (SQUARE) {
+                load_lane16(from + c * 32, r[0]);
+                load_lane16(from + c * 32 + 16, r[1]);
+            } else {
+                load_square16(from + c * 32, r[0]);
+                load_square16(from + c * 32 + (16u << 16), r[1]);
+            }
         };
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++block) {
-            ok = scales_ready(kb);
+        // the accumulators that this tile's even and odd blocks use, their barriers' parities (the same in every group)
+        const uint32_t even = 2 * (block & 1u) + half, odd = even ^ 2u;
+        const uint32_t from[2] = {t_lane + even * kCols, t_lane + odd * kCols};
+        const uint32_t full[2] = {bar0 + 8u * (kBarAccFull + even), bar0 + 8u * (kBarAccFull + odd)};
+        const uint32_t empty[2] = {empty0 + 8u * even, empty0 + 8u * odd};
+        const uint32_t parity[2] = {block >> 1 & 1u, (block + 1) >> 1 & 1u};
+        block += p.k_blocks;
+        bool soon = false;  // whether the next block was done when this one's last values had been read
+        for (int left = p.k_blocks; left > 0 && ok; left -= kGroup) {
+            ok = scales_ready();
             if (!ok) break;
-            const uint32_t at = scales_at(kb);
-            Pair f[SQUARE ? 1 : 4], g[4];
+            const uint32_t at = group % kScaleGroups * (kGroup * kScaleFloats * 4);
 #pragma unroll
-            for (int i = 0; i < (SQUARE ? 1 : 4); ++i) {
-                const uint32_t v = ld_shared_u32(rows + at + 32 * i);
-                f[i] = pair_of(v, v);
-            }
-            ok = ready(block);
-            if (!ok) break;
-            load(block, 0);
+            for (int q = 0; q < kGroup; ++q) {
+                if (q >= left) break;
+                Pair f[SQUARE ? 1 : 4], g[4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if (!SQUARE && c % 2 == 0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) g[i] = ld_shared_pair(columns + at + 64 * c + 32 * i);
+                for (int i = 0; i < (SQUARE ? 1 : 4); ++i) {
+                    const uint32_t v = ld_shared_u32(rows + at + q * (kScaleFloats * 4) + 32 * i);
+                    f[i] = pair_of(v, v);
                 }
-                tmem_wait(r[c & 1]);
-                if (c < 7)
-                    load(block, c + 1);
-                else
-                    release(block);
+                if (__all_sync(0xFFFFFFFFu, soon)) {
+                    tcgen05_fence_after_sync();
+                } else {
+                    ok = ready(full[q & 1], parity[q & 1] ^ (q >> 1));
+                    if (!ok) break;
+                }
+                load(from[q & 1], 0);
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    float* s = sum + c * 16 + e;
-                    const Pair x = pair_of(r[c & 1][e], r[c & 1][e + 1]);
-                    if constexpr (SQUARE)
-                        fma2(s[0], s[1], x, f[0]);
-                    else
-                        fma2(s[0], s[1], mul2(x, g[e / 4]), f[2 * (c & 1) + (e >> 1 & 1)]);
+                for (int c = 0; c < 4; ++c) {
+                    if (!SQUARE) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            g[i] = ld_shared_pair(columns + at + q * (kScaleFloats * 4) + 128 * c + 32 * i);
+                    }
+                    tmem_wait(r);
+                    if (c == 3) {
+                        release(empty[q & 1]);
+                        soon = mbar_test(full[(q + 1) & 1], parity[(q + 1) & 1] ^ ((q + 1) >> 1 & 1));
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            float* s = sum + c * 32 + h * 16 + e;
+                            const Pair x = pair_of(r[h][e], r[h][e + 1]);
+                            if constexpr (SQUARE)
+                                fma2(s[0], s[1], x, f[0]);
+                            else
+                                fma2(s[0], s[1], mul2(x, g[e / 4]), f[2 * h + (e >> 1 & 1)]);
+                        }
+                    }
+                    if (c < 3) load(from[q & 1], c + 1);
                 }
             }
-            release_scales(kb);
+            release_scales();
         }
         if (!ok) break;
         __syncwarp();  // (sbias)
@@ -551,11 +599,11 @@ __global__ void __launch_bounds__(kBlockThreads, 1) block_pair_kernel(const __gr
         prefetch_tensormap(&p.tm_D);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(bar0 + 8u * (kBarFull + s), 1);
-            mbar_init(bar0 + 8u * (kBarEmpty + s), 1);
+            mbar_init(bar0 + 8u * (kBarEmpty + s), 2);  // (a commit of each half)
         }
         for (int s = 0; s < kSchedSlots; ++s) {
             mbar_init(bar0 + 8u * (kBarSchedFull + s), 1);
-            mbar_init(bar0 + 8u * (kBarSchedEmpty + s), sched_consumers<kSumWarps>() + 2);  // (and the scales' warps)
+            mbar_init(bar0 + 8u * (kBarSchedEmpty + s), sched_consumers<kSumWarps>() + 3);  // (and the scales' warps, the second half's MMAs)
         }
         for (int s = 0; s < kScaleGroups; ++s) {
             mbar_init(bar0 + 8u * (kBarScaleFull + s), 1);
@@ -567,6 +615,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) block_pair_kernel(const __gr
         }
         mbar_init(bar0 + 8u * kBarStall, 1);
         mbar_init(bar0 + 8u * kBarDrain, 1);
+        mbar_init(bar0 + 8u * kBarDrain2, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -590,8 +639,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1) block_pair_kernel(const __gr
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 0 && !*abort_flag) {
             if (lane == 0) copy_operands(p, sbase, bar0, abort_flag);
-        } else if (warp == 1 && !*abort_flag) {
-            issue_blocks(p, sbase, bar0, tmem_base, abort_flag);
+        } else if ((warp == 1 || warp == 3) && !*abort_flag) {
+            issue_blocks(p, sbase, bar0, tmem_base, warp >> 1, abort_flag);
         } else if (warp == 2 && !*abort_flag) {
             stage_scales<SQUARE>(p, smem, bar0, abort_flag);
         }
