@@ -8,11 +8,11 @@
 // The tensor cores cannot apply such scales to a sum that they keep, so the sum of each block of
 // 128 k is a sum of its own: the MMA warp starts every K block with cleared accumulators and hands
 // them over, and the summing warps read them, multiply them by their scales and add them to the
-// tile's sums in fp32 registers.  What bounds it is this hand-over and the additions, not the MMAs:
-// 256 x 256 x 128 take 584 cycles on the pair, the sums of a block about 860 (SQUARE) and 1300.
+// tile's sums in fp32 registers.  What bounds it is this hand-over and the additions: 256 x 256 x 128
+// take 512 cycles of the pair's tensor cores, a block in all about 640 (SQUARE) and 1080.
 //   * Four accumulators of 128 columns, half a tile each: a half's MMAs run while the three before
-//     it are read, so that no MMA waits for a round trip through barriers (one accumulator for a
-//     whole tile, two in turn: 1977 us for 16384 x 8192 x 8192, 850 so, with what follows).
+//     it are read, so that no MMA waits for a round trip through barriers (a whole tile's, two in
+//     turn: 1977 us for 16384 x 8192 x 8192).
 //   * Eight summing warps (a lane quarter, half the tile's columns each), 128 sums a thread, two added
 //     an instruction.  A block is one chain of steps for each warp: its accumulators' barrier, four
 //     loads of 32 columns, the arrival that frees them.  What is in that chain counts, not the
@@ -20,11 +20,10 @@
 //   * SQUARE: a warp's columns share one scale, a thread (a row) has one factor a block.  Otherwise
 //     every column has its own, and a thread's values are loaded as four rows of 32 columns, so that
 //     32 scales a block come from shared memory for them and not 128 (whose 1024 cycles a block
-//     would bound it); the loads of this shape are the slower ones, and each value takes a product
-//     before its addition (1170 us).
+//     would bound it); each value then takes a product before its addition.
 //   * One warp brings the scales of all blocks into a ring in shared memory, ahead of the sums.
-// 16384 x 8192 x 8192: 850 us, 2.59 PFLOP/s (1170, 1.88 with a scale for each row of B); its MMAs
-// alone would take 590.
+// 16384 x 8192 x 8192: 717 us, 3.07 PFLOP/s, in a short run, 873 where the power limit holds; 4096 x 8192 x
+// 2064 64.0 us, 2.16 PFLOP/s, 83.8 with a scale for each row of B.
 #pragma once
 
 #include "block_sums.cuh"
@@ -37,7 +36,7 @@ namespace block_pair {
 using C = TileCfg<256, true>;
 constexpr int kCols = 128;                    // columns of D per accumulator
 constexpr int kHalfBytes = 64 * 128;          // a CTA's rows of B for half a tile's columns, in a stage
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kStageBytes = C::kStageBytes;
 // Four warps of copies, MMAs and scales (and an idle one), then those that sum: the registers are
 // given out by warpgroup, and the sums need more than an even share of the block's 384 x 168.
@@ -51,10 +50,15 @@ static_assert(128 * kIssueRegs + 32 * kSumWarps * kSumRegs <= kBlockThreads * 16
 constexpr int kGroup = 4;                     // K blocks of scales that are handed over together
 constexpr int kScaleGroups = 2;
 constexpr int kScaleFloats = 3 * 128;
-// Shared memory: the stages, a 2 KB box and the bias of its columns for each summing warp, the scales.
+// Shared memory: the stages, 2 KB boxes for each summing warp (one is filled while the other is read: 4096 x 8192 x
+// 2064 64.0 us with five stages and two boxes, 66.6 with six and one), the bias of three tiles' columns (a tile's is
+// staged with its first scales, two groups ahead of their use at most: when those of tile j + 3 are, the epilogue
+// of tile j is over), the scales.
+constexpr int kBoxes = 2;
+constexpr int kBiasTiles = 3;
 constexpr int kOffBox = kStages * kStageBytes;
-constexpr int kOffBias = kOffBox + kSumWarps * 2048;
-constexpr int kOffScale = kOffBias + kSumWarps * kCols * 4;
+constexpr int kOffBias = kOffBox + kSumWarps * kBoxes * 2048;
+constexpr int kOffScale = kOffBias + kBiasTiles * 256 * 4;
 constexpr int kOffBar = kOffScale + kScaleGroups * kGroup * kScaleFloats * 4;
 constexpr int kSmemBytes = 1024 + kOffBar + C::kBarBytes;  // (1024: alignment)
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -246,7 +250,8 @@ __device__ __forceinline__ void issue_blocks(const GemmParams& p, uint32_t sbase
     wait_bounded(drain, 0, abort_flag, kDrainLimitNs, false);
 }
 
-// One warp: the scales of every K block of every tile into the ring.
+// One warp: the scales of every K block of every tile into the ring, and each tile's bias along the columns (read by
+// the summing warps themselves it held up every tile: 2039 x 4096 x 1024 15.1 us, 14.4 so).
 template <bool SQUARE>
 __device__ __forceinline__ void stage_scales(const GemmParams& p, uint8_t* smem, uint32_t bar0, volatile int* abort_flag)
 {
@@ -256,6 +261,7 @@ __device__ __forceinline__ void stage_scales(const GemmParams& p, uint8_t* smem,
     constexpr int kB = SQUARE ? 2 : 8;        // scales of B of a lane and block
     constexpr int kAtOnce = SQUARE ? 4 : 2;   // blocks whose loads are on their way together
     float* ring = reinterpret_cast<float*>(smem + kOffScale);
+    const bool bias_along_cols = p.epilog != EPI_NONE && p.bias_layout == 1;
     grid_dependency_wait();
     uint32_t group = 0;
     int tile = w.first;
@@ -274,6 +280,14 @@ __device__ __forceinline__ void stage_scales(const GemmParams& p, uint8_t* smem,
 #pragma unroll
         for (int i = 0; i < kB; ++i)
             ib[i] = SQUARE ? min(tn * 2 + i, static_cast<int>(sb_row) - 1) : min(tn * 256 + lane + 32 * i, p.n - 1);
+        float bias[8];
+        if (bias_along_cols) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int col = tn * 256 + lane + 32 * i;
+                bias[i] = col < p.n ? load_16bit(p.bias, col, 1) : 0.0f;
+            }
+        }
         for (int kb0 = 0; kb0 < p.k_blocks; kb0 += kGroup, ++group) {
             const uint32_t slot = group % kScaleGroups;
 #pragma unroll
@@ -293,6 +307,11 @@ __device__ __forceinline__ void stage_scales(const GemmParams& p, uint8_t* smem,
                                                p.wait_limit_ns)) {
                     if (!*abort_flag) record_failure(p.status, abort_flag, kRoleProducer);
                     return;
+                }
+                if (bias_along_cols && kb0 == 0 && q0 == 0) {
+                    float* to = reinterpret_cast<float*>(smem + kOffBias) + j % kBiasTiles * 256 + lane;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) to[32 * i] = bias[i];
                 }
 #pragma unroll
                 for (int q = 0; q < kAtOnce; ++q) {
@@ -338,7 +357,7 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
     const bool along_cols = p.bias_layout == 1;
     // (a thread's rows: one, or four)
     auto row_of = [&](int q) { return SQUARE ? row0 + lane : row0 + lane / 4 + 8 * q; };
-    if (lane == 0) bulk_wait_group_read<0>();  // this warp's last box is read
+    if (lane == 0) bulk_wait_group_read<kBoxes - 1>();  // this box has been read
     __syncwarp();
     if constexpr (SQUARE) {
         const int row = row_of(0);
@@ -427,18 +446,17 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
     const int sw = static_cast<int>(threadIdx.x >> 5) - 4;
     const int quarter = sw & 3, half = sw >> 2;
     const WorkRange w = work_range<true>(p);
-    float* sbias = reinterpret_cast<float*>(smem + kOffBias) + sw * kCols;  // this warp's own, as the box
-    uint8_t* box = smem + kOffBox + sw * 2048;
-    const uint32_t box_u32 = sbase + kOffBox + sw * 2048;
+    uint8_t* box = smem + kOffBox + sw * (kBoxes * 2048);
+    const uint32_t box_u32 = sbase + kOffBox + sw * (kBoxes * 2048);
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t empty0 = map_shared_rank(bar0 + 8u * kBarAccEmpty, cluster_ctarank() & ~1u);
     // this thread's row's factor, or its four rows' scales and its columns'
     const uint32_t rows = sbase + kOffScale + 4 * (quarter * 32 + (SQUARE ? half * 128 + lane : lane / 4));
     const uint32_t columns = sbase + kOffScale + 4 * (128 + half * 128 + 2 * (lane & 3));
-    constexpr bool kBias = EPI != EPI_NONE;
     grid_dependency_wait();
 
     uint32_t block = 0, group = 0;  // K blocks and groups of scales so far, over all tiles
+    uint32_t stored = 0;            // boxes so far
     auto failed = [&]() {
         if (!*abort_flag) record_failure(p.status, abort_flag, kRoleEpilogue);
         return false;
@@ -489,11 +507,6 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
             }
             if (!ok) break;
             continue;
-        }
-        if (kBias && p.bias_layout == 1) {
-            __syncwarp();
-            for (int i = lane; i < kCols; i += 32)
-                sbias[i] = col0 + i < p.n ? load_16bit(p.bias, col0 + i, 1) : 0.0f;
         }
         float sum[kCols];
 #pragma unroll
@@ -570,12 +583,13 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
             release_scales();
         }
         if (!ok) break;
-        __syncwarp();  // (sbias)
+        const float* bias = reinterpret_cast<const float*>(smem + kOffBias) + j % kBiasTiles * 256 + half * kCols;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            if (col0 + c * 32 < p.n)
-                store_chunk<SQUARE, EPI>(p, sum + c * 32, sbias + c * 32, row0,
-                                         col0 + c * 32, box, box_u32);
+            if (col0 + c * 32 < p.n) {
+                const uint32_t at = stored++ % kBoxes * 2048;
+                store_chunk<SQUARE, EPI>(p, sum + c * 32, bias + c * 32, row0, col0 + c * 32, box + at, box_u32 + at);
+            }
     }
     if (lane == 0) bulk_wait_group_read<0>();
     __syncwarp();
