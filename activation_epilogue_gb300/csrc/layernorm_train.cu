@@ -10,7 +10,7 @@
 // first use, and two sums over the row's threads stand between the loads and the stores.  The first gives
 // a mean m0 in fp32; the second, of the deviations from it and of their squares, gives what m0 lacks
 // (mu = m0 + mean of the deviations) and the variance about mu, so that a row far from zero loses nothing
-// to the rounding of its mean.  16384 x 8192 bf16 with a residual to H and E4M3: 141.6 us, 943 MB at 6.65 TB/s,
+// to the rounding of its mean.  16384 x 8192 bf16 with a residual to H and E4M3: 141.2 us, 940 MB at 6.66 TB/s,
 // a copy's rate.  With E4M3 output sixteen lanes hold a block of 128 columns, whose scale
 // takes four shuffles and no barrier.  Sums, statistics, maxima and scales are fp32; H, Y and dX are
 // rounded once each, E4M3 codes once from fp32.
@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(kLongThreads) layernorm_long_kernel(const Laye
 // workspace; layernorm_sums_kernel adds those.  (Added up over a cluster of two to eight blocks first they
 // cost more than the rows saved: 8192 x 4096 46 us without, 46 to 68 so.)  The next row is copied to shared
 // memory while this one is worked on, every thread copying the vectors that it reads itself, so that the
-// copies need no barrier.  16384 x 8192 in bf16 without dH: 165.8 us, 805 MB at 4.86 TB/s (a copy of as many
-// bytes 160); 2039 x 1024: 6.1 us, the two launches' latency and 12.5 MB.
+// copies need no barrier.  16384 x 8192 in bf16 with dH: 165.8 us, 1074 MB at 6.5 TB/s (a copy's rate is 6.7);
+// 333 x 1000 in f16 with dH: 6.1 us, the latency of the two launches.
 
 // (h - mu) rstd, where h - mu may leave fp32: both are halved for rows of that size.
 struct RowStats {

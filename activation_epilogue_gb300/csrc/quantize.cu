@@ -1,8 +1,8 @@
 // E4M3 codes of a 16-bit matrix with a scale for each block of 1 x 128 or 128 x 128 values, row-major
 // and / or transposed in one pass (the products' A and transposed B in every direction of training).
 //
-// Bound by the bytes: 2 read and 1 written per value and output.  8192 x 16384 both ways in 128 x 128 blocks
-// 79.9 us, 537 MB at 6.7 TB/s, a copy's rate; 2039 x 4096 both ways in 1 x 128 blocks 9.2 us, 34 MB, of which
+// Bound by the bytes: 2 read and 1 written per value and output.  16384 x 8192 both ways in 128 x 128 blocks
+// 79.7 us, 537 MB at 6.7 TB/s, a copy's rate; 2039 x 4096 both ways in 1 x 128 blocks 9.2 us, 34 MB, of which
 // 5 are the bytes and the rest a launch and a tile's two barriers.
 //   * 1 x 128, row-major alone: sixteen lanes have a block, eight values each, and four rows at a time,
 //     every load issued first; no shared memory and no barrier.

@@ -304,8 +304,8 @@ typedef struct {
     const float* ln_stats;   /* LN_GELU_BIAS: m pairs (mean, rstd), 8-byte aligned */
     const float* ln_colsum;  /* LN_GELU_BIAS: n column sums of W' */
     const float* ln_bias;    /* LN_GELU_BIAS: n values beta . W + b */
-    const float* scale_a;    /* E4M3 plans: device fp32 scale of A (NULL otherwise) */
-    const float* scale_b;    /* E4M3 plans: device fp32 scale of B */
+    const float* scale_a;    /* E4M3 plans: device fp32 scale(s) of A (NULL otherwise) */
+    const float* scale_b;    /* E4M3 plans: device fp32 scale(s) of B */
 } gemm_epi_operands;
 
 /* The fused kernel on the operands in *ops (any epilog of the plan). */
