@@ -9,7 +9,7 @@
 // 128 k is a sum of its own: the MMA warp starts every K block with cleared accumulators and hands
 // them over, and the summing warps read them, multiply them by their scales and add them to the
 // tile's sums in fp32 registers.  What bounds it is this hand-over and the additions: 256 x 256 x 128
-// take 512 cycles of the pair's tensor cores, a block in all about 640 (SQUARE) and 1080.
+// take 512 cycles of the pair's tensor cores, a block in all about 660 (SQUARE) and 1090.
 //   * Four accumulators of 128 columns, half a tile each: a half's MMAs run while the three before
 //     it are read, so that no MMA waits for a round trip through barriers (a whole tile's, two in
 //     turn: 1977 us for 16384 x 8192 x 8192).
@@ -20,7 +20,9 @@
 //   * SQUARE: a warp's columns share one scale, a thread (a row) has one factor a block.  Otherwise
 //     every column has its own, and a thread's values are loaded as four rows of 32 columns, so that
 //     32 scales a block come from shared memory for them and not 128 (whose 1024 cycles a block
-//     would bound it); each value then takes a product before its addition.
+//     would bound it); each value then takes a product before its addition, 512 cycles of the fp32
+//     pipes.  (Without the reads of the columns' scales a block would take 90 cycles less, without the
+//     products 15; wider reads, scales by asynchronous copies and other orders of the products: 1 %.)
 //   * One warp brings the scales of all blocks into a ring in shared memory, ahead of the sums.
 // 16384 x 8192 x 8192: 717 us, 3.07 PFLOP/s, in a short run, 873 where the power limit holds; 4096 x 8192 x
 // 2064 64.0 us, 2.16 PFLOP/s, 83.8 with a scale for each row of B.
@@ -38,7 +40,7 @@ constexpr int kCols = 128;                    // columns of D per accumulator
 constexpr int kHalfBytes = 64 * 128;          // a CTA's rows of B for half a tile's columns, in a stage
 constexpr int kStages = 5;
 constexpr int kStageBytes = C::kStageBytes;
-// Four warps of copies, MMAs and scales (and an idle one), then those that sum: the registers are
+// Four warps of copies, MMAs (two) and scales, then those that sum: the registers are
 // given out by warpgroup, and the sums need more than an even share of the block's 384 x 168.
 constexpr int kSumWarps = 8;
 constexpr int kBlockThreads = 128 + 32 * kSumWarps;

@@ -214,3 +214,21 @@ def test_layernorm_past_32_bits(t, d):
     # (rows of zeros add nothing to the sums and to the sizes that bound their errors)
     assert torch.all((dgamma.double() - want[1]).abs() <= want[4])
     assert torch.all((dbeta.double() - want[2]).abs() <= want[5])
+
+
+@pytest.mark.parametrize("blocks", [1, 2])
+@pytest.mark.parametrize("order", [1, 2])
+@pytest.mark.parametrize("k", [16, 128, 144, 384, 512, 528, 640, 1040])
+def test_one_pair_walks_every_tile(k, order, blocks):
+    """15 tiles of one to nine blocks of k in turn: what is handed from tile to tile (accumulators, scales, the
+    bias of three tiles, boxes of D) in both orders."""
+    m, n = 520, 1032
+    p = ref.product_problem(m, n, k, blocks, seed=k, device="cuda")
+    for epilog in ("BIAS", "GELU_BIAS"):
+        D = torch.full((m, n), float("nan"), dtype=BF16, device="cuda")
+        with gemm_epi.Plan(m, n, k, "e4m3", epilog, SCALE_BLOCKS=blocks, VARIANT=3, GRID=2, TILE_ORDER=order) as plan:
+            for _ in range(2):
+                plan.execute(p["A"], p["B"], p["bias"], D, scales=(p["sa"], p["sb"]))
+            assert plan.sync_status() == 0
+        want, _, error = ref.product(p, blocks, epilog)
+        ref.check(D, want, error)
