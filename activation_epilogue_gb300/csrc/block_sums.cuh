@@ -104,11 +104,19 @@ __device__ __forceinline__ float2 unpair(Pair p)
     return v;
 }
 
+// GELU's argument from below: at -6.1 and before, GELU is within 7e-9 of 0 and so is its value there.  NaN stays NaN.
+__device__ __forceinline__ float gelu_floor(float x)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, 0fC0C33333;" : "=f"(y) : "f"(x));  // -6.1
+    return y;
+}
+
 // GELU of four values by gelu_erf_fast's formula, x / (1 + 2^(x p(x^2))), with one reciprocal for the four
-// denominators (1 / a0 = a1 a2 a3 / (a0 a1 a2 a3)): the special-function unit, sixteen lanes' work a cycle, is what a
-// tile's GELU waits for (2039 x 4096 x 1024 on CTA pairs: 0.7 us less than with two operations a value).  The exponents
-// stop at 30, where the product of four denominators still fits fp32 and neither a NaN nor an infinity reaches its
-// neighbours: down to -8 the result is then within 8 2^-30 = 7.5e-9 of gelu_erf_fast's; below -8 it is 0.
+// denominators (1 / a0 = a1 a2 a3 / (a0 a1 a2 a3)): the special-function unit, sixteen lanes' work a cycle, and the
+// instructions are what a tile's GELU waits for (2039 x 4096 x 1024 on CTA pairs: 0.7 us less than with two such
+// operations a value).  With x held to -6.1 ... 8 in the exponent, where a NaN becomes 8, the exponents stop below 30:
+// the product of four denominators fits fp32, and neither a NaN nor an infinity reaches its neighbours.
 __device__ __forceinline__ void gelu4(float* v)
 {
     const Pair k1 = pair_of(-2.3014667034f, -2.3014667034f), k3 = pair_of(-0.10654459149f, -0.10654459149f);
@@ -117,15 +125,15 @@ __device__ __forceinline__ void gelu4(float* v)
     float2 a[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        x[i] = pair_of(v[2 * i], v[2 * i + 1]);
-        const float2 s = unpair(mul2(x[i], x[i]));
-        const Pair s2 = pair_of(fminf(s.x, 64.0f), fminf(s.y, 64.0f));
+        const float lo = gelu_floor(v[2 * i]), hi = gelu_floor(v[2 * i + 1]);
+        x[i] = pair_of(lo, hi);
+        const Pair z = pair_of(fminf(lo, 8.0f), fminf(hi, 8.0f));
+        const Pair s = mul2(z, z);
         Pair p, q, d;
-        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(s2), "l"(k5), "l"(k3));
-        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(s2), "l"(q), "l"(k1));
-        const float2 u = unpair(mul2(x[i], p));
-        const Pair e = pair_of(exp2_approx(fminf(u.x, 30.0f)), exp2_approx(fminf(u.y, 30.0f)));
-        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(e), "l"(one));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(s), "l"(k5), "l"(k3));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(s), "l"(q), "l"(k1));
+        const float2 u = unpair(mul2(z, p));
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_of(exp2_approx(u.x), exp2_approx(u.y))), "l"(one));
         a[i] = unpair(d);
     }
     const float ab = a[0].x * a[0].y, cd = a[1].x * a[1].y;
@@ -135,8 +143,8 @@ __device__ __forceinline__ void gelu4(float* v)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const float2 y = unpair(mul2(x[i], mul2(pair_of(a[i].y, a[i].x), pair_of(over[i], over[i]))));
-        v[2 * i] = v[2 * i] < -8.0f ? 0.0f : y.x;
-        v[2 * i + 1] = v[2 * i + 1] < -8.0f ? 0.0f : y.y;
+        v[2 * i] = y.x;
+        v[2 * i + 1] = y.y;
     }
 }
 

@@ -87,8 +87,7 @@ __device__ __forceinline__ void load_values(uint32_t taddr, uint32_t (&r)[8]) { 
 __device__ __forceinline__ float apply(float v, int epilog)
 {
     if (epilog == EPI_RELU_BIAS || epilog == EPI_RELU_AUX_BIAS) return v > 0.0f ? v : 0.0f;
-    // (0 below -8, as with gelu4: an infinity's too)
-    return epilog == EPI_GELU_BIAS ? (v < -8.0f ? 0.0f : gelu_erf_fast(v)) : v;
+    return epilog == EPI_GELU_BIAS ? gelu_erf_fast(gelu_floor(v)) : v;  // (as gelu4; minus infinity is no NaN either)
 }
 
 template <int NP, bool SQUARE>
