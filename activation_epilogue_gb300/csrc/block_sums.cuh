@@ -87,12 +87,31 @@ __device__ __forceinline__ Pair mul2(Pair a, Pair b)
     return p;
 }
 
+// (x, y) += a
+__device__ __forceinline__ void add2(float& x, float& y, Pair a)
+{
+    Pair acc;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(x), "f"(y));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(a));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(acc));
+}
+
 // Shared memory by its own address (through generic ones the loads' latency is much longer).
 __device__ __forceinline__ Pair ld_shared_pair(uint32_t addr)
 {
     Pair v;
     asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
     return v;
+}
+
+__device__ __forceinline__ void ld_shared_pairs(uint32_t addr, Pair& a, Pair& b)
+{
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 __device__ __forceinline__ Pair pair_of(float a, float b) { return pair_of(__float_as_uint(a), __float_as_uint(b)); }

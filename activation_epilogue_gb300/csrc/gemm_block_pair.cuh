@@ -255,14 +255,13 @@ __device__ __forceinline__ void issue_blocks(const GemmParams& p, uint32_t sbase
 // One warp: the scales of every K block of every tile into the ring, and each tile's bias along the columns (read by
 // the summing warps themselves it held up every tile: 2039 x 4096 x 1024 15.1 us, 14.4 so).
 template <bool SQUARE>
-__device__ __forceinline__ void stage_scales(const GemmParams& p, uint8_t* smem, uint32_t bar0, volatile int* abort_flag)
+__device__ __forceinline__ void stage_scales(const GemmParams& p, uint32_t sbase, uint32_t bar0, volatile int* abort_flag)
 {
     const int lane = threadIdx.x & 31;
     const WorkRange w = work_range<true>(p);
     const long long sb_row = SQUARE ? (p.n + 127) / 128 : p.n;
     constexpr int kB = SQUARE ? 2 : 8;        // scales of B of a lane and block
     constexpr int kAtOnce = SQUARE ? 4 : 2;   // blocks whose loads are on their way together
-    float* ring = reinterpret_cast<float*>(smem + kOffScale);
     const bool bias_along_cols = p.epilog != EPI_NONE && p.bias_layout == 1;
     grid_dependency_wait();
     uint32_t group = 0;
@@ -311,21 +310,21 @@ __device__ __forceinline__ void stage_scales(const GemmParams& p, uint8_t* smem,
                     return;
                 }
                 if (bias_along_cols && kb0 == 0 && q0 == 0) {
-                    float* to = reinterpret_cast<float*>(smem + kOffBias) + j % kBiasTiles * 256 + lane;
+                    const uint32_t to = sbase + kOffBias + (j % kBiasTiles * 256 + lane) * 4;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) to[32 * i] = bias[i];
+                    for (int i = 0; i < 8; ++i) st_shared_u32(to + 128 * i, __float_as_uint(bias[i]));
                 }
 #pragma unroll
                 for (int q = 0; q < kAtOnce; ++q) {
-                    float* to = ring + (slot * kGroup + q0 + q) * kScaleFloats + lane;
+                    const uint32_t to = sbase + kOffScale + ((slot * kGroup + q0 + q) * kScaleFloats + lane) * 4;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        to[32 * i] = SQUARE ? a[q][i] * b[q][0] : a[q][i];
-                        if (SQUARE) to[128 + 32 * i] = a[q][i] * b[q][1];
+                        st_shared_u32(to + 128 * i, __float_as_uint(SQUARE ? a[q][i] * b[q][0] : a[q][i]));
+                        if (SQUARE) st_shared_u32(to + 512 + 128 * i, __float_as_uint(a[q][i] * b[q][1]));
                     }
                     if constexpr (!SQUARE) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) to[128 + 32 * i] = b[q][i];
+                        for (int i = 0; i < 8; ++i) st_shared_u32(to + 512 + 128 * i, __float_as_uint(b[q][i]));
                     }
                 }
             }
@@ -351,8 +350,8 @@ __device__ __forceinline__ void activate_block(float (&v)[N])
 
 // The epilogue of 32 of the warp's columns, `at` on, and their store through the warp's box.
 template <bool SQUARE, int EPI>
-__device__ __forceinline__ void store_chunk(const GemmParams& p, const float* sum, const float* bias, int row0, int at,
-                                            uint8_t* box, uint32_t box_u32)
+__device__ __forceinline__ void store_chunk(const GemmParams& p, const float* sum, uint32_t bias, int row0, int at,
+                                            uint32_t box)
 {
     const int lane = threadIdx.x & 31;
     constexpr bool kBias = EPI != EPI_NONE;
@@ -366,8 +365,19 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = sum[e];
-        if constexpr (kBias)
-            add_bias<32>(v, bias, along_cols, !along_cols && row < p.m ? load_16bit(p.bias, row, 1) : 0.0f);
+        if (kBias && along_cols) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                Pair a, b;
+                ld_shared_pairs(bias + 4 * e, a, b);
+                add2(v[e], v[e + 1], a);
+                add2(v[e + 2], v[e + 3], b);
+            }
+        } else if (kBias) {
+            const float b = row < p.m ? load_16bit(p.bias, row, 1) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] += b;
+        }
         if constexpr (EPI == EPI_RELU_AUX_BIAS) {
             uint32_t word = 0;
 #pragma unroll
@@ -387,9 +397,9 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
                     v[8 * q + 2 * h + 1] += __uint_as_float(ww[h] & 0xFFFF0000u);
                 }
             }
-            *reinterpret_cast<uint4*>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(pack2(v[8 * q], v[8 * q + 1], 1), pack2(v[8 * q + 2], v[8 * q + 3], 1),
-                           pack2(v[8 * q + 4], v[8 * q + 5], 1), pack2(v[8 * q + 6], v[8 * q + 7], 1));
+            st_shared_v4(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), pack2(v[8 * q], v[8 * q + 1], 1),
+                         pack2(v[8 * q + 2], v[8 * q + 3], 1), pack2(v[8 * q + 4], v[8 * q + 5], 1),
+                         pack2(v[8 * q + 6], v[8 * q + 7], 1));
         }
     } else {
         const int c2 = 2 * (lane & 3);
@@ -401,7 +411,7 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 b =
-                    kBias && along_cols ? *reinterpret_cast<const float2*>(bias + 8 * i + c2) : make_float2(lb, lb);
+                    kBias && along_cols ? unpair(ld_shared_pair(bias + 4 * (8 * i + c2))) : make_float2(lb, lb);
                 v[2 * i] = sum[16 * (q >> 1) + 4 * i + 2 * (q & 1)] + b.x;
                 v[2 * i + 1] = sum[16 * (q >> 1) + 4 * i + 2 * (q & 1) + 1] + b.y;
             }
@@ -426,8 +436,7 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
                     v[2 * i] += __uint_as_float(w << 16);
                     v[2 * i + 1] += __uint_as_float(w & 0xFFFF0000u);
                 }
-                *reinterpret_cast<uint32_t*>(box + r32 * 64 + ((i ^ ((r32 >> 1) & 3)) << 4) + 2 * c2) =
-                    pack2(v[2 * i], v[2 * i + 1], 1);
+                st_shared_u32(box + r32 * 64 + ((i ^ ((r32 >> 1) & 3)) << 4) + 2 * c2, pack2(v[2 * i], v[2 * i + 1], 1));
             }
         }
     }
@@ -435,21 +444,20 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, const float* su
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-        tma_store_2d(&p.tm_D, box_u32, at, row0);
+        tma_store_2d(&p.tm_D, box, at, row0);
         bulk_commit_group();
     }
 }
 
 template <bool SQUARE, int EPI>
-__device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, uint32_t sbase, uint32_t bar0,
+__device__ __forceinline__ void sum_blocks(const GemmParams& p, uint32_t sbase, uint32_t bar0,
                                            uint32_t tmem_base, volatile int* abort_flag)
 {
     const int lane = threadIdx.x & 31;
     const int sw = static_cast<int>(threadIdx.x >> 5) - 4;
     const int quarter = sw & 3, half = sw >> 2;
     const WorkRange w = work_range<true>(p);
-    uint8_t* box = smem + kOffBox + sw * (kBoxes * 2048);
-    const uint32_t box_u32 = sbase + kOffBox + sw * (kBoxes * 2048);
+    const uint32_t box = sbase + kOffBox + sw * (kBoxes * 2048);
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t empty0 = map_shared_rank(bar0 + 8u * kBarAccEmpty, cluster_ctarank() & ~1u);
     // this thread's row's factor, or its four rows' scales and its columns'
@@ -585,12 +593,12 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint8_t* smem, u
             release_scales();
         }
         if (!ok) break;
-        const float* bias = reinterpret_cast<const float*>(smem + kOffBias) + j % kBiasTiles * 256 + half * kCols;
+        const uint32_t bias = sbase + kOffBias + (j % kBiasTiles * 256 + half * kCols) * 4;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             if (col0 + c * 32 < p.n) {
-                const uint32_t at = stored++ % kBoxes * 2048;
-                store_chunk<SQUARE, EPI>(p, sum + c * 32, bias + c * 32, row0, col0 + c * 32, box + at, box_u32 + at);
+                store_chunk<SQUARE, EPI>(p, sum + c * 32, bias + c * 128, row0, col0 + c * 32,
+                                         box + stored++ % kBoxes * 2048);
             }
     }
     if (lane == 0) bulk_wait_group_read<0>();
@@ -658,12 +666,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1) block_pair_kernel(const __gr
         } else if ((warp == 1 || warp == 3) && !*abort_flag) {
             issue_blocks(p, sbase, bar0, tmem_base, warp >> 1, abort_flag);
         } else if (warp == 2 && !*abort_flag) {
-            stage_scales<SQUARE>(p, smem, bar0, abort_flag);
+            stage_scales<SQUARE>(p, sbase, bar0, abort_flag);
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-        if (!*abort_flag) sum_blocks<SQUARE, EPI>(p, smem, sbase, bar0, tmem_base, abort_flag);
+        if (!*abort_flag) sum_blocks<SQUARE, EPI>(p, sbase, bar0, tmem_base, abort_flag);
     }
     tcgen05_fence_before_sync();
     __syncthreads();
