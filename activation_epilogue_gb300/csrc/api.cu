@@ -606,10 +606,15 @@ gemm_epi_status configure(gemm_epi_plan_s* p)
     // 10.9 GB read and 8.98 ms dynamic against 26.4 GB and 9.89 ms static; 4096^3 (4 waves)
     // 87.4 us dynamic against 86.0 static; FFN GEMM 1 4096 x 4096 x 1024 GELU (4 waves) 35.2
     // against 32.4 us.  A plan on the caller's stack may have no counter: static.
+    // With block scales, where everyone knows the static order and only the other one is handed over (1.5 us a
+    // tile), from 100 waves of 64 or more K blocks: 65536 x 16384 x 8192 (215 waves) 6190 to 6280 us dynamic
+    // against 6530 to 6580 static, 32768 x 16384 x 8192 (107) 3130 to 3260 against 3240, 16384 x 8192 x 8192 (27)
+    // 798 to 803 against 783 to 788, 65536 x 16384 x 2048 1986 against 1820, k = 1024 1410 against 1095.
     if (p->variant == kRowPair) {
         const long long tiles = static_cast<long long>(p->tiles_m) * p->tiles_n;
         const long long pairs = p->grid / 2;
-        const bool want = p->opt_tile_order == 2 || (p->opt_tile_order == 0 && tiles >= 8 * pairs);
+        const bool many = p->scale_blocks ? p->k_blocks >= 64 && tiles >= 100 * pairs : tiles >= 8 * pairs;
+        const bool want = p->opt_tile_order == 2 || (p->opt_tile_order == 0 && many);
         p->dyn_order = want && p->d_sched != nullptr;
     }
     static const char* vname[] = {"empty", "row-tile", "swapped", "bias-only", "row-pair",

@@ -187,7 +187,8 @@ typedef enum {
     GEMM_EPI_OPT_TILE_ORDER = 11,   /* CTA-pair kernel: 2 = each pair takes its next tile,
                                        in raster order, from a counter in the plan's device
                                        memory as it goes (the automatic choice from eight
-                                       waves of tiles over the pairs up); 1 = static, pair q
+                                       waves of tiles over the pairs up, with SCALE_BLOCKS
+                                       from 100 of k >= 8192); 1 = static, pair q
                                        takes tiles q, q + pairs, ... (the automatic choice
                                        below that); the other kernels ignore it.  With 2 the
                                        plan's launches must not overlap on the GPU (they
