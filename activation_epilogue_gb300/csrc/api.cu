@@ -307,13 +307,13 @@ gemm_epi_status ensure_split_ws(gemm_epi_plan_s* p)
 // E4M3 with scales for blocks of 128 of k: CTA pairs on 256 x 256 tiles, or, for few rows of A, tiles of
 // 128 columns by up to 128 rows with K split over a cluster.  The latter up to 64 rows, where it streams B, and
 // as long as its tiles of 128 x 128 leave two SMs or more for each (a scale for each row of B, which costs the
-// pairs more: one).  Measured (n x k, few rows / pairs, GELU, us; in brackets with a scale for each row of B):
-// 64 rows of 16384 x 8192 27.5 / 31.5 (29.1 / 44.1); 128 rows of it (128 tiles) 36.5 / 33.4 (38.1 / 45.2);
-// 4096 x 4096 with 256 rows (64) 15.7 / 19.1, 512 (128) 21.2 / 19.4 (21.6 / 25.5), 768 (192) 41.5 / 20.4
-// (42.3 / 26.0); 8192 x 8192 with 128 (64) 22.1 / 31.4, 256 (128) 33.3 / 31.2 (35.5 / 43.9), 384 (192) 64.8 / 32.3
-// (69.3 / 44.5); 1024 x 4096 with 1024 (64) 15.5 / 18.5, 1536 (96) 20.9 / 18.6 (21.4 / 24.6).  With a short k
-// the two are closer: 4096 x 1024 with 128 (32) 8.0 / 9.6, 256 (64) 11.0 / 9.6 (11.1 / 11.3), 512 (128) 12.4 / 9.9
-// (12.4 / 11.6).
+// pairs more: one), twice that below 16 blocks of k.  Measured (n x k, few rows / pairs, GELU, us; in brackets
+// with a scale for each row of B): 64 rows of 16384 x 8192 27.5 / 31.5 (29.1 / 44.1), 128 rows of it (128 tiles)
+// 36.5 / 33.4 (38.1 / 45.2); 4096 x 4096 with 256 rows (64 tiles) 15.3 / 18.2, 512 (128) 20.4 / 18.3 (20.9 / 24.6),
+// 768 (192) 40.1 / 19.0 (40.9 / 25.0); 8192 x 8192 with 128 (64) 21.7 / 30.7, 256 (128) 32.5 / 30.3 (34.7 / 42.6),
+// 384 (192) 63.4 / 31.8 (67.7 / 43.4); 4096 x 2048 with 128 (32) 8.7 / 11.9, 256 (64) 12.2 / 11.8, 512 (128)
+// 14.7 / 12.2 (14.8 / 15.8); 4096 x 1024 with 64 (32) 6.5 / 8.5, 128 (32) 7.9 / 8.7, 256 (64) 10.7 / 8.7
+// (10.7 / 10.9), 512 (128) 11.7 / 9.0 (11.8 / 11.2); 4096 x 512 with 64 (32) 6.9 / 7.1, 128 (32) 9.4 / 7.3.
 gemm_epi_status configure_blocks(gemm_epi_plan_s* p)
 {
     const bool square = p->scale_blocks == GEMM_EPI_SCALE_BLOCKS_SQUARE;
@@ -321,7 +321,8 @@ gemm_epi_status configure_blocks(gemm_epi_plan_s* p)
     const int64_t column_tiles = (p->n + 127) / 128;
     int v = p->opt_variant;
     const int64_t tiles128 = column_tiles * ((p->m + 127) / 128);
-    if (v == 0) v = p->m <= 64 || tiles128 * (square ? 2 : 1) <= p->sm_count ? 2 : 3;
+    const int sms_each = (square ? 2 : 1) * (p->k_blocks < 16 ? 2 : 1);
+    if (v == 0) v = p->m <= 64 || tiles128 * sms_each <= p->sm_count ? 2 : 3;
     if (v != 2 && v != 3) return GEMM_EPI_ERR_INVALID_ARG;
     if (v == 3) {
         if (p->opt_bn != 0 && p->opt_bn != 256) return GEMM_EPI_ERR_INVALID_ARG;
