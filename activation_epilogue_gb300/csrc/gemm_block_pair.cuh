@@ -24,8 +24,8 @@
 //     pipes.  (Without the reads of the columns' scales a block would take 90 cycles less, without the
 //     products 15; wider reads, scales by asynchronous copies and other orders of the products: 1 %.)
 //   * One warp brings the scales of all blocks into a ring in shared memory, ahead of the sums.
-// 16384 x 8192 x 8192: 717 us, 3.07 PFLOP/s, in a short run, 873 where the power limit holds; 4096 x 8192 x
-// 2064 64.0 us, 2.16 PFLOP/s, 83.8 with a scale for each row of B.
+// 16384 x 8192 x 8192: 717 us, 3.07 PFLOP/s, in a short run, 858 where the power limit holds; 4096 x 8192 x
+// 2064 63.8 us, 2.17 PFLOP/s, 83.0 with a scale for each row of B.
 #pragma once
 
 #include "block_sums.cuh"
