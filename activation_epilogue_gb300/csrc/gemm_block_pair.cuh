@@ -171,10 +171,10 @@ __device__ __forceinline__ void copy_operands(const GemmParams& p, uint32_t sbas
             }
         }
     }
-    if (ok) return;
-    if (!*abort_flag) record_failure(p.status, abort_flag, kRoleProducer);
+    if (!ok && !*abort_flag) record_failure(p.status, abort_flag, kRoleProducer);
     if (!even) return;
-    // the copies on their way land before the CTA can leave (the even CTA's barriers count both CTAs' copies)
+    // the copies on their way land before the CTA can leave, also where another role gives up after this one's
+    // last copy (the even CTA's barriers count both CTAs' copies)
     for (long long f = issued > kStages ? issued - kStages : 0; f < issued; ++f)
         wait_bounded(bar0 + 8u * (kBarFull + static_cast<int>(f % kStages)), static_cast<uint32_t>(f / kStages & 1),
                      abort_flag, kDrainLimitNs, false);
@@ -243,9 +243,8 @@ __device__ __forceinline__ void issue_blocks(const GemmParams& p, uint32_t sbase
             }
         }
     }
-    if (ok) return;
-    if (!*abort_flag) record_failure(p.status, abort_flag, kRoleMma);
-    // every MMA issued completes before tensor memory is released
+    if (!ok && !*abort_flag) record_failure(p.status, abort_flag, kRoleMma);
+    // every MMA issued completes before tensor memory is released (also where the sums gave up on them)
     const uint32_t drain = bar0 + 8u * (h ? kBarDrain2 : kBarDrain);
     if (elected) mma_commit_pair(drain, mask_self);
     __syncwarp();

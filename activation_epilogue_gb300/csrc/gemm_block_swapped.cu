@@ -177,11 +177,10 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
                 copy(i, true, true);
                 ++issued;
             }
-            if (*abort_flag) {
-                // the copies on their way land before the block's shared memory is given back
-                for (int i = max(0, issued - L::kStages); i < issued; ++i)
-                    wait_bounded(bar0 + 8 * (kFull + i % L::kStages), i / L::kStages & 1, abort_flag, kDrainLimitNs, false);
-            }
+            // the copies on their way land before the block's shared memory is given back (also where another role
+            // gives up after the last of them)
+            for (int i = max(0, issued - L::kStages); i < issued; ++i)
+                wait_bounded(bar0 + 8 * (kFull + i % L::kStages), i / L::kStages & 1, abort_flag, kDrainLimitNs, false);
         }
         __syncwarp();
     } else if (warp == L::kMmaWarp) {
@@ -207,7 +206,7 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
             if (i > 0) {
                 // every MMA issued completes, and its commits arrive, before the block leaves
                 mma_commit(bar0 + 8 * kDrain);
-                wait_bounded(bar0 + 8 * kDrain, 0, abort_flag, i < blocks ? kDrainLimitNs : p.wait_limit_ns, false);
+                wait_bounded(bar0 + 8 * kDrain, 0, abort_flag, kDrainLimitNs, false);
             }
         }
         __syncwarp();
