@@ -79,7 +79,8 @@ typedef enum {
     GEMM_EPI_BF16 = 1, /* bfloat16 inputs and output */
     GEMM_EPI_E4M3 = 2  /* 8-bit floating-point inputs (E4M3: 4 exponent bits, 3 fraction bits,
                           bias 7, no infinities, max 448) with per-tensor fp32 scales (or, with
-                          GEMM_EPI_OPT_SCALE_A_ROWS, one for each row of A); bias,
+                          GEMM_EPI_OPT_SCALE_A_ROWS, one for each row of A; or, with
+                          GEMM_EPI_OPT_SCALE_BLOCKS, one for each block of 128 of k); bias,
                           residual and D in bfloat16.  A is m x k row-major; B is given
                           TRANSPOSED, n x k row-major (both operands contiguous along k), and
                           k must be a multiple of 16.  D = epi(scale_a * scale_b * (A.B) +
