@@ -258,7 +258,7 @@ __device__ __forceinline__ void stage_scales(const GemmParams& p, uint32_t sbase
 {
     const int lane = threadIdx.x & 31;
     const WorkRange w = work_range<true>(p);
-    const long long sb_row = SQUARE ? (p.n + 127) / 128 : p.n;
+    const long long sb_row = SQUARE ? (p.n - 1) / 128 + 1 : p.n;  // (n + 127 may pass 32 bits)
     constexpr int kB = SQUARE ? 2 : 8;        // scales of B of a lane and block
     constexpr int kAtOnce = SQUARE ? 4 : 2;   // blocks whose loads are on their way together
     const bool bias_along_cols = p.epilog != EPI_NONE && p.bias_layout == 1;

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
         __syncwarp();
     } else if (warp < L::kSumWarps && !p.debug_stall) {
         const int quarter = warp & 3, part = warp >> 2;
-        const long long sb_row = SQUARE ? (p.n + 127) / 128 : p.n;
+        const long long sb_row = SQUARE ? (p.n - 1) / 128 + 1 : p.n;  // (n + 127 may pass 32 bits)
         const uint32_t staged = sbase + L::kOffScale;
         float next[L::kStaged], next_b[SQUARE ? 1 : kGroup];
         auto load_scales = [&](int g) {  // of group g of this block's K blocks (the last one's again past the end)

@@ -183,6 +183,36 @@ def test_past_32_bits(m, n, k, blocks):
     ref.check(D[i:, j:], want, error, what="last")
 
 
+@pytest.mark.parametrize("blocks", [1, 2])
+@pytest.mark.parametrize("variant", [2, 3])
+@pytest.mark.parametrize("n", [2 ** 31 - 120, 2 ** 31 - 8])
+def test_the_largest_n(n, variant, blocks):
+    """n up to the largest that a plan takes, where n + 127 passes 32 bits: columns of the first, the middle and the
+    last tiles."""
+    torch.cuda.empty_cache()
+    m, k = 1, 16
+    g = torch.Generator(device="cuda").manual_seed(n % 1000)
+    B = torch.empty(n, k, dtype=torch.uint8, device="cuda")
+    for at in range(0, n, 2 ** 26):  # (no NaN: every code with its top bits below 0x78)
+        some = B[at:at + 2 ** 26]
+        some.copy_(torch.randint(0, 0x78, some.shape, dtype=torch.uint8, generator=g, device="cuda"))
+    p = {"A": torch.randn(m, k, generator=g, device="cuda").to(E4M3), "B": B.view(E4M3),
+         "sa": torch.rand(1, m, generator=g, device="cuda") + 0.5,
+         "sb": torch.rand(1, n if blocks == 2 else ref.up(n, 128) // 128, generator=g, device="cuda") + 0.5}
+    D = torch.full((m, n), float("nan"), dtype=BF16, device="cuda")
+    with gemm_epi.Plan(m, n, k, "e4m3", "NONE", SCALE_BLOCKS=blocks, VARIANT=variant) as plan:
+        plan.execute(p["A"], p["B"], None, D, scales=(p["sa"], p["sb"]))
+        assert plan.sync_status() == 0
+    cols = 2 ** 20
+    for first in (0, n // 2 // 128 * 128, (n - cols) // 128 * 128):
+        last = first + cols if first + cols + 128 <= n else n
+        sb = p["sb"][:, first:last] if blocks == 2 else p["sb"][:, first // 128:ref.up(last, 128) // 128]
+        want, _, error = ref.product({"A": p["A"], "B": p["B"][first:last], "sa": p["sa"], "sb": sb.contiguous()},
+                                     blocks, "NONE")
+        ref.check(D[:, first:last], want, error, what=f"from column {first}")
+    assert not D.isnan().any()
+
+
 @pytest.mark.parametrize("t,d", [(131200, 16384), (2 ** 28 + 40, 8), (40000, 65536)])
 def test_layernorm_past_32_bits(t, d):
     """More than 2^31 elements: the last rows, forward, to E4M3 and backward."""
