@@ -202,6 +202,7 @@ __device__ __forceinline__ void issue_blocks(const GemmParams& p, uint32_t sbase
     const uint32_t self = cluster_ctarank();
     const uint16_t mask_self = static_cast<uint16_t>(1u << self);
     const uint16_t mask_pair = static_cast<uint16_t>(3u << self);
+    grid_dependency_wait();  // (no copy lands earlier: the wait limit does not count the previous grid's time)
     const bool elected = elect_one();
     const uint64_t desc0 = make_sdesc_sw128(sbase, 0, 1024);
     const uint32_t b_at = static_cast<uint32_t>((C::kABytes + h * kHalfBytes) >> 4);

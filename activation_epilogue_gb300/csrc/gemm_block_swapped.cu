@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
     } else if (warp == L::kMmaWarp) {
         if (lane == 0 && !p.debug_stall) {
             constexpr uint32_t idesc = make_idesc_e4m3(kRowsB, NP);
+            grid_dependency_wait();  // (A does not land earlier: the wait limit does not count the previous grid's time)
             int i = 0;
             for (; i < blocks; ++i) {
                 const int s = i % L::kStages, acc = i % kAccs;
