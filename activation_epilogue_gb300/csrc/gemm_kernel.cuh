@@ -675,6 +675,9 @@ __device__ __forceinline__ void run_mma(const GemmParams& p, uint32_t sbase, uin
                                                PAIR ? 2 * kBM : (SWAP && p.swap_m64 ? 64 : kBM), BN);
     const WorkRange w = work_range<PAIR>(p);
     if (PAIR && w.pair_rank != 0) return;
+    // No copy lands before the previous grid has completed: the wait limit does not count its time.  (A single CTA's
+    // copying thread waits for it ahead of the set-up barrier.)
+    if constexpr (PAIR) grid_dependency_wait();
     // commit targets: this (even) CTA, its pair, every CTA whose stages these MMAs read from
     const uint32_t self = PAIR ? cluster_ctarank() : 0u;
     const uint16_t mask_self = static_cast<uint16_t>(1u << self);

@@ -60,6 +60,13 @@ def long_product():
     ((3, 264, 1040), "e4m3", dict(SCALE_BLOCKS=2, VARIANT=2, SPLIT_K=1, B_READY=1)),
     ((300, 264, 1040), "e4m3", dict(SCALE_BLOCKS=1, VARIANT=3)),
     ((300, 264, 1040), "e4m3", dict(SCALE_BLOCKS=2, VARIANT=3, TILE_ORDER=2, GRID=2)),
+    ((300, 264, 1040), "e4m3", dict()),
+    ((300, 264, 1040), "e4m3", dict(TILE_ORDER=2, GRID=2)),
+    ((300, 264, 1040), "bf16", dict(VARIANT=1)),
+    ((300, 264, 4096), "bf16", dict(VARIANT=1, SPLIT_K=4)),
+    ((30, 264, 1040), "bf16", dict(VARIANT=2, B_READY=1)),
+    ((300, 264, 1040), "bf16", dict(VARIANT=3)),
+    ((30, 264, 1040), "bf16", dict(VARIANT=5)),
 ])
 def test_a_predecessor_that_outlasts_the_limit(long_product, shape, dtype, options):
     """The limit is for the kernel's own waits: a healthy predecessor on the stream may take longer than it."""
