@@ -1089,7 +1089,7 @@ gemm_epi_status gemm_epi_plan_set_option(gemm_epi_plan_t p, gemm_epi_option opt,
         p->scale_blocks = static_cast<int>(value);
         break;
     case GEMM_EPI_OPT_DEBUG_STALL:
-        if (value != 0 && value != 1) return GEMM_EPI_ERR_INVALID_ARG;
+        if (value < 0 || value > 2) return GEMM_EPI_ERR_INVALID_ARG;
         p->debug_stall = static_cast<int>(value);
         return GEMM_EPI_OK;
     default:

@@ -29,6 +29,9 @@ constexpr int kGroup = 8;     // K blocks whose scales are staged together
 constexpr int kMaxStages = 12;
 constexpr int kAloneSmem = 200 * 1024;  // with this much a block has an SM to itself
 constexpr int kRedRow = kRowsB + 4;  // (a warp's sums meet different banks)
+// What a block of a cluster that gave up on a wait leaves for the others in the place of its sums: a NaN that no sum is
+// (arithmetic makes 0x7FFFFFFF).  Its flag read by them in a load of its own took 0.2 us a call.
+constexpr uint32_t kGaveUp = 0x7FC0DEADu;
 
 enum : int { kFull = 0, kEmpty = kMaxStages, kAccFull = 2 * kMaxStages, kAccEmpty = kAccFull + kAccs,
              kStall = kAccEmpty + kAccs, kDrain, kBars };
@@ -135,7 +138,8 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
     tcgen05_fence_after_sync();
     const uint32_t tmem = *holder;
     if (threadIdx.x == 0) grid_launch_dependents();
-    if (p.debug_stall) {
+    const bool stall = p.debug_stall == 1 || (p.debug_stall == 2 && rank == split - 1);
+    if (stall) {
         if (threadIdx.x == 0 && !wait_bounded(bar0 + 8 * kStall, 0, abort_flag, p.wait_limit_ns, false))
             record_failure(p.status, abort_flag, kRoleStallTest);
         __syncthreads();
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
     for (int i = 0; i < L::kOwn; ++i) sum[i] = 0.0f;
 
     if (warp == L::kProducerWarp) {
-        if (lane == 0 && !p.debug_stall) {
+        if (lane == 0 && !stall) {
             int issued = 0;
             auto copy = [&](int i, bool b, bool a) {
                 const int s = i % L::kStages;
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
         }
         __syncwarp();
     } else if (warp == L::kMmaWarp) {
-        if (lane == 0 && !p.debug_stall) {
+        if (lane == 0 && !stall) {
             constexpr uint32_t idesc = make_idesc_e4m3(kRowsB, NP);
             grid_dependency_wait();  // (A does not land earlier: the wait limit does not count the previous grid's time)
             int i = 0;
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
             }
         }
         __syncwarp();
-    } else if (warp < L::kSumWarps && !p.debug_stall) {
+    } else if (warp < L::kSumWarps && !stall) {
         const int quarter = warp & 3, part = warp >> 2;
         const long long sb_row = SQUARE ? (p.n - 1) / 128 + 1 : p.n;  // (n + 127 may pass 32 bits)
         const uint32_t staged = sbase + L::kOffScale;
@@ -310,14 +314,17 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
     }
     grid_dependency_wait();
     // The sums as [row of A][column of D] in shared memory, then the epilogue over all threads; with K split,
-    // block `rank` of the cluster takes every split-th set of rows and adds the blocks' sums in order.
+    // block `rank` of the cluster takes every split-th set of rows and adds the blocks' sums in order.  A block that
+    // gave up on a wait has kGaveUp in the place of its sums, and nothing of the tile is stored by any of them.
     float* red = reinterpret_cast<float*>(smem);
+    const bool failed = *abort_flag;
     if (warp < L::kSumWarps) {
 #pragma unroll
         for (int i = 0; i < L::kOwn; ++i) {
             const int c = i / (L::kChunk / 2), e = i % (L::kChunk / 2);  // the load, its value (see load_values)
             const int row = (warp >> 2) * L::kOwn + (c >> 1) * L::kChunk + (e >> 2) * 8 + 2 * (lane & 3) + (e & 1);
-            red[row * kRedRow + (warp & 3) * 32 + (c & 1) * 16 + (e >> 1 & 1) * 8 + (lane >> 2)] = sum[i];
+            red[row * kRedRow + (warp & 3) * 32 + (c & 1) * 16 + (e >> 1 & 1) * 8 + (lane >> 2)] =
+                failed ? __uint_as_float(kGaveUp) : sum[i];
         }
     }
     if (split > 1)
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
         __syncthreads();
     constexpr int kRowsAtOnce = L::kThreads / (kRowsB / 2);
     const int c2 = threadIdx.x % (kRowsB / 2) * 2, col = n0 + c2;
-    const bool there = col < p.n && !*abort_flag;  // (n is even)
+    const bool there = col < p.n && !failed;  // (n is even)
     const bool along_cols = p.bias_layout == 1, has_bias = p.epilog != EPI_NONE;
     float2 bias = make_float2(0.0f, 0.0f);
     if (there && has_bias && along_cols)
@@ -334,6 +341,7 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
     const int rows = min(NP, p.m - m0);
     for (int r = static_cast<int>(threadIdx.x) / (kRowsB / 2) + rank * kRowsAtOnce; r < rows; r += split * kRowsAtOnce) {
         float2 v = make_float2(0.0f, 0.0f);
+        bool store = there;
         if (split == 1) {
             v = *reinterpret_cast<const float2*>(red + r * kRedRow + c2);
         } else {
@@ -341,6 +349,7 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
                 const float2 w = ld_shared_cluster_f32x2(map_shared_rank(sbase + (r * kRedRow + c2) * 4, q));
                 v.x += w.x;
                 v.y += w.y;
+                store = store && __float_as_uint(w.x) != kGaveUp;
             }
         }
         const long long row = m0 + r;
@@ -352,11 +361,11 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
             uint32_t word = there ? ((v.x > 0.0f ? 1u : 0u) | (v.y > 0.0f ? 2u : 0u)) << (2 * (lane & 15)) : 0u;
 #pragma unroll
             for (int o = 8; o >= 1; o >>= 1) word |= __shfl_xor_sync(0xFFFFFFFFu, word, o);
-            if (there && (lane & 15) == 0) static_cast<uint32_t*>(p.aux)[row * p.aux_ld + col / 32] = word;
+            if (store && (lane & 15) == 0) static_cast<uint32_t*>(p.aux)[row * p.aux_ld + col / 32] = word;
         }
         v.x = apply(v.x, p.epilog);
         v.y = apply(v.y, p.epilog);
-        if (!there) continue;
+        if (!store) continue;
         const long long at = row * p.n + col;
         if (p.epilog == EPI_BIAS_RESIDUAL) {
             const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.residual) + at);

@@ -158,7 +158,9 @@ typedef enum {
     GEMM_EPI_OPT_DEBUG_STALL = 6,   /* 1: the next launches wait on a barrier nothing
                                        arrives at, run out the wait limit and report
                                        GEMM_EPI_ERR_DEVICE_TIMEOUT (a test of the timeout
-                                       path; no copy or MMA is issued) */
+                                       path; no copy or MMA is issued); 2: of each cluster
+                                       that splits K with SCALE_BLOCKS, the last block alone
+                                       (elsewhere as 1) */
     GEMM_EPI_OPT_PREFETCH = 7,      /* L2 prefetch distance in 64-deep K blocks, 0..64
                                        (0 = none) */
     GEMM_EPI_OPT_PDL = 8,           /* 1 (default): launch the fused kernel as a

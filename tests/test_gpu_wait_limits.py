@@ -85,3 +85,27 @@ def test_a_predecessor_that_outlasts_the_limit(long_product, shape, dtype, optio
     assert torch.equal(product.D, want)
     product.plan.free()
     assert long.plan.sync_status() == 0
+
+
+@pytest.mark.parametrize("blocks", [1, 2])
+@pytest.mark.parametrize("epilog", ["BIAS", "RELU_AUX_BIAS"])
+@pytest.mark.parametrize("split", [1, 2, 5, 8])
+def test_no_rows_of_a_cluster_that_gave_up(split, epilog, blocks):
+    """K split over a cluster, one block of which gives up on a wait: nothing of its tile is stored, neither by it nor
+    by the others, whose sums lack its part of k."""
+    m, n, k = 40, 1032, 2064
+    p = ref.product_problem(m, n, k, blocks, seed=split, device="cuda")
+    D = torch.full((m, n), 7.0, dtype=BF16, device="cuda")
+    aux = torch.full((m, (n + 31) // 32), -7, dtype=torch.int32, device="cuda") if epilog == "RELU_AUX_BIAS" else None
+    with gemm_epi.Plan(m, n, k, "e4m3", epilog, SCALE_BLOCKS=blocks, VARIANT=2, SPLIT_K=split, WAIT_LIMIT_US=2000,
+                       DEBUG_STALL=2) as plan:
+        for _ in range(2):
+            plan.execute(p["A"], p["B"], p["bias"], D, aux=aux, scales=(p["sa"], p["sb"]))
+            assert plan.sync_status() == 8
+            assert (D == 7).all() and (aux is None or (aux == -7).all())
+        plan.set_option("DEBUG_STALL", 0)
+        plan.set_option("WAIT_LIMIT_US", 0)
+        plan.execute(p["A"], p["B"], p["bias"], D, aux=aux, scales=(p["sa"], p["sb"]))
+        assert plan.sync_status() == 0
+    want, _, error = ref.product(p, blocks, epilog)
+    ref.check(D, want, error)
