@@ -584,7 +584,7 @@ __device__ __forceinline__ void sum_blocks(const GemmParams& p, uint32_t sbase, 
                             if constexpr (SQUARE)
                                 fma2(s[0], s[1], x, f[0]);
                             else
-                                fma2(s[0], s[1], mul2(x, g[e / 4]), f[2 * h + (e >> 1 & 1)]);
+                                fma2(s[0], s[1], x, mul2(g[e / 4], f[2 * h + (e >> 1 & 1)]));
                         }
                     }
                     if (c < 3) load(from[q & 1], c + 1);

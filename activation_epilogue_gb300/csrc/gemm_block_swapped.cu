@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(Layout<NP, SQUARE>::kThreads, Layout<NP, SQUAR
                         if constexpr (SQUARE)
                             fma2(s[0], s[1], x, f[q / 4]);
                         else
-                            fma2(s[0], s[1], mul2(x, f[q / 4]), fb[2 * (c & 1) + (q >> 1 & 1)]);
+                            fma2(s[0], s[1], x, mul2(f[q / 4], fb[2 * (c & 1) + (q >> 1 & 1)]));
                     }
                 }
             }

@@ -227,7 +227,8 @@ typedef enum {
  * of n and j' = j (ROWS; 16-byte aligned): what gemm_epi_e4m3_quantize and gemm_epi_layernorm_e4m3
  * write.  Each block's sum is an fp32 sum of its own; the blocks' sums times their scales are added in
  * fp32 in the order of k (where K is split, in order within a slice, then the slices'), the same in every
- * call.  The product of two scales is formed in fp32 and has to be finite in it.  Epilogs as for the
+ * call.  The product of two scales is formed in fp32, before it meets the block's sum: it has to be finite,
+ * and one below 2^-126 loses bits (below 2^-149 it is 0).  Epilogs as for the
  * other E4M3 plans, both bias layouts; D may be the residual itself, any other overlap of D or aux with
  * an operand is ERR_INVALID_ARG.  VARIANT is 0 (automatic), 3 (CTA pairs, TILE_N 256) or 2 (few rows of
  * A: TILE_N 16, 32, 64 or 128 rows of D; SPLIT_K slices, 1..8, over a cluster, or 0: as many as fit;

@@ -56,6 +56,24 @@ def test_activations_of_every_size(epilog, variant, blocks):
         assert torch.equal(got, torch.where(b > 0, b, 0.0))
 
 
+@pytest.mark.parametrize("variant", [2, 3])
+@pytest.mark.parametrize("blocks", [1, 2])
+@pytest.mark.parametrize("a,b", [(1e-27, 1e37), (1e37, 1e-27), (1e-3, 1e-27), (1e-27, 1e-3)])
+def test_scales_of_opposite_extremes(a, b, blocks, variant):
+    """The product of the two scales is formed first, whichever kernel runs: it has to be a normal number, a block's
+    sum times either scale need not."""
+    p = ref.product_problem(40, 264, 1040, blocks, seed=6, device="cuda")
+    p["sa"] *= a
+    p["sb"] *= b
+    D = torch.empty(40, 264, dtype=BF16, device="cuda")
+    with gemm_epi.Plan(40, 264, 1040, "e4m3", "NONE", SCALE_BLOCKS=blocks, VARIANT=variant) as plan:
+        plan.execute(p["A"], p["B"], None, D, scales=(p["sa"], p["sb"]))
+        assert plan.sync_status() == 0
+    want, _, error = ref.product(p, blocks, "NONE")
+    assert want.abs().max() < 3e38
+    ref.check(D, want, error)
+
+
 @pytest.mark.parametrize("blocks", [1, 2])
 @pytest.mark.parametrize("tile", [16, 32, 64, 128])
 @pytest.mark.parametrize("split", range(1, 9))
