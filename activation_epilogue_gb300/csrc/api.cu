@@ -305,24 +305,34 @@ gemm_epi_status ensure_split_ws(gemm_epi_plan_s* p)
 }
 
 // E4M3 with scales for blocks of 128 of k: CTA pairs on 256 x 256 tiles, or, for few rows of A, tiles of
-// 128 columns by up to 128 rows with K split over a cluster.  The latter up to 64 rows, where it streams B, and
-// as long as its tiles of 128 x 128 leave two SMs or more for each (a scale for each row of B, which costs the
-// pairs more: one), twice that below 16 blocks of k.  Measured (n x k, few rows / pairs, GELU, us; in brackets
-// with a scale for each row of B): 64 rows of 16384 x 8192 27.5 / 31.5 (29.1 / 44.1), 128 rows of it (128 tiles)
-// 36.5 / 33.4 (38.1 / 45.2); 4096 x 4096 with 256 rows (64 tiles) 15.3 / 18.2, 512 (128) 20.4 / 18.3 (20.9 / 24.6),
-// 768 (192) 40.1 / 19.0 (40.9 / 25.0); 8192 x 8192 with 128 (64) 21.7 / 30.7, 256 (128) 32.5 / 30.3 (34.7 / 42.6),
-// 384 (192) 63.4 / 31.8 (67.7 / 43.4); 4096 x 2048 with 128 (32) 8.7 / 11.9, 256 (64) 12.2 / 11.8, 512 (128)
-// 14.7 / 12.2 (14.8 / 15.8); 4096 x 1024 with 64 (32) 6.5 / 8.5, 128 (32) 7.9 / 8.7, 256 (64) 10.7 / 8.7
-// (10.7 / 10.9), 512 (128) 11.7 / 9.0 (11.8 / 11.2); 4096 x 512 with 64 (32) 6.9 / 7.1, 128 (32) 9.4 / 7.3.
+// 128 columns by up to 128 rows with K split over a cluster.  The latter up to 64 rows, where it streams B; above
+// that with 8 blocks of k or more (a scale for each row of B, which costs the pairs more: 6), as long as its tiles of
+// 128 x 128 leave two SMs or more for each (one), twice that below 20 (16) blocks of k.  Measured (n x k, few rows /
+// pairs, GELU, us; in brackets with a scale for each row of B):
+//   up to 64 rows: 64 of 16384 x 8192 27.5 / 31.5 (29.1 / 44.1), of 4096 x 1024 6.5 / 8.5, of 4096 x 512 6.9 / 7.1
+//   (7.0 / 8.8), of 4096 x 256 6.2 / 6.4 (6.4 / 7.7);
+//   few blocks of k: 128 rows (32 tiles) of 4096 x 256 9.1 / 6.6 (9.2 / 7.7), x 512 9.4 / 7.3 (9.5 / 8.8), x 640
+//   9.8 / 7.8 (9.9 / 9.6), x 768 8.9 / 8.1 (8.9 / 10.1), x 896 9.2 / 8.4 (9.2 / 10.5), x 1024 8.0 / 8.8 (8.1 / 11.1);
+//   4096 x 1024 with 256 rows (64) 10.8 / 8.7 (10.9 / 11.0), 512 (128) 11.8 / 9.2 (11.9 / 11.4); 4096 x 2048 with 128
+//   (32) 8.8 / 12.0, 256 (64) 12.4 / 11.8, 512 (128) 14.9 / 12.3 (15.0 / 16.1); 4096 x 2560 with 256 13.5 / 13.6, x
+//   3584 14.8 / 16.7, x 4096 15.3 / 18.2, with 512 20.4 / 18.3 (20.9 / 24.6), 768 (192) 40.1 / 19.0 (40.9 / 25.0);
+//   8192 x 8192 with 128 (64) 21.7 / 30.7, 256 (128) 32.5 / 30.3 (34.7 / 42.6), 384 (192) 63.4 / 31.8 (67.7 / 43.4);
+//   16384 x 8192 with 128 (128) 36.5 / 33.4 (38.1 / 45.2).
+bool few_rows_of_blocks(const gemm_epi_plan_s* p, bool square)
+{
+    if (p->m <= 64) return true;
+    if (p->k_blocks < (square ? 8 : 6)) return false;
+    const int64_t tiles128 = (p->n + 127) / 128 * ((p->m + 127) / 128);
+    return tiles128 * (square ? 2 : 1) * (p->k_blocks < (square ? 20 : 16) ? 2 : 1) <= p->sm_count;
+}
+
 gemm_epi_status configure_blocks(gemm_epi_plan_s* p)
 {
     const bool square = p->scale_blocks == GEMM_EPI_SCALE_BLOCKS_SQUARE;
     p->k_blocks = static_cast<int>((p->k + 127) / 128);
     const int64_t column_tiles = (p->n + 127) / 128;
     int v = p->opt_variant;
-    const int64_t tiles128 = column_tiles * ((p->m + 127) / 128);
-    const int sms_each = (square ? 2 : 1) * (p->k_blocks < 16 ? 2 : 1);
-    if (v == 0) v = p->m <= 64 || tiles128 * sms_each <= p->sm_count ? 2 : 3;
+    if (v == 0) v = few_rows_of_blocks(p, square) ? 2 : 3;
     if (v != 2 && v != 3) return GEMM_EPI_ERR_INVALID_ARG;
     if (v == 3) {
         if (p->opt_bn != 0 && p->opt_bn != 256) return GEMM_EPI_ERR_INVALID_ARG;

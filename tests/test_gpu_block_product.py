@@ -74,3 +74,13 @@ def test_shapes(m, n, k, opts, blocks):
 def test_epilogs(m, n, k, opts, epilog, layout, blocks):
     p = ref.product_problem(m, n, k, blocks, seed=len(epilog) + m, device="cuda")
     _check(p, blocks, epilog, layout, **opts)
+
+
+@pytest.mark.parametrize("m,n,k,few", [  # for either kind of scales: whether the kernel for few rows of A is quicker
+    (64, 4096, 512, (1, 1)), (64, 16384, 128, (1, 1)), (128, 4096, 512, (0, 0)), (512, 1024, 640, (0, 0)),
+    (128, 4096, 768, (0, 1)), (128, 4096, 1024, (1, 1)), (256, 4096, 1024, (0, 1)), (256, 4096, 2048, (0, 1)),
+    (256, 4096, 4096, (1, 1)), (512, 4096, 4096, (0, 1)), (768, 4096, 4096, (0, 0))])
+def test_which_kernel(m, n, k, few):
+    for blocks in (1, 2):
+        with gemm_epi.Plan(m, n, k, "e4m3", "GELU_BIAS", SCALE_BLOCKS=blocks) as plan:
+            assert ("variant=block-swapped" in plan.describe()) == bool(few[blocks - 1]), plan.describe()
