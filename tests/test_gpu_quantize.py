@@ -97,6 +97,35 @@ def test_nan_and_infinity(dtype, block):
     assert not Qt[:, 300:].view(torch.uint8).any()  # also where the scale is NaN
 
 
+@pytest.mark.parametrize("block", ["1X128", "128X128"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,cols", [(300, 272), (128, 384), (1, 144), (257, 16)])
+def test_which_blocks_a_nan_marks(rows, cols, dtype, block):
+    """The blocks that hold a NaN, and no others, have a NaN scale; those that hold an infinity and no NaN an infinite
+    one (corners of blocks and of the matrix among the places)."""
+    x = _matrix(rows, cols, dtype)
+    at = {(0, 0), (0, cols - 1), (rows - 1, 0), (rows - 1, cols - 1), (min(127, rows - 1), min(128, cols - 1)),
+          (min(128, rows - 1), min(127, cols - 1)), (rows // 2, cols // 2)}
+    for i, (r, c) in enumerate(sorted(at)):
+        x[r, c] = float(("nan", "inf", "-inf")[i % 3])
+    Q, s, Qt, st = _quantize(x, block)
+    for scale, y in ((s, x), (st, x.t())):
+        r, c = y.shape
+        high = 128 if block == "128X128" else 1
+
+        def blocks_with(mark):  # every element's block, by plain indexing
+            out = torch.zeros(r, c, dtype=torch.bool, device="cuda")
+            for i, j in mark.nonzero().tolist():
+                i0, j0 = i // high * high, j // 128 * 128
+                out[i0:i0 + high, j0:j0 + 128] = True
+            return out
+
+        nan, inf = blocks_with(y.isnan()), blocks_with(y.isinf())
+        wide = ref.spread(scale, block, r, c)
+        assert torch.equal(wide.isnan(), nan)
+        assert torch.equal(wide.isinf(), inf & ~nan)
+
+
 def test_rows_past_32_bits():
     """A matrix of more than 2^31 values: its last rows."""
     rows, cols = 2 ** 31 // 16384 + 130, 16384
