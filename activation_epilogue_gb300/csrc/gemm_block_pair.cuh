@@ -20,12 +20,14 @@
 //   * SQUARE: a warp's columns share one scale, a thread (a row) has one factor a block.  Otherwise
 //     every column has its own, and a thread's values are loaded as four rows of 32 columns, so that
 //     32 scales a block come from shared memory for them and not 128 (whose 1024 cycles a block
-//     would bound it); each value then takes a product before its addition, 512 cycles of the fp32
-//     pipes.  (Without the reads of the columns' scales a block would take 90 cycles less, without the
-//     products 15; wider reads, scales by asynchronous copies and other orders of the products: 1 %.)
+//     would bound it); each value then takes the product of its two scales (formed first: it alone has to be
+//     finite) before its addition, 512 cycles of the fp32 pipes.  (Without the reads of the columns' scales a block
+//     would take 90 cycles less, without the products 15; wider reads, scales by asynchronous copies and other orders
+//     of the products: 1 to 2 %.  The loads of sixteen lanes are not what costs: 84.0 us for 84.4 with SQUARE's, which
+//     itself takes 73.6 for 64.4 with these.)
 //   * One warp brings the scales of all blocks into a ring in shared memory, ahead of the sums.
-// 16384 x 8192 x 8192: 717 us, 3.07 PFLOP/s, in a short run, 858 where the power limit holds; 4096 x 8192 x
-// 2064 63.8 us, 2.17 PFLOP/s, 83.0 with a scale for each row of B.
+// 16384 x 8192 x 8192: 854 us, 2.57 PFLOP/s, where the power limit holds (717 in a short burst); 4096 x 8192 x
+// 2064 64.4 us, 2.15 PFLOP/s, 84.4 with a scale for each row of B.
 #pragma once
 
 #include "block_sums.cuh"

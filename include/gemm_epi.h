@@ -228,7 +228,8 @@ typedef enum {
  * write.  Each block's sum is an fp32 sum of its own; the blocks' sums times their scales are added in
  * fp32 in the order of k (where K is split, in order within a slice, then the slices'), the same in every
  * call.  The product of two scales is formed in fp32, before it meets the block's sum: it has to be finite,
- * and one below 2^-126 loses bits (below 2^-149 it is 0).  Epilogs as for the
+ * and one below 2^-126 loses bits (below 2^-149 it is 0).  A NaN or infinite scale reaches the rows or columns
+ * that it belongs to; RELU of a NaN is 0, with a 0 in the mask, as in the other plans.  Epilogs as for the
  * other E4M3 plans, both bias layouts; D may be the residual itself, any other overlap of D or aux with
  * an operand is ERR_INVALID_ARG.  VARIANT is 0 (automatic), 3 (CTA pairs, TILE_N 256) or 2 (few rows of
  * A: TILE_N 16, 32, 64 or 128 rows of D; SPLIT_K slices, 1..8, over a cluster, or 0: as many as fit;
@@ -459,7 +460,7 @@ gemm_epi_status gemm_epi_layernorm_forward(int64_t t, int64_t d, gemm_epi_dtype 
  * GEMM_EPI_OPT_SCALE_BLOCKS.  scale: ceil(d / 128) rows of t fp32, 4-byte aligned, written:
  * scale[b][i] = max |Y_ij| / 448 over columns j of block b; Q_ij = Y_ij * (1 / scale), Y not rounded to
  * 16 bits, the reciprocal and the rounding as in gemm_epi_e4m3_quantize.  Q: t x d bytes, 16-byte
- * aligned, overlapping nothing else. */
+ * aligned, overlapping nothing else.  (A plan takes it with d as its k: a multiple of 16.) */
 gemm_epi_status gemm_epi_layernorm_e4m3(int64_t t, int64_t d, gemm_epi_dtype dtype, const void* X,
                                         const void* residual, const void* gamma, const void* beta,
                                         float eps, void* H, void* Q, float* scale, float* stats,
@@ -503,9 +504,9 @@ int64_t gemm_epi_layernorm_workspace(int64_t t, int64_t d);
  * in 128 x 128 blocks; for dX = dD W^T: A from dD's rows, B from W's Q; for dW = X^T dD: A from X's Qt and
  * B from dD's Qt in 1 x 128 blocks (SCALE_BLOCKS_ROWS).  A block without a value of 2^-100 or more gets
  * scale 0 and zeros; a NaN gives its block a NaN scale and NaN codes, an infinity an infinite scale, zeros
- * and NaN for the infinite values.  X, Q, Qt 16-byte aligned, scale and scale_t 4-byte; no output overlaps
- * another buffer.  rows == 0 launches nothing.  One pass over X, whatever is written; asynchronous on
- * `stream` as above. */
+ * and NaN for the infinite values.  X, Q, Qt 16-byte aligned, scale and scale_t 4-byte (16 where they
+ * become the scale_b of a plan with SCALE_BLOCKS_ROWS); no output overlaps another buffer.  rows == 0
+ * launches nothing.  One pass over X, whatever is written; asynchronous on `stream` as above. */
 typedef enum {
     GEMM_EPI_BLOCK_1X128 = 0,
     GEMM_EPI_BLOCK_128X128 = 1
