@@ -44,7 +44,9 @@
  *     or bias; D may be the residual buffer itself (an in-place residual add).
  *   - All execute calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream) and return launch-time errors only; a device-side wait that ran out
- *     its time limit is reported by gemm_epi_sync_status.  The fused kernel is launched as
+ *     its time limit is reported by gemm_epi_sync_status (the outputs of such a call are not
+ *     to be used: a part of them may be unwritten, or lack a part of k).  The limit counts the
+ *     kernel's own waits, not the stream's previous work.  The fused kernel is launched as
  *     a programmatic dependent of the stream's previous work: it may start its set-up
  *     early, but reads and writes device memory only after that work has completed (except
  *     B under GEMM_EPI_OPT_B_READY, and prefetches of B into L2, which change no result).
